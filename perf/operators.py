@@ -206,9 +206,9 @@ def prepare(case, seed):
     if own:
         from sparsified_gradient_compression_amd import dgc
         if case["op"].startswith("linear"):
-            state["workspace"] = dgc.linear_workspace(m, case["n"], case["k"], t, backward=case["op"] != "linear")
+            state["workspace"] = dgc.linear_workspace(m, case["n"], case["k"], backward=case["op"] != "linear")
         else:
-            state["workspace"] = dgc.gated_ffn_workspace(m, case["d"], case["f"], t, backward=case["op"] != "gated_ffn")
+            state["workspace"] = dgc.gated_ffn_workspace(m, case["d"], case["f"], backward=case["op"] != "gated_ffn")
     return state
 
 
