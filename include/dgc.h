@@ -120,6 +120,22 @@ extern "C" {
 #define DGC_TIMER_DECODE 3    /* all of dgc_decode_accumulate, dgc_decode_sum
                                  or dgc_shared_sum */
 
+/* Element types of the layer and gradient-set operators. */
+#define DGC_BF16 1
+#define DGC_FP16 2
+#define DGC_FP32 3
+
+/* Activations of the layer operators. */
+#define DGC_ACT_NONE 0
+#define DGC_ACT_RELU 1      /* max(z, 0) */
+#define DGC_ACT_SILU 2      /* z / (1 + exp(-z)) */
+#define DGC_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
+#define DGC_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+
+/* Norms of the gradient-set operators. */
+#define DGC_NORM_L2 0  /* sqrt of the sum of squares, added in binary64 */
+#define DGC_NORM_MAX 1 /* the largest magnitude */
+
 typedef struct dgc_state dgc_state;
 
 /*
@@ -539,6 +555,159 @@ int dgc_set_option(dgc_state* st, int32_t option, int64_t value);
  */
 int dgc_get_kernel_time(dgc_state* st, int32_t timer, double* total_ms,
                         int64_t* count);
+
+/*
+ * Layer operators: what makes the gradients
+ * -----------------------------------------
+ * Matrices are rows of `ld` elements with contiguous columns (ld >= columns);
+ * neither rows nor pointers need more alignment than their element's, but
+ * rows on 16-byte boundaries are read and written faster.  Elements are
+ * DGC_BF16 or DGC_FP16 (`type`); sums are held in binary32 and rounded once.
+ * Sizes may be 0: an empty sum is 0.  Outputs must not overlap inputs, except
+ * that `y` may be `residual` itself, with the same ld.  Each call needs the
+ * workspace its *_workspace_bytes gives for the sizes alone (256-byte
+ * aligned, its contents free between calls; NULL where that is 0), and may
+ * not share it with a call on another stream.
+ * All return DGC_OK, DGC_EINVAL, DGC_ECAPACITY (workspace too small) or
+ * DGC_EHIP.
+ */
+
+/* y[m][n] = act(z) + residual, z = x[m][k] w[n][k]^T + bias[n].
+ * bias, residual and pre may be NULL; pre[m][n] receives z for the backward
+ * pass.  The activation sees z before that rounding. */
+typedef struct dgc_linear_args {
+    int64_t type, act, m, n, k;
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;
+    const void* bias;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+    void* pre;
+    int64_t ldpre;
+} dgc_linear_args;
+
+/* With dz = dy * act'(pre): dx[m][k] = dz w, dw[n][k] = dz^T x, dbias[n] =
+ * the column sums of dz.  Each of dx, dw, dbias may be NULL.  dw and dbias
+ * are of grad_type: `type`, or DGC_FP32 (a learner's flat gradient).  pre is
+ * not read for DGC_ACT_NONE; for other activations dz is rounded to `type`
+ * before the products, not before the column sums. */
+typedef struct dgc_linear_backward_args {
+    int64_t type, grad_type, act, m, n, k;
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;
+    const void* pre;
+    int64_t ldpre;
+    void* dx;
+    int64_t lddx;
+    void* dw;
+    int64_t lddw;
+    void* dbias;
+} dgc_linear_backward_args;
+
+/* h[m][f] = act(a) * b, a = x[m][d] w_gate[f][d]^T, b = x w_up[f][d]^T.
+ * gate and up (each may be NULL) receive a and b for the backward pass. */
+typedef struct dgc_gated_ffn_args {
+    int64_t type, act, m, d, f;
+    const void* x;
+    int64_t ldx;
+    const void* w_gate;
+    int64_t ldw_gate;
+    const void* w_up;
+    int64_t ldw_up;
+    void* h;
+    int64_t ldh;
+    void* gate;
+    int64_t ldgate;
+    void* up;
+    int64_t ldup;
+} dgc_gated_ffn_args;
+
+/* With da = dh * up * act'(gate) and db = dh * act(gate), both rounded to
+ * `type`: dx[m][d] = da w_gate + db w_up, dw_gate[f][d] = da^T x,
+ * dw_up = db^T x.  dx may be NULL, and dw_gate and dw_up together. */
+typedef struct dgc_gated_ffn_backward_args {
+    int64_t type, grad_type, act, m, d, f;
+    const void* dh;
+    int64_t lddh;
+    const void* x;
+    int64_t ldx;
+    const void* w_gate;
+    int64_t ldw_gate;
+    const void* w_up;
+    int64_t ldw_up;
+    const void* gate;
+    int64_t ldgate;
+    const void* up;
+    int64_t ldup;
+    void* dx;
+    int64_t lddx;
+    void* dw_gate;
+    int64_t lddw_gate;
+    void* dw_up;
+    int64_t lddw_up;
+} dgc_gated_ffn_backward_args;
+
+int dgc_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t backward, size_t* bytes);
+int dgc_linear(const dgc_linear_args* args, void* workspace, size_t workspace_bytes,
+               hipStream_t stream);
+int dgc_linear_backward(const dgc_linear_backward_args* args, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+int dgc_gated_ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int32_t backward,
+                                  size_t* bytes);
+int dgc_gated_ffn(const dgc_gated_ffn_args* args, void* workspace, size_t workspace_bytes,
+                  hipStream_t stream);
+int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* args, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gradient sets: from a model's tensors to a learner
+ * --------------------------------------------------
+ * A set is n_tensors gradients of given element counts and types
+ * (DGC_BF16, DGC_FP16 or DGC_FP32), each contiguous.  `grads` (and `outs`)
+ * are host arrays of device pointers, read during the call.
+ *   norm   = unscale * (sqrt(sum of all squares), or the largest magnitude),
+ *            in binary64; a NaN anywhere makes it NaN
+ *   scale  = (float)(unscale * (clip / norm if clip > 0 and norm > clip, else 1))
+ * unscale (> 0, finite) undoes a loss scale or an accumulation count first.
+ * Results do not depend on timing: no atomics.  Calls on one set must not run
+ * concurrently on two streams.  Nothing is kept between calls.
+ */
+typedef struct dgc_gradset dgc_gradset;
+
+int dgc_gradset_bytes(int32_t n_tensors, const int64_t* sizes, const int32_t* types,
+                      size_t* bytes);
+
+/* Uploads the layout into the workspace (256-byte aligned) and waits for it. */
+int dgc_gradset_init(dgc_gradset** set, int32_t n_tensors, const int64_t* sizes,
+                     const int32_t* types, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+
+/* The norm alone, into *out_norm (device). */
+int dgc_gradset_norm(const dgc_gradset* set, const void* const* grads, int32_t norm,
+                     double unscale, double* out_norm, hipStream_t stream);
+
+/* outs[t] = grads[t] * scale in tensor t's own type, in binary32 rounded
+ * once; outs[t] may be grads[t].  out_norm and out_scale (device) may be NULL. */
+int dgc_gradset_clip(const dgc_gradset* set, const void* const* grads, void* const* outs,
+                     double clip, int32_t norm, double unscale, double* out_norm,
+                     float* out_scale, hipStream_t stream);
+
+/* The same in binary32 into flat, tensors end to end: the layout of
+ * dgc_compress, to be called there with clip 0. */
+int dgc_gradset_pack(const dgc_gradset* set, const void* const* grads, float* flat, double clip,
+                     int32_t norm, double unscale, double* out_norm, float* out_scale,
+                     hipStream_t stream);
+
+/* Free the host-side set.  Device memory stays the caller's. */
+void dgc_gradset_destroy(dgc_gradset* set);
 
 /* Free the host-side state.  Device memory stays the caller's. */
 void dgc_destroy_state(dgc_state* st);

@@ -7,6 +7,7 @@ FP32 instructions disabled, so every binary32 operation rounds once, as the
 method's arithmetic is defined.
 """
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -17,9 +18,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libdgc.so")
-SOURCES = [os.path.join(CSRC, "dgc_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in
+           ("dgc_api.hip", "dgc_gradset.hip", "dgc_layers.hip", "layers_bf16.hip", "layers_fp16.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
-                     ("dgc_device.hpp", "kernel_fused.hpp", "kernels_binlocal.hpp", "kernels_sampled.hpp",
+                     ("layers.hpp", "layers_elem.hpp", "layers_launch.hpp", "layers_tile.hpp",
+                      "dgc_device.hpp", "kernel_fused.hpp", "kernels_binlocal.hpp", "kernels_sampled.hpp",
                       "kernels_compress.hpp", "kernels_codec.hpp", "kernels_shared.hpp", "kernels_tensor.hpp")] + [os.path.join(ROOT, "include", "dgc.h")]
 
 ARCH = os.environ.get("DGC_OFFLOAD_ARCH", "gfx950")
@@ -48,11 +51,21 @@ def build(verbose=True):
     """Compile libdgc.so (always recompiles)."""
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + SOURCES + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+
+    objects = [os.path.join(LIBDIR, os.path.basename(s) + ".o") for s in SOURCES]
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+        list(pool.map(lambda so: run([hipcc()] + compile_flags + ["-c", so[0], "-o", so[1]]),
+                      zip(SOURCES, objects)))
+    run([hipcc(), f"--offload-arch={ARCH}", "-shared"] + objects + ["-o", tmp])
     os.replace(tmp, LIB)
+    for o in objects:
+        os.remove(o)
     return LIB
 
 
