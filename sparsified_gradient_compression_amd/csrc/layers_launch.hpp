@@ -2,6 +2,7 @@
 // element type's source file instantiates it.
 #pragma once
 
+#include "layers_big.hpp"
 #include "layers_elem.hpp"
 #include "layers_tile.hpp"
 
@@ -11,11 +12,30 @@ namespace layers {
 #define DGC_LAYERS_CHECK() \
     if (hipGetLastError() != hipSuccess) return DGC_EHIP
 
+// Whether a matrix's rows lie on 16 bytes and end there too, with offsets
+// within 128 rows (64 of k) inside 2^31 bytes: what loads from memory
+// straight to LDS need.
+inline bool direct(const Mat& a, int64_t cols) {
+    return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.ld % 8 == 0 && cols % 8 == 0 &&
+           a.ld <= (int64_t(1) << 22);
+}
+
+inline bool direct(const Product& p) {
+    const int64_t ca = p.form == kDw ? p.m : p.k, cb = p.form == kRows || p.form == kPair ? p.k : p.n;
+    const bool two_a = p.form != kRows && p.form != kPair && p.parts == 2;
+    const bool two_b = p.form == kPair || (p.form == kDx && p.parts == 2);
+    if (!direct(p.a[0], ca) || !direct(p.b[0], cb)) return false;
+    if (two_a && (!direct(p.a[1], ca) || p.a[1].ld != p.a[0].ld)) return false;
+    return !two_b || (direct(p.b[1], cb) && p.b[1].ld == p.b[0].ld);
+}
+
 template <class T, int FORM>
 int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
     const int64_t blocks = a.mt * a.nt * (FORM == kDw ? a.parts : 1) * c.splits;
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
-    if (c.tile == 0)
+    if (c.tile == 2)
+        k_big<T, FORM><<<dim3(unsigned(blocks)), 512, 0, s>>>(a);
+    else if (c.tile == 0)
         k_tile<T, FORM, 64, 64, 2, 2><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
     else
         k_tile<T, FORM, 128, 128, 2, 2><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
@@ -26,8 +46,15 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
 template <class T>
 int Launch<T>::product(const Product& p, void* ws, hipStream_t s) {
     if (p.m == 0 || p.n == 0) return DGC_OK;
-    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts);
-    const int64_t side = c.tile ? 128 : 64;
+    Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts);
+    const int64_t big = cdiv64(p.m, 256) * cdiv64(p.form == kPair ? 2 * p.n : p.n, 256) *
+                        (p.form == kDw ? p.parts : 1);
+    if (big >= 128 && direct(p)) {
+        c.tile = 2;
+        c.splits = 1;
+        c.per = cdiv64(p.k, 64) * (p.form == kDx ? p.parts : 1);
+    }
+    const int64_t side = c.tile == 2 ? 256 : c.tile ? 128 : 64;
     TileArgs a{};
     for (int i = 0; i < 2; ++i) {
         a.a[i] = p.a[i].p;

@@ -307,6 +307,58 @@ struct Frag {
     }
 };
 
+// A wave's outputs leave through its own LDS (MT * 16 rows of NTW * 16
+// columns in binary32, NTW = 2 or 4): what finishes an element is then one
+// short loop whose lanes hold 8 consecutive columns each, instead of the
+// whole of it unrolled over every register.
+//   columns of the first and the second half of the wave's start at n0, n1
+//   (kPair: of the first and the second product, the same ones)
+template <class T, int FORM, int MT, int NTW>
+__device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, int64_t m0,
+                                         int64_t n0, int64_t n1, int lane, float* lds) {
+    constexpr bool PAIR = FORM == kPair;
+    constexpr int W = NTW * 16;                     // columns in LDS
+    constexpr int kLanes = PAIR ? W / 16 : W / 8;   // lanes per row
+    constexpr int kRows = 64 / kLanes;
+    const int c = lane % kLanes;
+    const int64_t n = c * 8 < W / 2 ? n0 + c * 8 : n1 + c * 8 - W / 2;
+#pragma unroll 1
+    for (int r = lane / kLanes; r < MT * 16; r += kRows) {
+        const int64_t m = m0 + r;
+        if (m >= A.M) break;
+        float v[8], v2[8];
+        const int key = (r & (W / 8 - 1)) << 1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            *reinterpret_cast<f32x4*>(v + 4 * q) =
+                *reinterpret_cast<const f32x4*>(lds + r * W + ((2 * c + q) ^ key) * 4);
+            if (PAIR)
+                *reinterpret_cast<f32x4*>(v2 + 4 * q) = *reinterpret_cast<const f32x4*>(
+                    lds + r * W + ((2 * c + q + W / 8) ^ key) * 4);
+        }
+        const int valid = A.N - n < 8 ? int(A.N - n) : 8;
+        if (valid <= 0) continue;
+        if (A.part) {
+            const int planes = PAIR ? 2 : A.outs;
+            float* o = A.part + (((int64_t(split) * planes + z) * A.M + m) * A.N + n);
+            store_wide<8>(o, valid, v);
+            if (PAIR) store_wide<8>(o + A.M * A.N, valid, v2);
+        } else {
+            finish_row<T, PAIR, 8>(A.fin, z, m, n, A.N, v, v2);
+        }
+    }
+}
+
+// Matrix tile j (of NT that share their columns by n_row<NT>, or TR: that lie
+// side by side) of rows 16 mt, at column `col`, into that LDS.
+template <int NTW, int NT, bool TR>
+__device__ __forceinline__ void put_tile(float* lds, int mt, int col, int j, int lane, f32x4 v) {
+    constexpr int W = NTW * 16;
+    const int r = mt * 16 + (lane & 15), g = lane >> 4;
+    const int c4 = col / 4 + (TR ? j * 4 + g : g * NT + j);
+    *reinterpret_cast<f32x4*>(lds + r * W + (c4 ^ ((r & (W / 8 - 1)) << 1)) * 4) = v;
+}
+
 // BM x BN outputs per workgroup of WM x WN waves.  LDS holds two tiles of
 // each side; the next one travels through registers while this one is used.
 template <class T, int FORM, int BM, int BN, int WM, int WN>
@@ -317,8 +369,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile(TileArgs A) {
     constexpr int NT = PAIR ? NTW / 2 : NTW;              // ... of one product
     constexpr int kPiecesA = BM * 8 / kThreads, kPiecesB = BN * 8 / kThreads;
     typedef typename Arith<T>::v8 v8;
-    __shared__ __align__(16) T sa[2][BM * kStep];
-    __shared__ __align__(16) T sb[2][BN * kStep];
+    __shared__ __align__(16) T smem[2 * (BM + BN) * kStep];
+    T (&sa)[2][BM * kStep] = *reinterpret_cast<T (*)[2][BM * kStep]>(smem);
+    T (&sb)[2][BN * kStep] = *reinterpret_cast<T (*)[2][BN * kStep]>(smem + 2 * BM * kStep);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
 
@@ -415,34 +468,17 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile(TileArgs A) {
         if (t + 1 < last) place_lds(buf ^ 1);
     }
 
-    // lane (g, i) holds row m = i of a tile and columns 4g..4g+3 of its 16
-    const int i = lane & 15, g = lane >> 4;
+    __syncthreads();
+    constexpr int kOwn = MT * NTW * 256;  // outputs of a wave
+    static_assert(WM * WN * kOwn * 4 <= int(sizeof(sa) + sizeof(sb)), "outputs fit the tiles' LDS");
+    float* out = reinterpret_cast<float*>(smem) + wave * kOwn;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int64_t m = m0 + (wm * MT + mt) * 16 + i;
-        if (m >= A.M) continue;
-        constexpr int C = BTR ? 4 : 4 * NT;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int q = 0; q < 4 * NT / C; ++q) {
-            const int64_t n = n0 + wn * NT * 16 + (BTR ? q * 16 + g * 4 : g * C);
-            float v[C], v2[C];
-#pragma unroll
-            for (int e = 0; e < C; ++e) {
-                v[e] = acc[mt][q + e / 4][e % 4];
-                v2[e] = PAIR ? acc[mt][(PAIR ? NT : 0) + q + e / 4][e % 4] : 0.0f;
-            }
-            if (A.part) {
-                const int valid = A.N - n < C ? int(A.N - n) : C;
-                if (valid <= 0) continue;
-                const int planes = PAIR ? 2 : A.outs;
-                float* o = A.part + (((int64_t(split) * planes + z) * A.M + m) * A.N + n);
-                store_wide<C>(o, valid, v);
-                if (PAIR) store_wide<C>(o + A.M * A.N, valid, v2);
-            } else {
-                finish_row<T, PAIR, C>(A.fin, z, m, n, A.N, v, v2);
-            }
-        }
-    }
+        for (int j = 0; j < NTW; ++j)
+            put_tile<NTW, NT, BTR>(out, mt, j / NT * NT * 16, j % NT, lane, acc[mt][j]);
+    const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
+    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out);
 }
 
 // The sums of all splits, added in their order, then finished.  One thread

@@ -170,6 +170,22 @@ def test_gated_ffn_backward_sizes(m, n, k):
         run_ffn_backward(m, k, n, dtype, act, wide)
 
 
+# many tiles of every size that the products have, with ragged last ones; sums of one step to many
+@pytest.mark.parametrize("k", (8, 64, 72, 200, 1352))
+def test_many_tiles(k):
+    m, n = 2900, 3016
+    say(f"many tiles {m} {n} {k}")
+    run_linear(m, n, k, BF16, "silu", True, True, True)
+    run_linear(m, n, k, FP16, "none", False, False, False, pad=8)
+    run_ffn(m, k, 1528, BF16, "gelu", True)
+    run_linear_backward(m, k, n, BF16, "none", True)      # dx: sums over k
+    run_linear_backward(m, k, n, FP16, "relu", False)
+    run_linear_backward(k, m + 4, n, BF16, "none", False)  # dw: sums over k
+    run_linear_backward(k, m + 4, n, FP16, "silu", True)
+    run_ffn_backward(m, n, k, BF16, "silu", False)
+    run_ffn_backward(k, n, 1456, FP16, "gelu_tanh", True)
+
+
 # (row padding, first element): rows on 16 bytes, on 2 bytes, and a start off 16 bytes
 @pytest.mark.parametrize("pad,shift", [(8, 0), (8, 8), (1, 0), (13, 3), (0, 1), (64, 4)])
 @pytest.mark.parametrize("m,n,k", [(1, 72, 520), (7, 1001, 264), (136, 264, 200), (600, 1032, 328)])
