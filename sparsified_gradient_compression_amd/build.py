@@ -1,4 +1,5 @@
-"""Build libdgc.so for gfx950 with hipcc, in-tree.
+"""Build libdgc.so for gfx950 with hipcc, and the torch module over it with
+g++, in-tree.
 
     python -m sparsified_gradient_compression_amd.build
 
@@ -18,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libdgc.so")
+BINDING = os.path.join(LIBDIR, "_dgc_torch.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("dgc_api.hip", "dgc_gradset.hip", "dgc_layers.hip", "layers_bf16.hip", "layers_fp16.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
@@ -42,13 +45,28 @@ HIPCC_FLAGS = [
 ]
 
 
+def binding_command(out):
+    """g++ on the torch module: no GPU code, torch's headers and C++ ABI, and libdgc.so beside it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], "/opt/rocm/include",
+                                               os.path.join(ROOT, "include")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+            + [f for i in include for f in ("-isystem", i)]
+            + [BINDING_SOURCE, "-o", out, "-L", LIBDIR, "-l:libdgc.so", "-Wl,-rpath,$ORIGIN",
+               "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+
+
 def hipcc():
     exe = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
     return exe
 
 
 def build(verbose=True):
-    """Compile libdgc.so (always recompiles)."""
+    """Compile libdgc.so and the torch module over it (always recompiles)."""
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = LIB + ".tmp"
     compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
@@ -64,16 +82,18 @@ def build(verbose=True):
                       zip(SOURCES, objects)))
     run([hipcc(), f"--offload-arch={ARCH}", "-shared"] + objects + ["-o", tmp])
     os.replace(tmp, LIB)
+    run(binding_command(BINDING + ".tmp"))
+    os.replace(BINDING + ".tmp", BINDING)
     for o in objects:
         os.remove(o)
     return LIB
 
 
 def is_stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in DEPENDS)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    return any(os.path.getmtime(f) > t for f in DEPENDS + [BINDING_SOURCE])
 
 
 if __name__ == "__main__":

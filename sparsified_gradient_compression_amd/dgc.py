@@ -8,8 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
-from array import array
 from fractions import Fraction
 from typing import List, Optional, Sequence, Tuple
 
@@ -122,7 +120,7 @@ def lib() -> ctypes.CDLL:
         f.argtypes = [i64, i64, i64, i32, ctypes.POINTER(size)]
         f.restype = ctypes.c_int
         for call in (name, name + "_backward"):  # an argument block, workspace, its bytes, stream
-            getattr(L, call).argtypes = [ctypes.c_char_p, P, size, P]
+            getattr(L, call).argtypes = [P, P, size, P]
             getattr(L, call).restype = ctypes.c_int
     L.dgc_gradset_bytes.argtypes = [i32, P, P, ctypes.POINTER(size)]
     L.dgc_gradset_bytes.restype = ctypes.c_int
@@ -555,13 +553,6 @@ def _type_codes():
     return _types
 
 
-def _half_type(x, what: str) -> int:
-    code = _type_codes().get(x.dtype)
-    if code not in (DGC_BF16, DGC_FP16):
-        raise ValueError(f"{what}: expected bfloat16 or float16, got {x.dtype}")
-    return code
-
-
 def _act(act: str) -> int:
     code = ACTIVATIONS.get(act)
     if code is None:
@@ -569,46 +560,43 @@ def _act(act: str) -> int:
     return code
 
 
-def _mat(t, name: str, rows: int, cols: int, dtype, device: int) -> Tuple[int, int]:
-    """(pointer, leading dimension) of a rows x cols matrix; (0, 0) for None."""
-    if t is None:
-        return 0, 0
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != device or device < 0:
-        raise ValueError(f"{name}: expected a tensor on the device of the first argument, a GPU")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if rows <= 1:
-        ld = cols
-    if (step != 1 and cols > 1) or ld < cols:
-        raise ValueError(f"{name}: columns must be contiguous and rows must not overlap")
-    return t.data_ptr(), ld
+_native = None
 
 
-def _vec(t, name: str, n: int, dtype, device: int) -> int:
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on the same device")
-    return t.data_ptr()
+def _torch_calls():
+    """The module that checks torch tensors and calls libdgc (csrc/binding.cpp).  Raises if it has not been built."""
+    global _native
+    if _native is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, which the module needs)
+        lib()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"{_build.BINDING} is missing: build it with "
+                               "`python -m sparsified_gradient_compression_amd.build`")
+        spec = importlib.util.spec_from_file_location("_dgc_torch", _build.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module
+    return _native
 
 
-def _space(workspace, need, x, stream):
-    """(pointer, bytes) of the caller's workspace, or of a fresh one of need() bytes.  The fresh one is
-    returned too; it stays reserved until the call's stream has passed."""
-    if workspace is not None:
-        if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
-            raise ValueError("workspace: expected a contiguous tensor on the same device")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    size = need()
-    if size == 0:
-        return None, 0
+def _stream_on(x, stream) -> int:
+    """The handle of `stream`, or of the current stream of x's device."""
+    if stream is None:
+        import torch
+        if not x.is_cuda:
+            return 0  # refused by the call itself
+        return torch._C._cuda_getCurrentRawStream(x.get_device())
+    return _stream(stream)
+
+
+def _fresh(size: int, x, stream):
+    """A workspace of `size` bytes for one call; it stays reserved until the call's stream has passed."""
     import torch
-    fresh = torch.empty(size, dtype=torch.uint8, device=x.device)
-    _hold(fresh, stream)
-    return fresh.data_ptr(), size
+    t = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _hold(t, stream)
+    return t
 
 
 def _hold(t, stream):
@@ -625,13 +613,6 @@ def _new(x, shape, dtype, stream):
     t = torch.empty(shape, dtype=dtype, device=x.device)
     _hold(t, stream)
     return t
-
-
-def _sizes(x, w, name: str) -> Tuple[int, int, int]:
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"{name}: x and its weight must be matrices of equal width, got "
-                         f"{tuple(x.shape)} and {tuple(w.shape)}")
-    return x.shape[0], w.shape[0], x.shape[1]
 
 
 def _workspace(fn: str, m: int, n: int, k: int, backward: bool) -> int:
@@ -660,26 +641,17 @@ def gated_ffn_workspace(m: int, d: int, f: int, backward: bool = False, device="
     return torch.empty(dgc_gated_ffn_workspace_bytes(m, d, f, backward), dtype=torch.uint8, device=device)
 
 
-_pack_linear = struct.Struct("=5q" + "Qq" * 2 + "Q" + "Qq" * 3).pack
-_pack_linear_backward = struct.Struct("=6q" + "Qq" * 6 + "Q").pack
-_pack_ffn = struct.Struct("=5q" + "Qq" * 6).pack
-_pack_ffn_backward = struct.Struct("=6q" + "Qq" * 9).pack
-
-
 def linear(x, w, bias=None, residual=None, act: str = "none", out=None, pre=None, workspace=None, stream=None):
     """act(x w^T + bias) + residual for x [m, k] and w [n, k] (bfloat16 or float16, contiguous columns).
 
     `out` and `pre` are written if given; `pre` receives x w^T + bias for linear_backward.  `out` may be
     `residual`.  `workspace` is what linear_workspace(m, n, k) gives; without one the call allocates it."""
-    m, n, k = _sizes(x, w, "linear")
-    t, dt, dev = _half_type(x, "linear"), x.dtype, x.get_device()
     if out is None:
-        out = _new(x, (m, n), dt, stream)
-    args = _pack_linear(t, _act(act), m, n, k, *_mat(x, "x", m, k, dt, dev), *_mat(w, "w", n, k, dt, dev),
-                        _vec(bias, "bias", n, dt, dev), *_mat(residual, "residual", m, n, dt, dev),
-                        *_mat(out, "out", m, n, dt, dev), *_mat(pre, "pre", m, n, dt, dev))
-    ws, size = _space(workspace, lambda: dgc_linear_workspace_bytes(m, n, k), x, stream)
-    _check(lib().dgc_linear(args, ws, size, _stream(stream)), "dgc_linear")
+        out = _new(x, (x.shape[0], w.shape[0]), x.dtype, stream)
+    if workspace is None:
+        workspace = _fresh(dgc_linear_workspace_bytes(x.shape[0], w.shape[0], x.shape[-1]), x, stream)
+    _check(_torch_calls().linear(_act(act), x, w, bias, residual, out, pre, workspace, _stream_on(x, stream)),
+           "dgc_linear")
     return out
 
 
@@ -688,35 +660,22 @@ def linear_backward(dy, x, w, pre=None, act: str = "none", dx=None, dw=None, dbi
     """Gradients of linear for the incoming dy [m, n]: with dz = dy * act'(pre), writes each given one of
     dx [m, k] = dz w, dw [n, k] = dz^T x and dbias [n] = the column sums of dz.  dw and dbias are of x's
     type or float32 (the same for both): views of a learner's flat gradient.  Returns (dx, dw, dbias)."""
-    m, n, k = _sizes(x, w, "linear_backward")
-    t, dt, dev, a = _half_type(x, "linear_backward"), x.dtype, x.get_device(), _act(act)
-    if a != DGC_ACT_NONE and pre is None:
-        raise ValueError("linear_backward: an activation's gradient needs pre")
-    gt = dw.dtype if dw is not None else dbias.dtype if dbias is not None else dt
-    g = _type_codes().get(gt)
-    if g != t and g != DGC_FP32:
-        raise ValueError(f"linear_backward: weight gradients are {dt} or float32, not {gt}")
-    args = _pack_linear_backward(t, g, a, m, n, k, *_mat(dy, "dy", m, n, dt, dev), *_mat(x, "x", m, k, dt, dev),
-                                 *_mat(w, "w", n, k, dt, dev), *_mat(pre, "pre", m, n, dt, dev),
-                                 *_mat(dx, "dx", m, k, dt, dev), *_mat(dw, "dw", n, k, gt, dev),
-                                 _vec(dbias, "dbias", n, gt, dev))
-    ws, size = _space(workspace, lambda: dgc_linear_workspace_bytes(m, n, k, True), x, stream)
-    _check(lib().dgc_linear_backward(args, ws, size, _stream(stream)), "dgc_linear_backward")
+    if workspace is None:
+        workspace = _fresh(dgc_linear_workspace_bytes(x.shape[0], w.shape[0], x.shape[-1], True), x, stream)
+    _check(_torch_calls().linear_backward(_act(act), dy, x, w, pre, dx, dw, dbias, workspace, _stream_on(x, stream)),
+           "dgc_linear_backward")
     return dx, dw, dbias
 
 
 def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, gate=None, up=None, workspace=None, stream=None):
     """act(x w_gate^T) * (x w_up^T) for x [m, d] and weights [f, d].  `gate` and `up` receive the two
     products for gated_ffn_backward.  `workspace`: gated_ffn_workspace(m, d, f)."""
-    m, f, d = _sizes(x, w_gate, "gated_ffn")
-    t, dt, dev = _half_type(x, "gated_ffn"), x.dtype, x.get_device()
     if out is None:
-        out = _new(x, (m, f), dt, stream)
-    args = _pack_ffn(t, _act(act), m, d, f, *_mat(x, "x", m, d, dt, dev), *_mat(w_gate, "w_gate", f, d, dt, dev),
-                     *_mat(w_up, "w_up", f, d, dt, dev), *_mat(out, "out", m, f, dt, dev),
-                     *_mat(gate, "gate", m, f, dt, dev), *_mat(up, "up", m, f, dt, dev))
-    ws, size = _space(workspace, lambda: dgc_gated_ffn_workspace_bytes(m, d, f), x, stream)
-    _check(lib().dgc_gated_ffn(args, ws, size, _stream(stream)), "dgc_gated_ffn")
+        out = _new(x, (x.shape[0], w_gate.shape[0]), x.dtype, stream)
+    if workspace is None:
+        workspace = _fresh(dgc_gated_ffn_workspace_bytes(x.shape[0], x.shape[-1], w_gate.shape[0]), x, stream)
+    _check(_torch_calls().gated_ffn(_act(act), x, w_gate, w_up, out, gate, up, workspace, _stream_on(x, stream)),
+           "dgc_gated_ffn")
     return out
 
 
@@ -724,21 +683,10 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None
                        workspace=None, stream=None):
     """Gradients of gated_ffn for the incoming dh [m, f] and the saved gate and up: writes dx [m, d] if
     given, and dw_gate and dw_up [f, d] (together; x's type or float32).  Returns (dx, dw_gate, dw_up)."""
-    m, f, d = _sizes(x, w_gate, "gated_ffn_backward")
-    t, dt, dev = _half_type(x, "gated_ffn_backward"), x.dtype, x.get_device()
-    if (dw_gate is None) != (dw_up is None):
-        raise ValueError("gated_ffn_backward: dw_gate and dw_up come together")
-    gt = dt if dw_gate is None else dw_gate.dtype
-    g = _type_codes().get(gt)
-    if g != t and g != DGC_FP32:
-        raise ValueError(f"gated_ffn_backward: weight gradients are {dt} or float32, not {gt}")
-    args = _pack_ffn_backward(t, g, _act(act), m, d, f, *_mat(dh, "dh", m, f, dt, dev), *_mat(x, "x", m, d, dt, dev),
-                              *_mat(w_gate, "w_gate", f, d, dt, dev), *_mat(w_up, "w_up", f, d, dt, dev),
-                              *_mat(gate, "gate", m, f, dt, dev), *_mat(up, "up", m, f, dt, dev),
-                              *_mat(dx, "dx", m, d, dt, dev), *_mat(dw_gate, "dw_gate", f, d, gt, dev),
-                              *_mat(dw_up, "dw_up", f, d, gt, dev))
-    ws, size = _space(workspace, lambda: dgc_gated_ffn_workspace_bytes(m, d, f, True), x, stream)
-    _check(lib().dgc_gated_ffn_backward(args, ws, size, _stream(stream)), "dgc_gated_ffn_backward")
+    if workspace is None:
+        workspace = _fresh(dgc_gated_ffn_workspace_bytes(x.shape[0], x.shape[-1], w_gate.shape[0], True), x, stream)
+    _check(_torch_calls().gated_ffn_backward(_act(act), dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
+                                             _stream_on(x, stream)), "dgc_gated_ffn_backward")
     return dx, dw_gate, dw_up
 
 
@@ -772,19 +720,10 @@ class GradSet:
         self.scale = torch.empty(1, dtype=torch.float32, device=device)
         handle, s = ctypes.c_void_p(), _i64(self.sizes)
         t = np.ascontiguousarray(np.asarray(codes, np.int32))
+        self._layout = s.tobytes(), t.tobytes(), self.device
         _check(lib().dgc_gradset_init(ctypes.byref(handle), len(s), _hp(s), _hp(t), self.workspace.data_ptr(),
                                       self.workspace.numel(), _stream(stream)), "dgc_gradset_init")
         self.set = handle
-
-    def _pointers(self, tensors, what: str) -> array:
-        """The tensors' addresses, once every one is what the set was made for."""
-        import torch
-        t = torch.Tensor
-        if [x.dtype for x in tensors] != self.dtypes or list(map(t.numel, tensors)) != self.sizes:
-            raise ValueError(f"{what}: tensors differ from the set's shapes or dtypes")
-        if not all(map(t.is_contiguous, tensors)) or set(map(t.get_device, tensors)) != {self.device}:
-            raise ValueError(f"{what}: expected contiguous tensors on the set's device")
-        return array("Q", map(t.data_ptr, tensors))
 
     @staticmethod
     def _norm(norm: str) -> int:
@@ -795,33 +734,23 @@ class GradSet:
 
     def norm(self, grads: Sequence, norm: str = "l2", unscale: float = 1.0, stream=None):
         """unscale * the norm over all gradients, as a float64 tensor of one element."""
-        g = self._pointers(grads, "grads")
-        _check(lib().dgc_gradset_norm(self.set, g.buffer_info()[0], self._norm(norm), unscale,
-                                      self.total.data_ptr(), _stream(stream)), "dgc_gradset_norm")
+        _check(_torch_calls().set_norm(self.set.value, *self._layout, grads, self._norm(norm), unscale, self.total,
+                                       _stream_on(self.total, stream)), "dgc_gradset_norm")
         return self.total
 
     def clip(self, grads: Sequence, clip: float, out: Optional[Sequence] = None, norm: str = "l2",
              unscale: float = 1.0, stream=None):
         """out[t] = grads[t] * scale (in place without `out`), scale = unscale * min(1, clip / norm), for
         clip > 0.  Returns the norm."""
-        g = self._pointers(grads, "grads")
-        o = g if out is None else self._pointers(out, "out")
-        _check(lib().dgc_gradset_clip(self.set, g.buffer_info()[0], o.buffer_info()[0], clip, self._norm(norm),
-                                      unscale, self.total.data_ptr(), self.scale.data_ptr(), _stream(stream)),
-               "dgc_gradset_clip")
+        _check(_torch_calls().set_clip(self.set.value, *self._layout, grads, out, clip, self._norm(norm), unscale,
+                                       self.total, self.scale, _stream_on(self.total, stream)), "dgc_gradset_clip")
         return self.total
 
     def pack(self, grads: Sequence, flat, clip: float, norm: str = "l2", unscale: float = 1.0, stream=None):
         """The clipped gradients in float32, end to end in `flat`: what Learner.compress takes (with its own
         clip 0).  Returns the norm."""
-        import torch
-        g = self._pointers(grads, "grads")
-        if flat.dtype != torch.float32 or flat.numel() < self.n or flat.get_device() != self.device \
-                or not flat.is_contiguous():
-            raise ValueError(f"flat: expected at least {self.n} contiguous float32 elements on the set's device")
-        _check(lib().dgc_gradset_pack(self.set, g.buffer_info()[0], flat.data_ptr(), clip, self._norm(norm),
-                                      unscale, self.total.data_ptr(), self.scale.data_ptr(), _stream(stream)),
-               "dgc_gradset_pack")
+        _check(_torch_calls().set_pack(self.set.value, *self._layout, grads, flat, clip, self._norm(norm), unscale,
+                                       self.total, self.scale, _stream_on(self.total, stream)), "dgc_gradset_pack")
         return self.total
 
     def close(self):

@@ -5,6 +5,7 @@ the binding with host tensors, and the host code under sanitizers."""
 import ctypes
 import os
 import shutil
+import struct
 import subprocess
 
 import numpy as np
@@ -19,39 +20,47 @@ OK, EINVAL, ECAP = dgc.DGC_OK, dgc.DGC_EINVAL, dgc.DGC_ECAPACITY
 CSRC = os.path.join(ROOT, "sparsified_gradient_compression_amd", "csrc")
 A = 1 << 20  # an aligned address
 
+# the argument blocks of include/dgc.h, field by field
+LINEAR, LINEAR_BACKWARD = "=5q" + "Qq" * 2 + "Q" + "Qq" * 3, "=6q" + "Qq" * 6 + "Q"
+FFN, FFN_BACKWARD = "=5q" + "Qq" * 6, "=6q" + "Qq" * 9
+
+
+def call(name, fmt, values, ws, size):
+    return getattr(dgc.lib(), name)(struct.pack(fmt, *values), ws, size, None)
+
 
 def linear(ws=A, size=1 << 40, **kw):
     v = dict(type=1, act=0, m=4, n=8, k=16, x=A, ldx=16, w=A, ldw=16, bias=0, residual=0, ldr=0, y=A, ldy=8, pre=0, ldpre=0)
     v.update(kw)
-    return dgc.lib().dgc_linear(dgc._pack_linear(*v.values()), ws, size, None)
+    return call("dgc_linear", LINEAR, v.values(), ws, size)
 
 
 def linear_backward(ws=A, size=1 << 40, **kw):
     v = dict(type=1, grad_type=1, act=0, m=4, n=8, k=16, dy=A, lddy=8, x=A, ldx=16, w=A, ldw=16, pre=0, ldpre=0,
              dx=A, lddx=16, dw=A, lddw=16, dbias=0)
     v.update(kw)
-    return dgc.lib().dgc_linear_backward(dgc._pack_linear_backward(*v.values()), ws, size, None)
+    return call("dgc_linear_backward", LINEAR_BACKWARD, v.values(), ws, size)
 
 
 def ffn(ws=A, size=1 << 40, **kw):
     v = dict(type=1, act=2, m=4, d=16, f=8, x=A, ldx=16, w_gate=A, ldw_gate=16, w_up=A, ldw_up=16, h=A, ldh=8,
              gate=0, ldgate=0, up=0, ldup=0)
     v.update(kw)
-    return dgc.lib().dgc_gated_ffn(dgc._pack_ffn(*v.values()), ws, size, None)
+    return call("dgc_gated_ffn", FFN, v.values(), ws, size)
 
 
 def ffn_backward(ws=A, size=1 << 40, **kw):
     v = dict(type=1, grad_type=1, act=2, m=4, d=16, f=8, dh=A, lddh=8, x=A, ldx=16, w_gate=A, ldw_gate=16, w_up=A,
              ldw_up=16, gate=A, ldgate=8, up=A, ldup=8, dx=A, lddx=16, dw_gate=A, lddw_gate=16, dw_up=A, lddw_up=16)
     v.update(kw)
-    return dgc.lib().dgc_gated_ffn_backward(dgc._pack_ffn_backward(*v.values()), ws, size, None)
+    return call("dgc_gated_ffn_backward", FFN_BACKWARD, v.values(), ws, size)
 
 
 COMMON = [dict(type=0), dict(type=3), dict(act=-1), dict(act=5), dict(m=-1), dict(m=1 << 41), dict(x=0), dict(x=A + 1),
           dict(ldx=15), dict(ldx=1 << 60)]
 
 
-@pytest.mark.parametrize("call,bad", [
+@pytest.mark.parametrize("fn,bad", [
     (linear, COMMON + [dict(w=0), dict(ldw=15), dict(y=0), dict(ldy=7), dict(bias=A + 1), dict(residual=A, ldr=7),
                        dict(pre=A, ldpre=7), dict(n=-1), dict(k=-5), dict(y=A + 1), dict(m=1 << 40, ldx=1 << 39)]),
     (linear_backward, COMMON + [dict(dy=0), dict(lddy=7), dict(w=0), dict(act=1, pre=0), dict(act=1, pre=A, ldpre=7),
@@ -62,9 +71,9 @@ COMMON = [dict(type=0), dict(type=3), dict(act=-1), dict(act=5), dict(m=-1), dic
     (ffn_backward, COMMON + [dict(dh=0), dict(gate=0), dict(up=0), dict(ldgate=7), dict(dw_up=0), dict(dw_gate=0),
                              dict(grad_type=2), dict(lddx=15), dict(lddw_up=15), dict(w_gate=0), dict(ws=A + 8),
                              dict(ws=None), dict(grad_type=3, dw_gate=A + 2)])])
-def test_bad_arguments_are_refused_before_any_launch(call, bad):
+def test_bad_arguments_are_refused_before_any_launch(fn, bad):
     for kw in bad:
-        assert call(**kw) == EINVAL, kw
+        assert fn(**kw) == EINVAL, kw
 
 
 def test_null_argument_blocks_and_small_workspaces():
