@@ -21,17 +21,26 @@ size_t round_up(size_t x) { return (x + kPad - 1) / kPad * kPad; }
 
 }  // namespace
 
-Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts) {
+Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct) {
     Cut c;
     const int64_t outs = form == kDw ? parts : 1;
     const int64_t steps = cdiv64(k, 64) * (form == kDx ? parts : 1);
     const int64_t wide = form == kPair ? 2 * n : n;
-    c.tile = cdiv64(m, 128) * cdiv64(wide, 128) * outs >= kCUs ? 1 : 0;
-    const int64_t side = c.tile ? 128 : 64;
-    const int64_t tiles = cdiv64(m, side) * cdiv64(wide, side) * outs;
+    const auto tiles = [&](int tile) {
+        const TileSize t = tile_size(tile);
+        return cdiv64(m, t.m) * cdiv64(wide, t.n) * outs;
+    };
+    if (direct && tiles(kBig256) >= kCUs / 2)
+        c.tile = kBig256;
+    else if (tiles(kGuarded128) >= kCUs)
+        c.tile = direct ? kT128w8 : kGuarded128;
+    else
+        c.tile = direct ? (steps >= 8 ? kMid64x2 : kMid64) : kGuarded64;
     // too few tiles for the chip: cut the long axis, at least 4 steps each
+    const int64_t have = tiles(c.tile);
     int64_t splits = 1;
-    if (tiles > 0 && tiles < kCUs) splits = std::min(cdiv64(2 * kCUs, tiles), steps / 4);
+    if (have > 0 && have < kCUs && c.tile != kBig256)
+        splits = std::min(cdiv64(2 * kCUs, have), steps / 4);
     splits = std::max<int64_t>(splits, 1);
     c.per = std::max<int64_t>(cdiv64(steps, splits), 1);
     c.splits = int(std::max<int64_t>(cdiv64(steps, c.per), 1));
@@ -39,10 +48,12 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts) {
 }
 
 size_t product_bytes(int form, int64_t m, int64_t n, int64_t k, int parts) {
-    const Cut c = plan_product(form, m, n, k, parts);
-    if (c.splits == 1) return 0;
     const int64_t planes = form == kPair ? 2 : form == kDw ? parts : 1;
-    return round_up(size_t(c.splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
+    int64_t splits = 1;
+    for (const bool direct : {false, true})
+        splits = std::max<int64_t>(splits, plan_product(form, m, n, k, parts, direct).splits);
+    if (splits == 1) return 0;
+    return round_up(size_t(splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
 }
 
 namespace {

@@ -46,16 +46,40 @@ struct Product {
     Finish fin;
 };
 
-// Split of a product over its long axis: `splits` workgroups per tile, each
-// over `per` steps of 64; their 32-bit sums meet in the workspace.
+// The kernels: guarded and thin ones take any strides and alignment, the
+// others rows on 16 bytes.
+enum Tile {
+    kGuarded64, kGuarded128, kThin,
+    kMid64, kMid64x2, kBig256,
+    kT64k2s2, kT64k4, kT128s2, kT128w8, kT128x64, kT32x64, kT64x128, kT128w8s2, kT64x32
+};
+
+struct TileSize { int m, n; };
+inline TileSize tile_size(int t) {
+    switch (t) {
+        case kBig256: return {256, 256};
+        case kGuarded128: case kT128s2: case kT128w8: case kT128w8s2: return {128, 128};
+        case kThin: return {64, 16};
+        case kT128x64: return {128, 64};
+        case kT64x128: return {64, 128};
+        case kT32x64: return {32, 64};
+        case kT64x32: return {64, 32};
+        default: return {64, 64};
+    }
+}
+
+// Which kernel, and the split of a product over its long axis: `splits`
+// workgroups per tile, each over `per` steps of 64; their 32-bit sums meet in
+// the workspace.
 struct Cut {
-    int tile = 0;  // 0: 64 x 64, 1: 128 x 128
+    int tile = kGuarded64;
     int splits = 1;
     int64_t per = 0;
 };
 
-// Chosen from the sizes alone, so that a workspace can be made before the call.
-Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts);
+// From the sizes, and whether the operands' rows lie on 16 bytes.
+Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct);
+// The workspace of either, from the sizes alone.
 size_t product_bytes(int form, int64_t m, int64_t n, int64_t k, int parts);
 
 // The launchers, for DGC_BF16 and DGC_FP16 elements.  Each returns a DGC_* code.

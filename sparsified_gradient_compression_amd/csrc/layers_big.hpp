@@ -3,123 +3,35 @@
 //
 // Eight waves, two per SIMD, in two groups of four.  A group's waves lie on
 // different SIMDs, and the groups run half a phase apart: while one multiplies
-// (16 matrix instructions, 256 cycles), the other reads its next registers
+// (32 matrix instructions, 512 cycles), the other reads its next registers
 // from LDS and orders tiles from memory, so a SIMD's matrix unit always has a
 // wave to work for.  A barrier after every half phase keeps them so.
 //
 // LDS holds two tiles of 64 steps of k (128 KB), each as four regions: halves
-// of 128 rows of a (A0, A1) and of b (B0, B1).  A tile takes four phases:
+// of 128 rows of a (A0, A1) and of b (B0, B1).  A tile takes two phases:
 //
-//   read A0 | A0 x first B half | read the second B half | A0 x it
-//   read A1 | A1 x second half  | read the next tile's first half | A1 x first
+//   read A0, B0, B1, order A1 of the next tile            | multiply A0 x B
+//   read A1, order A0, B0, B1 of the tile after the next  | multiply A1 x B
 //
-// The half of b that the next tile starts with alternates, so that each phase
-// reads 8 or 4 fragments and none waits for registers.  Every phase also
-// orders one region of the tile after the next, into the region whose last
-// reads are over: memory goes straight to LDS, six phases (3000 cycles) ahead
-// of its use, and `vmcnt(12)` at the end of each read half phase is all the
-// waiting there is (six regions of two loads are in flight beyond it).
+// Every region is ordered as soon as its last reads are over, memory goes
+// straight to LDS, and it has three phases (3000 cycles) to come: at the end
+// of each half phase of reads `vmcnt(8)`, four regions of two loads, is all
+// the waiting there is.  Half phases of 16 matrix instructions leave the reads
+// less time than they take (8192 x 8192 x 4096: 394 us).
 #pragma once
 
-#include "layers_tile.hpp"
+#include "layers_direct.hpp"
 
 namespace dgc {
 namespace layers {
 
-// A byte offset past every buffer descriptor's end: reads as zero.
-constexpr uint32_t kOutside = 0x80000000u;
-
 constexpr int kRegion = 128 * kStep;  // elements of a region
-
-// s_waitcnt: at most 12 loads in flight, no LDS read.
-constexpr int kWait12Lds0 = 12 | (7 << 4) | (0 << 8);
 
 __device__ __forceinline__ void half_phase_end() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 }
-
-// How one side's regions come to LDS and to the registers.
-//   TR:    stored with m (n) contiguous: region [64 k][128]
-//   else:  stored with k contiguous:     region [128][64]
-//   NT:    16-row tiles of a wave in a region; NSIDE: dealt by n_row<NT>
-template <class T, bool TR, int NT, bool NSIDE>
-struct Side {
-    typedef typename Arith<T>::v8 v8;
-    uint32_t at[2][2];  // byte offset of this lane's pieces: half, load; kOutside if none
-    int k_at;           // first k of the lane's piece (TR: of load 0)
-    int frag[TR ? NT : 2];
-
-    // rows: how many rows (columns) exist from this tile's first on, per half
-    __device__ __forceinline__ void init(int64_t ld, int64_t rows0, int64_t rows1, int wave,
-                                         int lane, int base) {
-        const int i = lane & 15, g = lane >> 4;
-        if constexpr (TR) {
-            const int k = wave * 4 + (lane >> 4);
-            const int piece = ((((lane & 15) >> 1) ^ k_key<128>(k)) << 1) | (lane & 1);
-            k_at = k;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int l = 0; l < 2; ++l) {
-                    const int64_t have = h ? rows1 : rows0;
-                    at[h][l] = piece * 8 < have
-                                   ? uint32_t((int64_t(k + 32 * l) * ld + h * 128 + piece * 8) * 2)
-                                   : kOutside;
-                }
-            const int kk = g * 8 + (i >> 2);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                frag[j] = kk * 128 + ((((base >> 4) + j) ^ k_key<128>(kk)) << 4) + (i & 3) * 4;
-        } else {
-            const int r = wave * 8 + (lane >> 3);
-            const int piece = (lane & 7) ^ row_key<NT, NSIDE>(r);
-            k_at = piece * 8;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int l = 0; l < 2; ++l) {
-                    const int64_t have = h ? rows1 : rows0;
-                    const int row = r + 64 * l;
-                    at[h][l] = row < have ? uint32_t((int64_t(row) * ld + piece * 8) * 2) : kOutside;
-                }
-            const int fr = base + (NSIDE ? n_row<NT>(i, 0) : i);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                frag[s] = fr * kStep + (((s * 4 + g) ^ row_key<NT, NSIDE>(fr)) << 3);
-        }
-    }
-
-    // Order half h of a tile at `p` (its first row, its first k) of which
-    // `left` steps of k exist, into region `lds`.
-    __device__ __forceinline__ void order(const T* p, int left, int h, T* lds, int wave) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not know 16-byte loads to LDS
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<T*>(p), short(0), int(0x7FFFFFFF), 0x00020000);
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-            const uint32_t v = k_at + (TR ? 32 * l : 0) < left ? at[h][l] : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (DGC_LDS void*)(lds + (l * 8 + wave) * 512), 16, int(v), 0, 0, 0);
-        }
-#endif
-    }
-
-    // Fragment j, steps 32 s .. 32 s + 31, of a region.
-    __device__ __forceinline__ v8 get(const T* lds, int j, int s) const {
-        if constexpr (TR) {
-            union { s16x4 h[2]; v8 v; } u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (DGC_LDS s16x4*)(const_cast<T*>(lds + frag[j] + s * 32 * 128 + h * 4 * 128)));
-            return u.v;
-        } else {
-            return *reinterpret_cast<const v8*>(lds + frag[s] + j * (NSIDE ? 4 : 16) * kStep);
-        }
-    }
-};
 
 template <class T, int FORM>
 __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
@@ -147,11 +59,13 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     const int first = split * int(A.per);
     const int last = first + int(A.per) < total ? first + int(A.per) : total;
 
-    Side<T, ATR, 4, false> sa;
-    Side<T, BTR, 2, true> sb;
+    Side<T, ATR, 4, false, 128, 8> sa[2];
+    Side<T, BTR, 2, true, 128, 8> sb[2];
     const int64_t lda = A.lda[0], ldb = A.ldb[0];
-    sa.init(lda, A.M - m0, A.M - m0 - 128, wave, lane, wm * 64);
-    sb.init(ldb, A.N - n0, PAIR ? A.N - n0 : A.N - n0 - 128, wave, lane, wn * 32);
+    for (int h = 0; h < 2; ++h) {
+        sa[h].init(lda, A.M - m0 - h * 128, wave, lane, wm * 64);
+        sb[h].init(ldb, A.N - n0 - (PAIR ? 0 : h * 128), wave, lane, wn * 32);
+    }
 
     // Half h of tile t.  Beyond the last tile nothing is read, but the loads
     // are counted all the same.
@@ -160,18 +74,18 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
         const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
         const int64_t left = t < last ? A.K - k0 : 0;
         const T* p = static_cast<const T*>(A.a[FORM == kDw ? z : seg]) +
-                     (ATR ? k0 * lda + m0 : (m0 + h * 128) * lda + k0);
-        sa.order(left > 0 ? p : static_cast<const T*>(A.a[0]), left < kStep ? int(left) : kStep,
-                 h, lds, wave);
+                     (ATR ? k0 * lda + m0 + h * 128 : (m0 + h * 128) * lda + k0);
+        sa[h].order(left > 0 ? p : static_cast<const T*>(A.a[0]),
+                    left < kStep ? int(left) : kStep, lds, wave);
     };
     auto order_b = [&](int t, int h, T* lds) {
         const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
         const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
         const int64_t left = t < last ? A.K - k0 : 0;
         const T* p = static_cast<const T*>(A.b[PAIR ? h : seg]) +
-                     (BTR ? k0 * ldb + n0 : (n0 + (PAIR ? 0 : h * 128)) * ldb + k0);
-        sb.order(left > 0 ? p : static_cast<const T*>(A.b[0]), left < kStep ? int(left) : kStep,
-                 h, lds, wave);
+                     (BTR ? k0 * ldb + n0 + h * 128 : (n0 + (PAIR ? 0 : h * 128)) * ldb + k0);
+        sb[h].order(left > 0 ? p : static_cast<const T*>(A.b[0]),
+                    left < kStep ? int(left) : kStep, lds, wave);
     };
 
     f32x4 acc[2][2][4][2];
@@ -185,74 +99,69 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i][s] = sa.get(lds, i, s);
+            for (int i = 0; i < 4; ++i) fa[i][s] = sa[0].get(lds, i, s);
     };
     auto read_b = [&](int h, const T* lds) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[h][j][s] = sb.get(lds, j, s);
+            for (int j = 0; j < 2; ++j) fb[h][j][s] = sb[0].get(lds, j, s);
     };
     auto read_end = [&]() {
-        __builtin_amdgcn_s_waitcnt(kWait12Lds0);
+        __builtin_amdgcn_s_waitcnt(wait_for(8, 0));
         half_phase_end();
     };
-    auto multiply = [&](int ha, int hb) {
+    auto multiply = [&](int ha) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[ha][hb][i][j] = Arith<T>::mma(fb[hb][j][s], fa[i][s], acc[ha][hb][i][j]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[ha][hb][i][j] =
+                            Arith<T>::mma(fb[hb][j][s], fa[i][s], acc[ha][hb][i][j]);
         __builtin_amdgcn_s_setprio(0);
         half_phase_end();
     };
-    // Tile t, of the parity whose first half of b is f: its four regions, and
-    // the next tile's first region of b.
-    auto tile = [&](int t, int f, T* la0, T* la1, T* lbf, T* lbs, const T* next) {
+    auto tile = [&](int t, T* la0, T* la1, T* lb0, T* lb1, T* other_a1) {
+        read_b(0, lb0);
         read_a(la0);
-        order_b(t + 2, f, lbf);
+        read_b(1, lb1);
+        order_a(t + 1, 1, other_a1);
         read_end();
-        multiply(0, f);
-        read_b(1 - f, lbs);
-        order_a(t + 2, 0, la0);
-        read_end();
-        multiply(0, 1 - f);
+        multiply(0);
         read_a(la1);
-        order_b(t + 2, 1 - f, lbs);
+        order_a(t + 2, 0, la0);
+        order_b(t + 2, 0, lb0);
+        order_b(t + 2, 1, lb1);
         read_end();
-        multiply(1, 1 - f);
-        read_b(1 - f, next);
-        order_a(t + 2, 1, la1);
-        read_end();
-        multiply(1, f);
+        multiply(1);
     };
 
-    order_b(first, 0, b00);
     order_a(first, 0, a00);
+    order_b(first, 0, b00);
     order_b(first, 1, b01);
     order_a(first, 1, a01);
-    order_b(first + 1, 1, b11);
     order_a(first + 1, 0, a10);
     order_b(first + 1, 0, b10);
-    order_a(first + 1, 1, a11);
+    order_b(first + 1, 1, b11);
     read_end();
-    read_b(0, b00);
-    read_end();  // tile first + 2 may go there from now on
     if (wm == 1) half_phase_end();
     // by twos: with an odd count the last tile is one of zeros
     for (int t = first; t < last; t += 2) {
-        tile(t, 0, a00, a01, b00, b01, b11);
-        tile(t + 1, 1, a10, a11, b11, b10, b00);
+        tile(t, a00, a01, b00, b01, a11);
+        tile(t + 1, a10, a11, b10, b11, a01);
     }
     if (wm == 0) half_phase_end();
     __builtin_amdgcn_s_waitcnt(0);
 
     __syncthreads();  // nobody reads a region any more, and no load is under way
 
-    // 64 x 64 outputs of the wave at a time, in the 16 KB of one region
+    // 64 x 64 outputs of the wave at a time, in the 16 KB of one region (which the
+    // compiler need not tell apart any more)
     T* const own = wave < 4 ? (wave < 2 ? (wave ? a01 : a00) : (wave & 1 ? a11 : a10))
                             : (wave < 6 ? (wave & 1 ? b01 : b00) : (wave & 1 ? b11 : b10));
     float* out = reinterpret_cast<float*>(own);
@@ -265,7 +174,7 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
                 put_tile<4, 2, BTR>(out, mt, j / 2 * 32, j % 2, lane, acc[ha][j / 2][mt][j % 2]);
         const int64_t n = n0 + wn * 32;
         put_wave<T, FORM, 4, 4>(A, split, z, m0 + ha * 128 + wm * 64, n, PAIR ? n : n + 128, lane,
-                                out);
+                                out, 0, 1, 0);
     }
 }
 

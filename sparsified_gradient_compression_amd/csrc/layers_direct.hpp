@@ -1,0 +1,97 @@
+// layers_direct.hpp -- operand tiles that go from memory straight to LDS.
+#pragma once
+
+#include "layers_tile.hpp"
+
+namespace dgc {
+namespace layers {
+
+// A byte offset past every buffer descriptor's end: reads as zero.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// s_waitcnt's operand: at most `loads` loads and `lds` LDS operations under way.
+constexpr int wait_for(int loads, int lds) {
+    return (loads & 15) | (loads >> 4) << 14 | 7 << 4 | lds << 8;
+}
+
+// How the regions of one side come to LDS and to the registers.  A region is
+// 64 steps of k of R rows (columns), brought in by W waves.
+//   TR:    stored with m (n) contiguous: [64 k][R] in LDS
+//   else:  stored with k contiguous:     [R][64]
+//   NT:    16-row tiles of a wave in a region; NSIDE: dealt by n_row<NT>
+// The swizzle of piece_at is applied to the addresses in memory: a wave's load
+// fills 1 KB of LDS in lane order.
+template <class T, bool TR, int NT, bool NSIDE, int R, int W>
+struct Side {
+    typedef typename Arith<T>::v8 v8;
+    static constexpr int kLoads = R / (8 * W);    // of a wave, per region
+    static constexpr int kRowsK = W * 512 / R;    // TR: steps of k per load of all waves
+    uint32_t at[kLoads];  // byte offset of this lane's pieces; kOutside if none
+    int k_at;             // first k of the lane's piece (TR: of load 0)
+    int frag[TR ? NT : 2];
+
+    // have: how many rows (columns) there are from the region's first on
+    __device__ __forceinline__ void init(int64_t ld, int64_t have, int wave, int lane, int base) {
+        const int i = lane & 15, g = lane >> 4;
+        if constexpr (TR) {
+            constexpr int kPer = R / 8;  // pieces of a step of k
+            const int k = wave * (64 / kPer) + lane / kPer, p = lane % kPer;
+            const int piece = (((p >> 1) ^ k_key<R>(k)) << 1) | (p & 1);
+            k_at = k;
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l)
+                at[l] = piece * 8 < have
+                            ? uint32_t((int64_t(k + kRowsK * l) * ld + piece * 8) * 2)
+                            : kOutside;
+            const int kk = g * 8 + (i >> 2);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                frag[j] = kk * R + ((((base >> 4) + j) ^ k_key<R>(kk)) << 4) + (i & 3) * 4;
+        } else {
+            const int r = wave * 8 + (lane >> 3);
+            const int piece = (lane & 7) ^ row_key<NT, NSIDE>(r);
+            k_at = piece * 8;
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                const int row = r + 8 * W * l;
+                at[l] = row < have ? uint32_t((int64_t(row) * ld + piece * 8) * 2) : kOutside;
+            }
+            const int fr = base + (NSIDE ? n_row<NT>(i, 0) : i);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                frag[s] = fr * kStep + (((s * 4 + g) ^ row_key<NT, NSIDE>(fr)) << 3);
+        }
+    }
+
+    // Order the region at `p` (its first row, its first k) of which `left`
+    // steps of k exist, into `lds`.
+    __device__ __forceinline__ void order(const T* p, int left, T* lds, int wave) const {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not know 16-byte loads to LDS
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T*>(p), short(0), int(0x7FFFFFFF), 0x00020000);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+            const uint32_t v = k_at + (TR ? kRowsK * l : 0) < left ? at[l] : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (DGC_LDS void*)(lds + (l * W + wave) * 512), 16, int(v), 0, 0, 0);
+        }
+#endif
+    }
+
+    // Fragment j, steps 32 s .. 32 s + 31, of a region.
+    __device__ __forceinline__ v8 get(const T* lds, int j, int s) const {
+        if constexpr (TR) {
+            union { s16x4 h[2]; v8 v; } u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (DGC_LDS s16x4*)(const_cast<T*>(lds + frag[j] + s * 32 * R + h * 4 * R)));
+            return u.v;
+        } else {
+            return *reinterpret_cast<const v8*>(lds + frag[s] + j * (NSIDE ? 4 : 16) * kStep);
+        }
+    }
+};
+
+}  // namespace layers
+}  // namespace dgc

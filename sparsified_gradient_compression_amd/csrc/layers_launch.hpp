@@ -4,6 +4,8 @@
 
 #include "layers_big.hpp"
 #include "layers_elem.hpp"
+#include "layers_mid.hpp"
+#include "layers_thin.hpp"
 #include "layers_tile.hpp"
 
 namespace dgc {
@@ -33,12 +35,36 @@ template <class T, int FORM>
 int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
     const int64_t blocks = a.mt * a.nt * (FORM == kDw ? a.parts : 1) * c.splits;
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
-    if (c.tile == 2)
-        k_big<T, FORM><<<dim3(unsigned(blocks)), 512, 0, s>>>(a);
-    else if (c.tile == 0)
-        k_tile<T, FORM, 64, 64, 2, 2><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
-    else
-        k_tile<T, FORM, 128, 128, 2, 2><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    switch (c.tile) {
+        case kGuarded64: k_tile<T, FORM, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a); break;
+        case kGuarded128: k_tile<T, FORM, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a); break;
+        case kMid64: k_mid<T, FORM, 64, 64, 2, 2, 1, 4><<<grid, 256, 0, s>>>(a); break;
+        case kMid64x2: k_mid<T, FORM, 64, 64, 2, 2, 2, 4><<<grid, 512, 0, s>>>(a); break;
+        case kT64k2s2: k_mid<T, FORM, 64, 64, 2, 2, 4, 2><<<grid, 1024, 0, s>>>(a); break;
+        case kT64k4: k_mid<T, FORM, 64, 64, 2, 2, 2, 2><<<grid, 512, 0, s>>>(a); break;
+        case kT128s2: k_mid<T, FORM, 128, 128, 2, 2, 1, 2><<<grid, 256, 0, s>>>(a); break;
+        case kT128w8: k_mid<T, FORM, 128, 128, 2, 4, 1, 4><<<grid, 512, 0, s>>>(a); break;
+        case kT128w8s2: k_mid<T, FORM, 128, 128, 2, 4, 1, 2><<<grid, 512, 0, s>>>(a); break;
+        case kT128x64: k_mid<T, FORM, 128, 64, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a); break;
+        case kT64x128: k_mid<T, FORM, 64, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a); break;
+        case kT32x64: k_mid<T, FORM, 32, 64, 2, 2, 4, 3><<<grid, 1024, 0, s>>>(a); break;
+        case kT64x32:
+            if constexpr (FORM != kPair) k_mid<T, FORM, 64, 32, 4, 1, 4, 3><<<grid, 1024, 0, s>>>(a);
+            break;
+        case kThin:
+            if constexpr (FORM == kRows || FORM == kPair) {
+                const dim3 rows(unsigned(cdiv64(a.N, 16)));
+                if (a.M <= 16)
+                    k_thin<T, FORM == kPair, 1><<<rows, 512, 0, s>>>(a);
+                else if (a.M <= 32)
+                    k_thin<T, FORM == kPair, 2><<<rows, 512, 0, s>>>(a);
+                else
+                    k_thin<T, FORM == kPair, 4><<<rows, 512, 0, s>>>(a);
+            }
+            break;
+        default: k_big<T, FORM><<<grid, 512, 0, s>>>(a);
+    }
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }
@@ -46,15 +72,8 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
 template <class T>
 int Launch<T>::product(const Product& p, void* ws, hipStream_t s) {
     if (p.m == 0 || p.n == 0) return DGC_OK;
-    Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts);
-    const int64_t big = cdiv64(p.m, 256) * cdiv64(p.form == kPair ? 2 * p.n : p.n, 256) *
-                        (p.form == kDw ? p.parts : 1);
-    if (big >= 128 && direct(p)) {
-        c.tile = 2;
-        c.splits = 1;
-        c.per = cdiv64(p.k, 64) * (p.form == kDx ? p.parts : 1);
-    }
-    const int64_t side = c.tile == 2 ? 256 : c.tile ? 128 : 64;
+    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p));
+    const TileSize side = tile_size(c.tile);
     TileArgs a{};
     for (int i = 0; i < 2; ++i) {
         a.a[i] = p.a[i].p;
@@ -65,8 +84,8 @@ int Launch<T>::product(const Product& p, void* ws, hipStream_t s) {
     a.M = p.m;
     a.N = p.n;
     a.K = p.k;
-    a.mt = cdiv64(p.m, side);
-    a.nt = cdiv64(p.n, p.form == kPair ? side / 2 : side);
+    a.mt = cdiv64(p.m, side.m);
+    a.nt = cdiv64(p.n, p.form == kPair ? side.n / 2 : side.n);
     a.per = c.per;
     a.splits = c.splits;
     a.parts = p.parts;

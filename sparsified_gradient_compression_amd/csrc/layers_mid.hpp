@@ -1,0 +1,142 @@
+// layers_mid.hpp -- outputs of one or two hundred tiles, or few: bound by
+// latency and by how many workgroups there are rather than by the matrix units.
+//
+// A ring of S tiles of 64 steps of k in LDS: loads go from memory straight
+// there, S - 1 tiles ahead, and one barrier per tile both ends the reads of
+// the oldest and shows the newest.  With KG > 1 as many groups of waves share
+// the outputs and take the tiles of k in turn, each in a ring of its own, so
+// that a long sum takes fewer steps; their sums meet in LDS.
+#pragma once
+
+#include "layers_direct.hpp"
+
+namespace dgc {
+namespace layers {
+
+template <class T, int FORM, int BM, int BN, int WM, int WN, int KG, int S>
+__global__ __launch_bounds__(WM* WN* KG * 64) void k_mid(TileArgs A) {
+    constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
+    constexpr int W = WM * WN;
+    constexpr int MT = BM / WM / 16, NTW = BN / WN / 16;  // 16 x 16 tiles of a wave
+    constexpr int NT = PAIR ? NTW / 2 : NTW;              // ... of one product
+    constexpr int RB = PAIR ? BN / 2 : BN;                // rows of a region of b
+    constexpr int kTile = (BM + BN) * kStep;              // elements of both sides' tiles
+    typedef typename Arith<T>::v8 v8;
+    __shared__ __align__(16) T s0[KG * kTile], s1[KG * kTile];
+    __shared__ __align__(16) T s2[S > 2 ? KG * kTile : 8], s3[S > 3 ? KG * kTile : 8];
+    const int lane = threadIdx.x & 63;
+    const int all = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int wave = all % W, group = all / W;
+    const int wm = wave / WN, wn = wave % WN;
+
+    const int64_t tiles = A.mt * A.nt;
+    int64_t id = blockIdx.x;
+    const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
+    const int split = int(id / per_split);
+    id -= split * per_split;
+    const int z = FORM == kDw ? int(id / tiles) : 0;
+    id -= z * tiles;
+    int64_t tm, tn;
+    place(id, A.mt, A.nt, tm, tn);
+    const int64_t m0 = tm * BM, n0 = tn * RB;
+
+    const int ksteps = int((A.K + kStep - 1) / kStep);
+    const int total = ksteps * (FORM == kDx ? A.parts : 1);
+    const int first = split * int(A.per);
+    const int last = first + int(A.per) < total ? first + int(A.per) : total;
+    const int rounds = (last - first + KG - 1) / KG;
+
+    Side<T, ATR, MT, false, BM, W> sa;
+    Side<T, BTR, NT, true, RB, W> sb;
+    const int64_t lda = A.lda[0], ldb = A.ldb[0];
+    sa.init(lda, A.M - m0, wave, lane, wm * MT * 16);
+    sb.init(ldb, A.N - n0, wave, lane, wn * NT * 16);
+    constexpr int kLoads = decltype(sa)::kLoads + (PAIR ? 2 : 1) * decltype(sb)::kLoads;
+
+    // The group's tile of round r; nothing is read beyond the last one.
+    auto order = [&](int r, T* ring) {
+        const int t = first + r * KG + group;
+        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
+        const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
+        const int64_t more = t < last ? A.K - k0 : 0;
+        const int left = more < kStep ? int(more) : kStep;
+        const int64_t at = more > 0 ? k0 : 0;
+        T* lds = ring + group * kTile;
+        sa.order(static_cast<const T*>(A.a[FORM == kDw ? z : seg]) +
+                     (ATR ? at * lda + m0 : m0 * lda + at), left, lds, wave);
+#pragma unroll
+        for (int w = 0; w < (PAIR ? 2 : 1); ++w)
+            sb.order(static_cast<const T*>(A.b[PAIR ? w : seg]) +
+                         (BTR ? at * ldb + n0 : n0 * ldb + at), left,
+                     lds + BM * kStep + w * RB * kStep, wave);
+    };
+
+    f32x4 acc[MT][NTW];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    auto round = [&](int r, const T* use, T* fill) {
+        __builtin_amdgcn_s_waitcnt(wait_for((S - 2) * kLoads, 15));
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        order(r + S - 1, fill);
+        const T* la = use + group * kTile;
+        const T* lb = la + BM * kStep;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            v8 fa[MT], fb[NTW];
+#pragma unroll
+            for (int j = 0; j < NTW; ++j)
+                fb[j] = sb.get(lb + (PAIR ? j / NT * RB * kStep : 0), PAIR ? j % NT : j, s);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) fa[i] = sa.get(la, i, s);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NTW; ++j) acc[i][j] = Arith<T>::mma(fb[j], fa[i], acc[i][j]);
+        }
+    };
+    order(0, s0);
+    if (S > 2) order(1, s1);
+    if (S > 3) order(2, s2);
+    for (int r = 0; r < rounds;) {
+        round(r, s0, S == 2 ? s1 : S == 3 ? s2 : s3);
+        if (++r >= rounds) break;
+        round(r, s1, s0);
+        if (++r >= rounds) break;
+        if constexpr (S > 2) {
+            round(r, s2, s1);
+            if (++r >= rounds) break;
+        }
+        if constexpr (S > 3) {
+            round(r, s3, s2);
+            if (++r >= rounds) break;
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
+    __syncthreads();  // nobody reads the ring any more, and no load is under way
+
+    // the outputs' 32-bit sums through LDS: as many waves' as fit in a tile of
+    // the ring, the others' in the next
+    constexpr int kOwn = MT * NTW * 256;
+    constexpr int kFit = KG * kTile * int(sizeof(T)) / (kOwn * 4);
+    constexpr int kGroupStride = W * kOwn;
+    static_assert(KG == 1 ? 2 * kFit >= W : kFit >= KG * W, "outputs fit the ring");
+    float* out = reinterpret_cast<float*>(wave < kFit ? s0 : s1) + wave % kFit * kOwn;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+            put_tile<NTW, NT, BTR>(out + group * kGroupStride, mt, j / NT * NT * 16, j % NT, lane,
+                                   acc[mt][j]);
+    if (KG > 1) __syncthreads();
+    const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
+    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out, group, KG,
+                               kGroupStride);
+}
+
+}  // namespace layers
+}  // namespace dgc

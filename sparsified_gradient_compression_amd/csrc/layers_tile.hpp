@@ -313,9 +313,12 @@ struct Frag {
 // whole of it unrolled over every register.
 //   columns of the first and the second half of the wave's start at n0, n1
 //   (kPair: of the first and the second product, the same ones)
+//   groups: so many waves hold sums of the same outputs, `stride` floats
+//   apart, to be added in that order; each finishes its share of the rows
 template <class T, int FORM, int MT, int NTW>
 __device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, int64_t m0,
-                                         int64_t n0, int64_t n1, int lane, float* lds) {
+                                         int64_t n0, int64_t n1, int lane, const float* lds,
+                                         int group, int groups, int stride) {
     constexpr bool PAIR = FORM == kPair;
     constexpr int W = NTW * 16;                     // columns in LDS
     constexpr int kLanes = PAIR ? W / 16 : W / 8;   // lanes per row
@@ -323,18 +326,23 @@ __device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, in
     const int c = lane % kLanes;
     const int64_t n = c * 8 < W / 2 ? n0 + c * 8 : n1 + c * 8 - W / 2;
 #pragma unroll 1
-    for (int r = lane / kLanes; r < MT * 16; r += kRows) {
+    for (int r = group * kRows + lane / kLanes; r < MT * 16; r += kRows * groups) {
         const int64_t m = m0 + r;
         if (m >= A.M) break;
         float v[8], v2[8];
         const int key = (r & (W / 8 - 1)) << 1;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            *reinterpret_cast<f32x4*>(v + 4 * q) =
-                *reinterpret_cast<const f32x4*>(lds + r * W + ((2 * c + q) ^ key) * 4);
-            if (PAIR)
-                *reinterpret_cast<f32x4*>(v2 + 4 * q) = *reinterpret_cast<const f32x4*>(
-                    lds + r * W + ((2 * c + q + W / 8) ^ key) * 4);
+            const float* p = lds + r * W + ((2 * c + q) ^ key) * 4;
+            const float* p2 = lds + r * W + ((2 * c + q + W / 8) ^ key) * 4;
+            f32x4 t = *reinterpret_cast<const f32x4*>(p), t2 = {0, 0, 0, 0};
+            if (PAIR) t2 = *reinterpret_cast<const f32x4*>(p2);
+            for (int w = 1; w < groups; ++w) {
+                t += *reinterpret_cast<const f32x4*>(p + w * stride);
+                if (PAIR) t2 += *reinterpret_cast<const f32x4*>(p2 + w * stride);
+            }
+            *reinterpret_cast<f32x4*>(v + 4 * q) = t;
+            *reinterpret_cast<f32x4*>(v2 + 4 * q) = t2;
         }
         const int valid = A.N - n < 8 ? int(A.N - n) : 8;
         if (valid <= 0) continue;
@@ -478,7 +486,8 @@ __global__ __launch_bounds__(WM* WN * 64) void k_tile(TileArgs A) {
         for (int j = 0; j < NTW; ++j)
             put_tile<NTW, NT, BTR>(out, mt, j / NT * NT * 16, j % NT, lane, acc[mt][j]);
     const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
-    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out);
+    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out, 0, 1,
+                               0);
 }
 
 // The sums of all splits, added in their order, then finished.  One thread
