@@ -13,10 +13,20 @@ namespace dgc {
 namespace layers {
 
 // A matrix in device memory: rows of `ld` elements, the columns contiguous.
+// padded: its rows go on with zeros up to a multiple of 8 columns.
 struct Mat {
     const void* p = nullptr;
     int64_t ld = 0;
+    bool padded = false;
 };
+
+// Whether a matrix's rows lie on 16 bytes and end there too, with offsets
+// within 128 rows (64 of k) inside 2^31 bytes: what loads from memory
+// straight to LDS need.
+inline bool direct(const Mat& a, int64_t cols) {
+    return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.ld % 8 == 0 &&
+           (a.padded || cols % 8 == 0) && a.ld <= (int64_t(1) << 22);
+}
 
 // How an output is finished from the 32-bit sums of its product.
 struct Finish {
@@ -46,56 +56,62 @@ struct Product {
     Finish fin;
 };
 
-// The kernels: guarded and thin ones take any strides and alignment, the
-// others rows on 16 bytes.
-enum Tile {
-    kGuarded64, kGuarded128, kThin,
-    kMid64, kMid64x2, kBig256,
-    kT64k2s2, kT64k4, kT128s2, kT128w8, kT128x64, kT32x64, kT64x128, kT128w8s2, kT64x32
-};
+// The kernels.  Guarded and thin ones take any strides and alignment, the
+// others rows on 16 bytes.  Outputs per workgroup:
+//   kGuarded  64 x 64     kMid32  32 x 64, four groups of waves over k
+//   kThin     64 x 16     kMid64  64 x 64, two groups
+//   kBig      256 x 256   kMid128 128 x 128 with a ring of four tiles, one
+//                         workgroup per compute unit; kPair128 with two, and two
+enum Tile { kGuarded, kThin, kMid32, kMid64, kMid128, kPair128, kBig };
 
-struct TileSize { int m, n; };
-inline TileSize tile_size(int t) {
-    switch (t) {
-        case kBig256: return {256, 256};
-        case kGuarded128: case kT128s2: case kT128w8: case kT128w8s2: return {128, 128};
-        case kThin: return {64, 16};
-        case kT128x64: return {128, 64};
-        case kT64x128: return {64, 128};
-        case kT32x64: return {32, 64};
-        case kT64x32: return {64, 32};
-        default: return {64, 64};
-    }
-}
+struct TileSize {
+    int64_t m, n;
+};
+constexpr TileSize kTileSize[] = {{64, 64},   {64, 16},   {32, 64},  {64, 64},
+                                  {128, 128}, {128, 128}, {256, 256}};
 
 // Which kernel, and the split of a product over its long axis: `splits`
 // workgroups per tile, each over `per` steps of 64; their 32-bit sums meet in
 // the workspace.
 struct Cut {
-    int tile = kGuarded64;
+    int tile = kGuarded;
     int splits = 1;
     int64_t per = 0;
+    double us = 0;  // what it is expected to take
 };
 
 // From the sizes, and whether the operands' rows lie on 16 bytes.
 Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct);
-// The workspace of either, from the sizes alone.
-size_t product_bytes(int form, int64_t m, int64_t n, int64_t k, int parts);
 
 // The launchers, for DGC_BF16 and DGC_FP16 elements.  Each returns a DGC_* code.
 template <class T>
 struct Launch {
     static int product(const Product& p, void* ws, hipStream_t s);
-    // dz = dy * act'(pre) (dz null: not written), and the column sums of dz
-    // into dbias (null: none) through `part`.
+    // dz = dy * act'(pre) (dz null: not written; its rows padded with zeros to
+    // ldz), and the column sums of dz into dbias (null: none) through `part`.
     static int slope(int64_t m, int64_t n, Mat dy, Mat pre, int act, void* dz, int64_t ldz,
                      void* dbias, int wide, float* part, hipStream_t s);
-    // da = dh * up * act'(gate), db = dh * act(gate)
+    // da = dh * up * act'(gate), db = dh * act(gate), rows padded to ld
     static int gate_slope(int64_t m, int64_t f, Mat dh, Mat gate, Mat up, int act, void* da,
                           void* db, int64_t ld, hipStream_t s);
 };
 
-constexpr int64_t kSumRows = 128;  // rows per block of a column sum
+// Rows that are laid out anew, on 16 bytes and padded with zeros.
+struct Repack {
+    const void* from[3];
+    void* to[3];
+    int64_t ld[3], rows[3], cols[3];
+    int count = 0;
+};
+int repack(const Repack& r, hipStream_t s);
+
+// Rows per workgroup of a column sum over 512 columns: enough workgroups for
+// the chip (8 waves on each SIMD), then as few as that.
+inline int64_t sum_rows(int64_t m, int64_t n) {
+    int64_t r = 8;
+    while (r < 128 && (n + 511) / 512 * (m / r) > 2048) r *= 2;
+    return r;
+}
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -12,19 +12,19 @@
 namespace dgc {
 namespace layers {
 
-// dz = dy * act'(pre), and the sums of dz's columns over kSumRows rows each.
-// A block covers 512 columns (64 threads, 8 columns each) by kSumRows rows
+// dz = dy * act'(pre), and the sums of dz's columns over `per` rows each.
+// A block covers 512 columns (64 threads, 8 columns each) by `per` rows
 // (4 rows of threads).  The column sums use dz before it is rounded.
 template <class T>
-__global__ __launch_bounds__(256) void k_slope(int64_t M, int64_t N, const T* dy, int64_t lddy,
+__global__ __launch_bounds__(256) void k_slope(int64_t M, int64_t N, int64_t per, const T* dy, int64_t lddy,
                                                const T* pre, int64_t ldp, int act, T* dz,
                                                int64_t ldz, float* part) {
     __shared__ float sums[4][512];
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
     const int64_t n = int64_t(blockIdx.x) * 512 + tx * 8;
     const int valid = N - n >= 8 ? 8 : N > n ? int(N - n) : 0;
-    const int64_t m0 = int64_t(blockIdx.y) * kSumRows;
-    const int64_t m1 = m0 + kSumRows < M ? m0 + kSumRows : M;
+    const int64_t m0 = int64_t(blockIdx.y) * per;
+    const int64_t m1 = m0 + per < M ? m0 + per : M;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (valid > 0) {
 #pragma unroll 4
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void k_slope(int64_t M, int64_t N, const T* dy
                     d[i] *= slope;
                 }
             }
-            if (dz) store_row<T, 8>(dz + m * ldz + n, valid, d);
+            if (dz) store_row<T, 8>(dz + m * ldz + n, 8, d);  // zeros in the padding
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += d[i];
         }
@@ -66,6 +66,7 @@ __global__ __launch_bounds__(256) void k_sum_columns(int64_t rows, int64_t N, co
     const int64_t n = int64_t(blockIdx.x) * 32 + tx;
     float s = 0.0f;
     if (n < N)
+#pragma unroll 8
         for (int64_t r = ty; r < rows; r += 8) s += part[r * N + n];
     sums[ty][tx] = s;
     __syncthreads();
@@ -97,8 +98,8 @@ __global__ __launch_bounds__(256) void k_gate_slope(int64_t M, int64_t F, const 
         oa[i] = d[i] * b[i] * slope;
         ob[i] = d[i] * value;
     }
-    store_row<T, 8>(da + m * ld + n, valid, oa);
-    store_row<T, 8>(db + m * ld + n, valid, ob);
+    store_row<T, 8>(da + m * ld + n, 8, oa);  // zeros in the padding
+    store_row<T, 8>(db + m * ld + n, 8, ob);
 }
 
 }  // namespace layers

@@ -14,14 +14,6 @@ namespace layers {
 #define DGC_LAYERS_CHECK() \
     if (hipGetLastError() != hipSuccess) return DGC_EHIP
 
-// Whether a matrix's rows lie on 16 bytes and end there too, with offsets
-// within 128 rows (64 of k) inside 2^31 bytes: what loads from memory
-// straight to LDS need.
-inline bool direct(const Mat& a, int64_t cols) {
-    return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.ld % 8 == 0 && cols % 8 == 0 &&
-           a.ld <= (int64_t(1) << 22);
-}
-
 inline bool direct(const Product& p) {
     const int64_t ca = p.form == kDw ? p.m : p.k, cb = p.form == kRows || p.form == kPair ? p.k : p.n;
     const bool two_a = p.form != kRows && p.form != kPair && p.parts == 2;
@@ -37,24 +29,15 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (c.tile) {
-        case kGuarded64: k_tile<T, FORM, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a); break;
-        case kGuarded128: k_tile<T, FORM, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a); break;
-        case kMid64: k_mid<T, FORM, 64, 64, 2, 2, 1, 4><<<grid, 256, 0, s>>>(a); break;
-        case kMid64x2: k_mid<T, FORM, 64, 64, 2, 2, 2, 4><<<grid, 512, 0, s>>>(a); break;
-        case kT64k2s2: k_mid<T, FORM, 64, 64, 2, 2, 4, 2><<<grid, 1024, 0, s>>>(a); break;
-        case kT64k4: k_mid<T, FORM, 64, 64, 2, 2, 2, 2><<<grid, 512, 0, s>>>(a); break;
-        case kT128s2: k_mid<T, FORM, 128, 128, 2, 2, 1, 2><<<grid, 256, 0, s>>>(a); break;
-        case kT128w8: k_mid<T, FORM, 128, 128, 2, 4, 1, 4><<<grid, 512, 0, s>>>(a); break;
-        case kT128w8s2: k_mid<T, FORM, 128, 128, 2, 4, 1, 2><<<grid, 512, 0, s>>>(a); break;
-        case kT128x64: k_mid<T, FORM, 128, 64, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a); break;
-        case kT64x128: k_mid<T, FORM, 64, 128, 2, 2, 1, 3><<<grid, 256, 0, s>>>(a); break;
-        case kT32x64: k_mid<T, FORM, 32, 64, 2, 2, 4, 3><<<grid, 1024, 0, s>>>(a); break;
-        case kT64x32:
-            if constexpr (FORM != kPair) k_mid<T, FORM, 64, 32, 4, 1, 4, 3><<<grid, 1024, 0, s>>>(a);
-            break;
-        case kThin:
+        case kGuarded: k_tile<T, FORM, 64, 64, 2, 2><<<grid, 256, 0, s>>>(a); break;
+        case kMid32: k_mid<T, FORM, 32, 64, 2, 2, 4, 3><<<grid, 1024, 0, s>>>(a); break;
+        case kMid64: k_mid<T, FORM, 64, 64, 2, 2, 2, 4><<<grid, 512, 0, s>>>(a); break;
+        case kMid128: k_mid<T, FORM, 128, 128, 2, 4, 1, 4><<<grid, 512, 0, s>>>(a); break;
+        case kPair128: k_mid<T, FORM, 128, 128, 2, 4, 1, 2><<<grid, 512, 0, s>>>(a); break;
+        case kBig: k_big<T, FORM><<<grid, 512, 0, s>>>(a); break;
+        default:
             if constexpr (FORM == kRows || FORM == kPair) {
-                const dim3 rows(unsigned(cdiv64(a.N, 16)));
+                const dim3 rows(static_cast<unsigned>(cdiv64(a.N, 16)));
                 if (a.M <= 16)
                     k_thin<T, FORM == kPair, 1><<<rows, 512, 0, s>>>(a);
                 else if (a.M <= 32)
@@ -62,8 +45,6 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
                 else
                     k_thin<T, FORM == kPair, 4><<<rows, 512, 0, s>>>(a);
             }
-            break;
-        default: k_big<T, FORM><<<grid, 512, 0, s>>>(a);
     }
     DGC_LAYERS_CHECK();
     return DGC_OK;
@@ -73,7 +54,7 @@ template <class T>
 int Launch<T>::product(const Product& p, void* ws, hipStream_t s) {
     if (p.m == 0 || p.n == 0) return DGC_OK;
     const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p));
-    const TileSize side = tile_size(c.tile);
+    const TileSize side = kTileSize[c.tile];
     TileArgs a{};
     for (int i = 0; i < 2; ++i) {
         a.a[i] = p.a[i].p;
@@ -114,17 +95,16 @@ template <class T>
 int Launch<T>::slope(int64_t m, int64_t n, Mat dy, Mat pre, int act, void* dz, int64_t ldz,
                      void* dbias, int wide, float* part, hipStream_t s) {
     if (n == 0 || (!dz && !dbias)) return DGC_OK;
-    const int64_t rows = cdiv64(m, kSumRows);
-    if (rows > 65535 * 32768ll) return DGC_EINVAL;
+    const int64_t per = sum_rows(m, n), rows = cdiv64(m, per);
     if (m > 0) {
         // grid.y holds at most 65535 blocks of rows
         const int64_t kMost = 65535;
         for (int64_t r = 0; r < rows; r += kMost) {
             const int64_t now = rows - r < kMost ? rows - r : kMost;
-            const int64_t m0 = r * kSumRows;
-            const int64_t left = m - m0 < now * kSumRows ? m - m0 : now * kSumRows;
+            const int64_t m0 = r * per;
+            const int64_t left = m - m0 < now * per ? m - m0 : now * per;
             k_slope<T><<<dim3(unsigned(cdiv64(n, 512)), unsigned(now)), 256, 0, s>>>(
-                left, n, static_cast<const T*>(dy.p) + m0 * dy.ld, dy.ld,
+                left, n, per, static_cast<const T*>(dy.p) + m0 * dy.ld, dy.ld,
                 pre.p ? static_cast<const T*>(pre.p) + m0 * pre.ld : nullptr, pre.ld, act,
                 dz ? static_cast<T*>(dz) + m0 * ldz : nullptr, ldz,
                 dbias ? part + r * n : nullptr);
