@@ -36,7 +36,7 @@ struct Cost {
     int64_t round, light;
     double start, full_step, light_step;
 };
-constexpr Cost kCosts[] = {{kGuarded, 512, 256, 3.0, 0.85, 0.66}, {kMid32, 256, 256, 2.5, 0.17, 0.17},
+constexpr Cost kCosts[] = {{kGuarded, 256, 256, 3.0, 0.22, 0.22}, {kMid32, 256, 256, 2.5, 0.17, 0.17},
                            {kMid64, 256, 256, 2.5, 0.24, 0.24},   {kMid128, 256, 256, 3.0, 0.62, 0.62},
                            {kPair128, 512, 256, 3.0, 1.08, 0.80}, {kBig, 256, 256, 5.0, 1.50, 1.50}};
 
@@ -44,6 +44,15 @@ constexpr Cost kCosts[] = {{kGuarded, 512, 256, 3.0, 0.85, 0.66}, {kMid32, 256, 
 double join_us(double bytes) { return 6.0 + bytes / 3e6; }
 
 }  // namespace
+
+bool direct(const Product& p) {
+    const int64_t ca = p.form == kDw ? p.m : p.k, cb = p.form == kRows || p.form == kPair ? p.k : p.n;
+    const bool two_a = p.form != kRows && p.form != kPair && p.parts == 2;
+    const bool two_b = p.form == kPair || (p.form == kDx && p.parts == 2);
+    if (!direct(p.a[0], ca) || !direct(p.b[0], cb)) return false;
+    if (two_a && (!direct(p.a[1], ca) || p.a[1].ld != p.a[0].ld)) return false;
+    return !two_b || (direct(p.b[1], cb) && p.b[1].ld == p.b[0].ld);
+}
 
 Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct) {
     const int64_t outs = form == kDw ? parts : 1;
@@ -86,6 +95,32 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
 }
 
 namespace {
+
+constexpr double kLaunchUs = 3.0;  // between two launches
+
+// The kernel that takes both gradients of a layer in the least time, together.
+int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
+    int tile = kGuarded;
+    best = 1e30;
+    const double sx = double(std::max<int64_t>(cdiv64(dx.k, 64) * dx.parts, 1));
+    const double sw = double(std::max<int64_t>(cdiv64(dw.k, 64), 1));
+    for (const Cost& c : kCosts) {
+        if ((c.tile == kGuarded) == direct || c.tile == kBig) continue;
+        const TileSize t = kTileSize[c.tile];
+        const double nx = double(cdiv64(dx.m, t.m) * cdiv64(dx.n, t.n));
+        const double nw = double(cdiv64(dw.m, t.m) * cdiv64(dw.n, t.n) * dw.parts);
+        // workgroups of both kinds fill up the rounds: as much as all of them
+        // take, at least as long as the longer kind's
+        const double all = (nx * sx + nw * sw) / double(c.round) * c.full_step;
+        const double us = c.start + std::max(all, std::max(sx, sw) * c.light_step) +
+                          (nx + nw > double(c.round) ? c.start / 2 : 0);
+        if (us < best) {
+            best = us;
+            tile = c.tile;
+        }
+    }
+    return tile;
+}
 
 // Sizes whose products of two stay far from 2^63 bytes.
 constexpr int64_t kMostSide = int64_t(1) << 40;
@@ -196,52 +231,44 @@ Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
     return {to, pad8(cols), true};
 }
 
-// Rows at any even address to rows on 16 bytes, zeros up to their ends; one
-// thread per 8 elements.
-__global__ __launch_bounds__(256) void k_repack(Repack r) {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    typedef u32x4 u32x4_any __attribute__((aligned(2), may_alias));
-    int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        if (i >= r.count) return;
-        const int64_t per = (r.cols[i] + 7) / 8, have = per * r.rows[i];
-        if (id < have) {
-            const int64_t row = id / per, col = (id - row * per) * 8;
-            const uint16_t* p = static_cast<const uint16_t*>(r.from[i]) + row * r.ld[i] + col;
-            u32x4 v;
-            if (col + 8 <= r.cols[i]) {
-                v = *reinterpret_cast<const u32x4_any*>(p);
-            } else {
-                uint16_t t[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] = col + e < r.cols[i] ? p[e] : uint16_t(0);
-                __builtin_memcpy(&v, t, 16);
-            }
-            reinterpret_cast<u32x4*>(r.to[i])[id] = v;
-            return;
-        }
-        id -= have;
-    }
+int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
+    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p));
+    return type == DGC_BF16 ? Launch<__bf16>::product(p, c, ws, s)
+                            : Launch<_Float16>::product(p, c, ws, s);
 }
 
-int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
-    return type == DGC_BF16 ? Launch<__bf16>::product(p, ws, s)
-                            : Launch<_Float16>::product(p, ws, s);
+int run_prepare(int64_t type, const SlopeArgs& a, const Repack& r, hipStream_t s) {
+    return type == DGC_BF16 ? Launch<__bf16>::prepare(a, r, s)
+                            : Launch<_Float16>::prepare(a, r, s);
+}
+
+// The gradients' products and the column sums: in one launch where a kernel
+// takes both products whole in less time than each its own way and a launch
+// more.  Either product's output may be null.
+int run_gradients(int64_t type, const Product& dx, const Product& dw, const Sums& sums, void* ws,
+                  hipStream_t s) {
+    const bool has_dx = dx.fin.out[0] && dx.m > 0 && dx.n > 0;
+    const bool has_dw = dw.fin.out[0] && dw.m > 0 && dw.n > 0;
+    int rc = DGC_OK;
+    if (has_dx && has_dw) {
+        const bool d = direct(dx) && direct(dw);
+        const Cut cx = plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx));
+        const Cut cw = plan_product(kDw, dw.m, dw.n, dw.k, dw.parts, direct(dw));
+        const double apart = cx.us + cw.us + (sums.out ? 2 : 1) * kLaunchUs;
+        double us = 0;
+        const int tile = plan_both(dx, dw, d, us);
+        if (us < apart)
+            return type == DGC_BF16 ? Launch<__bf16>::both(dx, dw, tile, sums, s)
+                                    : Launch<_Float16>::both(dx, dw, tile, sums, s);
+    }
+    if (has_dx) rc = run_product(type, dx, ws, s);
+    if (rc == DGC_OK && has_dw) rc = run_product(type, dw, ws, s);
+    if (rc == DGC_OK)
+        rc = type == DGC_BF16 ? Launch<__bf16>::sum(sums, s) : Launch<_Float16>::sum(sums, s);
+    return rc;
 }
 
 }  // namespace
-
-int repack(const Repack& r, hipStream_t s) {
-    if (r.count == 0) return DGC_OK;
-    int64_t pieces = 0;
-    for (int i = 0; i < r.count; ++i) pieces += r.rows[i] * ((r.cols[i] + 7) / 8);
-    const int64_t blocks = cdiv64(pieces, 256);
-    if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
-    k_repack<<<dim3(unsigned(blocks)), 256, 0, s>>>(r);
-    return hipGetLastError() == hipSuccess ? DGC_OK : DGC_EHIP;
-}
-
 }  // namespace layers
 }  // namespace dgc
 
@@ -281,7 +308,7 @@ int dgc_linear(const dgc_linear_args* a, void* workspace, size_t workspace_bytes
     p.k = k;
     p.a[0] = packed(r, sp.pack, {a->x, a->ldx}, m, k, ws + sp.x);
     p.b[0] = packed(r, sp.pack, {a->w, a->ldw}, n, k, ws + sp.w);
-    rc = repack(r, stream);
+    rc = run_prepare(a->type, SlopeArgs{}, r, stream);
     if (rc != DGC_OK) return rc;
     p.fin.out[0] = a->y;
     p.fin.ldo = a->ldy;
@@ -316,42 +343,50 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     Mat x{a->x, a->ldx}, w{a->w, a->ldw}, dz{a->dy, a->lddy};
     if (a->dw) x = packed(r, sp.pack, x, m, k, ws + sp.x);
     if (a->dx) w = packed(r, sp.pack, w, n, k, ws + sp.w);
-    rc = repack(r, stream);
-    if (rc != DGC_OK) return rc;
     // without an activation dz is dy, copied only where its rows do not lie on 16 bytes
     const bool copied = (a->dx || a->dw) && (sloped || (sp.pack && !direct(dz, n)));
     if (copied) dz = {ws + sp.dz, pad8(n), true};
-    rc = (a->type == DGC_BF16 ? Launch<__bf16>::slope : Launch<_Float16>::slope)(
-        m, n, {a->dy, a->lddy}, {sloped ? a->pre : nullptr, a->ldpre}, int(a->act),
-        copied ? ws + sp.dz : nullptr, pad8(n), a->dbias, wide,
-        reinterpret_cast<float*>(ws + sp.sums), stream);
+    SlopeArgs sl;
+    Sums sums;
+    if (copied || a->dbias) {
+        sl.M = m;
+        sl.N = n;
+        sl.per = sum_rows(m, n);
+        sl.dy = a->dy;
+        sl.lddy = a->lddy;
+        sl.pre = a->pre;
+        sl.ldp = a->ldpre;
+        sl.act = int32_t(a->act);
+        sl.dz = copied ? ws + sp.dz : nullptr;
+        sl.ldz = pad8(n);
+        sl.part = a->dbias ? reinterpret_cast<float*>(ws + sp.sums) : nullptr;
+        sums.rows = cdiv64(m, sl.per);
+        sums.N = n;
+        sums.part = sl.part;
+        sums.out = a->dbias;
+        sums.wide = wide;
+    }
+    rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
-    Product p;
-    if (a->dx) {
-        p.form = kDx;
-        p.m = m;
-        p.n = k;
-        p.k = n;
-        p.a[0] = dz;
-        p.b[0] = w;
-        p.fin.out[0] = a->dx;
-        p.fin.ldo = a->lddx;
-        rc = run_product(a->type, p, ws + sp.part, stream);
-        if (rc != DGC_OK) return rc;
-    }
-    if (a->dw) {
-        p.form = kDw;
-        p.m = n;
-        p.n = k;
-        p.k = m;
-        p.a[0] = dz;
-        p.b[0] = x;
-        p.fin.out[0] = a->dw;
-        p.fin.ldo = a->lddw;
-        p.fin.wide = wide;
-        rc = run_product(a->type, p, ws + sp.part, stream);
-    }
-    return rc;
+    Product dx, dw;
+    dx.form = kDx;
+    dx.m = m;
+    dx.n = k;
+    dx.k = n;
+    dx.a[0] = dz;
+    dx.b[0] = w;
+    dx.fin.out[0] = a->dx;
+    dx.fin.ldo = a->lddx;
+    dw.form = kDw;
+    dw.m = n;
+    dw.n = k;
+    dw.k = m;
+    dw.a[0] = dz;
+    dw.b[0] = x;
+    dw.fin.out[0] = a->dw;
+    dw.fin.ldo = a->lddw;
+    dw.fin.wide = wide;
+    return run_gradients(a->type, dx, dw, sums, ws + sp.part, stream);
 }
 
 int dgc_gated_ffn(const dgc_gated_ffn_args* a, void* workspace, size_t workspace_bytes,
@@ -375,7 +410,7 @@ int dgc_gated_ffn(const dgc_gated_ffn_args* a, void* workspace, size_t workspace
     p.a[0] = packed(r, sp.pack, {a->x, a->ldx}, m, d, ws + sp.x);
     p.b[0] = packed(r, sp.pack, {a->w_gate, a->ldw_gate}, f, d, ws + sp.w);
     p.b[1] = packed(r, sp.pack, {a->w_up, a->ldw_up}, f, d, ws + sp.w2);
-    rc = repack(r, stream);
+    rc = run_prepare(a->type, SlopeArgs{}, r, stream);
     if (rc != DGC_OK) return rc;
     p.fin.out[0] = a->h;
     p.fin.ldo = a->ldh;
@@ -407,7 +442,6 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     if (!a->dx && !a->dw_gate) return DGC_OK;
     char* ws = static_cast<char*>(workspace);
     const int64_t ld = pad8(f);
-    void *da = ws + sp.dz, *db = ws + sp.dz + row_bytes(m, f);
     Repack r;
     Mat x{a->x, a->ldx}, wg{a->w_gate, a->ldw_gate}, wu{a->w_up, a->ldw_up};
     if (a->dw_gate) x = packed(r, sp.pack, x, m, d, ws + sp.x);
@@ -415,42 +449,45 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
         wg = packed(r, sp.pack, wg, f, d, ws + sp.w);
         wu = packed(r, sp.pack, wu, f, d, ws + sp.w2);
     }
-    rc = repack(r, stream);
+    SlopeArgs sl;
+    sl.M = m;
+    sl.N = f;
+    sl.dy = a->dh;
+    sl.lddy = a->lddh;
+    sl.pre = a->gate;
+    sl.ldp = a->ldgate;
+    sl.up = a->up;
+    sl.ldu = a->ldup;
+    sl.act = int32_t(a->act);
+    sl.dz = ws + sp.dz;
+    sl.dz2 = ws + sp.dz + row_bytes(m, f);
+    sl.ldz = ld;
+    rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
-    rc = (a->type == DGC_BF16 ? Launch<__bf16>::gate_slope : Launch<_Float16>::gate_slope)(
-        m, f, {a->dh, a->lddh}, {a->gate, a->ldgate}, {a->up, a->ldup}, int(a->act), da, db, ld,
-        stream);
-    if (rc != DGC_OK) return rc;
-    Product p;
-    p.parts = 2;
-    p.a[0] = {da, ld, true};
-    p.a[1] = {db, ld, true};
-    if (a->dx) {
-        p.form = kDx;
-        p.m = m;
-        p.n = d;
-        p.k = f;
-        p.b[0] = wg;
-        p.b[1] = wu;
-        p.fin.out[0] = a->dx;
-        p.fin.ldo = a->lddx;
-        rc = run_product(a->type, p, ws + sp.part, stream);
-        if (rc != DGC_OK) return rc;
-    }
-    if (a->dw_gate) {
-        p.form = kDw;
-        p.m = f;
-        p.n = d;
-        p.k = m;
-        p.b[0] = x;
-        p.fin.out[0] = a->dw_gate;
-        p.fin.ldo = a->lddw_gate;
-        p.fin.out[1] = a->dw_up;
-        p.fin.ldo2 = a->lddw_up;
-        p.fin.wide = wide;
-        rc = run_product(a->type, p, ws + sp.part, stream);
-    }
-    return rc;
+    Product dx, dw;
+    dx.form = kDx;
+    dx.parts = 2;
+    dx.m = m;
+    dx.n = d;
+    dx.k = f;
+    dx.b[0] = wg;
+    dx.b[1] = wu;
+    dx.fin.out[0] = a->dx;
+    dx.fin.ldo = a->lddx;
+    dw.form = kDw;
+    dw.parts = 2;
+    dw.m = f;
+    dw.n = d;
+    dw.k = m;
+    dw.b[0] = x;
+    dw.fin.out[0] = a->dw_gate;
+    dw.fin.ldo = a->lddw_gate;
+    dw.fin.out[1] = a->dw_up;
+    dw.fin.ldo2 = a->lddw_up;
+    dw.fin.wide = wide;
+    dx.a[0] = dw.a[0] = {sl.dz, ld, true};
+    dx.a[1] = dw.a[1] = {sl.dz2, ld, true};
+    return run_gradients(a->type, dx, dw, Sums{}, ws + sp.part, stream);
 }
 
 }  // extern "C"

@@ -58,7 +58,7 @@ struct Product {
 
 // The kernels.  Guarded and thin ones take any strides and alignment, the
 // others rows on 16 bytes.  Outputs per workgroup:
-//   kGuarded  64 x 64     kMid32  32 x 64, four groups of waves over k
+//   kGuarded  64 x 64, four groups; kMid32  32 x 64, four groups of waves over k
 //   kThin     64 x 16     kMid64  64 x 64, two groups
 //   kBig      256 x 256   kMid128 128 x 128 with a ring of four tiles, one
 //                         workgroup per compute unit; kPair128 with two, and two
@@ -80,20 +80,30 @@ struct Cut {
     double us = 0;  // what it is expected to take
 };
 
+// Whether the kernels that take rows on 16 bytes can take this product.
+bool direct(const Product& p);
+
 // From the sizes, and whether the operands' rows lie on 16 bytes.
 Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct);
 
-// The launchers, for DGC_BF16 and DGC_FP16 elements.  Each returns a DGC_* code.
-template <class T>
-struct Launch {
-    static int product(const Product& p, void* ws, hipStream_t s);
-    // dz = dy * act'(pre) (dz null: not written; its rows padded with zeros to
-    // ldz), and the column sums of dz into dbias (null: none) through `part`.
-    static int slope(int64_t m, int64_t n, Mat dy, Mat pre, int act, void* dz, int64_t ldz,
-                     void* dbias, int wide, float* part, hipStream_t s);
-    // da = dh * up * act'(gate), db = dh * act(gate), rows padded to ld
-    static int gate_slope(int64_t m, int64_t f, Mat dh, Mat gate, Mat up, int act, void* da,
-                          void* db, int64_t ld, hipStream_t s);
+// dz = dy * act'(pre), its rows padded with zeros to ldz, and the sums of its
+// columns over `per` rows each into `part` (either null: not wanted); with
+// `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums.
+struct SlopeArgs {
+    int64_t M = 0, N = 0, per = 0;
+    const void *dy = nullptr, *pre = nullptr, *up = nullptr;
+    int64_t lddy = 0, ldp = 0, ldu = 0, ldz = 0;
+    void *dz = nullptr, *dz2 = nullptr;
+    float* part = nullptr;
+    int32_t act = 0;
+};
+
+// The partial column sums, to be added up into `out` (null: none).
+struct Sums {
+    int64_t rows = 0, N = 0;
+    const float* part = nullptr;
+    void* out = nullptr;
+    int32_t wide = 0;
 };
 
 // Rows that are laid out anew, on 16 bytes and padded with zeros.
@@ -103,7 +113,6 @@ struct Repack {
     int64_t ld[3], rows[3], cols[3];
     int count = 0;
 };
-int repack(const Repack& r, hipStream_t s);
 
 // Rows per workgroup of a column sum over 512 columns: enough workgroups for
 // the chip (8 waves on each SIMD), then as few as that.
@@ -112,6 +121,19 @@ inline int64_t sum_rows(int64_t m, int64_t n) {
     while (r < 128 && (n + 511) / 512 * (m / r) > 2048) r *= 2;
     return r;
 }
+
+// The launchers, for DGC_BF16 and DGC_FP16 elements.  Each returns a DGC_* code.
+template <class T>
+struct Launch {
+    static int product(const Product& p, const Cut& c, void* ws, hipStream_t s);
+    // dx and dw of one layer (neither split, the same kernel for both) and the
+    // column sums in one launch
+    static int both(const Product& dx, const Product& dw, int tile, const Sums& sums,
+                    hipStream_t s);
+    // slopes (none if a.N is 0) and rows laid out anew in one launch
+    static int prepare(const SlopeArgs& a, const Repack& r, hipStream_t s);
+    static int sum(const Sums& a, hipStream_t s);
+};
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

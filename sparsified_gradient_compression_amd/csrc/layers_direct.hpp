@@ -22,17 +22,15 @@ constexpr int wait_for(int loads, int lds) {
 // The swizzle of piece_at is applied to the addresses in memory: a wave's load
 // fills 1 KB of LDS in lane order.
 template <class T, bool TR, int NT, bool NSIDE, int R, int W>
-struct Side {
-    typedef typename Arith<T>::v8 v8;
+struct Side : Frags<T, TR, NT, NSIDE, R> {
     static constexpr int kLoads = R / (8 * W);    // of a wave, per region
     static constexpr int kRowsK = W * 512 / R;    // TR: steps of k per load of all waves
     uint32_t at[kLoads];  // byte offset of this lane's pieces; kOutside if none
     int k_at;             // first k of the lane's piece (TR: of load 0)
-    int frag[TR ? NT : 2];
 
     // have: how many rows (columns) there are from the region's first on
     __device__ __forceinline__ void init(int64_t ld, int64_t have, int wave, int lane, int base) {
-        const int i = lane & 15, g = lane >> 4;
+        Frags<T, TR, NT, NSIDE, R>::init(lane, base);
         if constexpr (TR) {
             constexpr int kPer = R / 8;  // pieces of a step of k
             const int k = wave * (64 / kPer) + lane / kPer, p = lane % kPer;
@@ -43,10 +41,6 @@ struct Side {
                 at[l] = piece * 8 < have
                             ? uint32_t((int64_t(k + kRowsK * l) * ld + piece * 8) * 2)
                             : kOutside;
-            const int kk = g * 8 + (i >> 2);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                frag[j] = kk * R + ((((base >> 4) + j) ^ k_key<R>(kk)) << 4) + (i & 3) * 4;
         } else {
             const int r = wave * 8 + (lane >> 3);
             const int piece = (lane & 7) ^ row_key<NT, NSIDE>(r);
@@ -56,10 +50,6 @@ struct Side {
                 const int row = r + 8 * W * l;
                 at[l] = row < have ? uint32_t((int64_t(row) * ld + piece * 8) * 2) : kOutside;
             }
-            const int fr = base + (NSIDE ? n_row<NT>(i, 0) : i);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                frag[s] = fr * kStep + (((s * 4 + g) ^ row_key<NT, NSIDE>(fr)) << 3);
         }
     }
 
@@ -76,20 +66,6 @@ struct Side {
                 rsrc, (DGC_LDS void*)(lds + (l * W + wave) * 512), 16, int(v), 0, 0, 0);
         }
 #endif
-    }
-
-    // Fragment j, steps 32 s .. 32 s + 31, of a region.
-    __device__ __forceinline__ v8 get(const T* lds, int j, int s) const {
-        if constexpr (TR) {
-            union { s16x4 h[2]; v8 v; } u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (DGC_LDS s16x4*)(const_cast<T*>(lds + frag[j] + s * 32 * R + h * 4 * R)));
-            return u.v;
-        } else {
-            return *reinterpret_cast<const v8*>(lds + frag[s] + j * (NSIDE ? 4 : 16) * kStep);
-        }
     }
 };
 

@@ -1,5 +1,6 @@
 // layers_elem.hpp -- the element-wise passes of the layer gradients: what the
-// activation's slope makes of an incoming gradient, and column sums.
+// activation's slope makes of an incoming gradient, column sums, and operands
+// laid out anew.
 //
 // The products that follow take 16-bit operands, so dz (da, db) is rounded
 // once to the elements' own type here, as the incoming gradient was: a
@@ -12,94 +13,152 @@
 namespace dgc {
 namespace layers {
 
-// dz = dy * act'(pre), and the sums of dz's columns over `per` rows each.
-// A block covers 512 columns (64 threads, 8 columns each) by `per` rows
-// (4 rows of threads).  The column sums use dz before it is rounded.
+// dz = dy * act'(pre) and the sums of dz's columns (before it is rounded) over
+// `per` rows each.  A block of 256 threads covers 512 columns (64 threads, 8
+// columns each) by `per` rows (4 rows of threads).
 template <class T>
-__global__ __launch_bounds__(256) void k_slope(int64_t M, int64_t N, int64_t per, const T* dy, int64_t lddy,
-                                               const T* pre, int64_t ldp, int act, T* dz,
-                                               int64_t ldz, float* part) {
-    __shared__ float sums[4][512];
+__device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, float (*sums)[512]) {
+    const int64_t across = (A.N + 511) / 512;
+    const int64_t by = id / across, bx = id - by * across;
     const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    const int64_t n = int64_t(blockIdx.x) * 512 + tx * 8;
-    const int valid = N - n >= 8 ? 8 : N > n ? int(N - n) : 0;
-    const int64_t m0 = int64_t(blockIdx.y) * per;
-    const int64_t m1 = m0 + per < M ? m0 + per : M;
+    const int64_t n = bx * 512 + tx * 8;
+    const int valid = A.N - n >= 8 ? 8 : A.N > n ? int(A.N - n) : 0;
+    const int64_t m0 = by * A.per;
+    const int64_t m1 = m0 + A.per < A.M ? m0 + A.per : A.M;
+    const T* dy = static_cast<const T*>(A.dy);
+    const T* pre = static_cast<const T*>(A.pre);
+    T* dz = static_cast<T*>(A.dz);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (valid > 0) {
-#pragma unroll 4
-        for (int64_t m = m0 + ty; m < m1; m += 4) {
-            float d[8], z[8];
-            load_row<T, 8>(dy + m * lddy + n, valid, d);
-            if (act != DGC_ACT_NONE) {
-                load_row<T, 8>(pre + m * ldp + n, valid, z);
+        for (int64_t m = m0 + ty; m < m1; m += 8) {  // two rows' loads under way
+            float d[2][8], z[2][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float value, slope;
-                    act_pair(act, z[i], value, slope);
-                    d[i] *= slope;
+            for (int r = 0; r < 2; ++r)
+                if (m + 4 * r < m1) {
+                    load_row<T, 8>(dy + (m + 4 * r) * A.lddy + n, valid, d[r]);
+                    if (A.act != DGC_ACT_NONE)
+                        load_row<T, 8>(pre + (m + 4 * r) * A.ldp + n, valid, z[r]);
                 }
-            }
-            if (dz) store_row<T, 8>(dz + m * ldz + n, 8, d);  // zeros in the padding
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += d[i];
+            for (int r = 0; r < 2; ++r)
+                if (m + 4 * r < m1) {
+                    if (A.act != DGC_ACT_NONE) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float value, slope;
+                            act_pair(A.act, z[r][i], value, slope);
+                            d[r][i] *= slope;
+                        }
+                    }
+                    // zeros in the padding
+                    if (dz) store_row<T, 8>(dz + (m + 4 * r) * A.ldz + n, 8, d[r]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += d[r][i];
+                }
         }
     }
-    if (!part) return;
+    if (!A.part) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[ty][tx * 8 + i] = sum[i];
     __syncthreads();
     for (int c = threadIdx.x; c < 512; c += 256) {
-        const int64_t at = int64_t(blockIdx.x) * 512 + c;
-        if (at < N)
-            part[int64_t(blockIdx.y) * N + at] =
-                (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+        const int64_t at = bx * 512 + c;
+        if (at < A.N)
+            A.part[by * A.N + at] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
     }
 }
 
-// The partial column sums, added in order: 32 columns per block, 8 threads each.
-template <class O>
-__global__ __launch_bounds__(256) void k_sum_columns(int64_t rows, int64_t N, const float* part,
-                                                     O* out) {
-    __shared__ float sums[8][32];
+// The partial column sums, added in order: 32 columns per workgroup.
+template <class T, int THREADS>
+__device__ __forceinline__ void sum_columns(const Sums& A, int64_t id, float* lds) {
+    constexpr int kRows = THREADS / 32;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t n = int64_t(blockIdx.x) * 32 + tx;
+    const int64_t n = id * 32 + tx;
     float s = 0.0f;
-    if (n < N)
+    if (n < A.N) {
 #pragma unroll 8
-        for (int64_t r = ty; r < rows; r += 8) s += part[r * N + n];
-    sums[ty][tx] = s;
+        for (int64_t r = ty; r < A.rows; r += kRows) s += A.part[r * A.N + n];
+    }
+    lds[ty * 32 + tx] = s;
     __syncthreads();
-    if (ty == 0 && n < N) {
-        for (int i = 1; i < 8; ++i) s += sums[i][tx];
-        out[n] = O(s);
+    if (ty == 0 && n < A.N) {
+        for (int i = 1; i < kRows; ++i) s += lds[i * 32 + tx];
+        if (A.wide)
+            static_cast<float*>(A.out)[n] = s;
+        else
+            static_cast<T*>(A.out)[n] = T(s);
     }
 }
 
-// da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements.
 template <class T>
-__global__ __launch_bounds__(256) void k_gate_slope(int64_t M, int64_t F, const T* dh,
-                                                    int64_t lddh, const T* gate, int64_t ldg,
-                                                    const T* up, int64_t ldu, int act, T* da,
-                                                    T* db, int64_t ld) {
-    const int64_t groups = (F + 7) / 8;
-    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (id >= groups * M) return;
-    const int64_t m = id / groups, n = (id - m * groups) * 8;
-    const int valid = F - n >= 8 ? 8 : int(F - n);
-    float d[8], a[8], b[8], oa[8], ob[8];
-    load_row<T, 8>(dh + m * lddh + n, valid, d);
-    load_row<T, 8>(gate + m * ldg + n, valid, a);
-    load_row<T, 8>(up + m * ldu + n, valid, b);
+__global__ __launch_bounds__(256) void k_sum_columns(Sums A) {
+    __shared__ float lds[256];
+    sum_columns<T, 256>(A, blockIdx.x, lds);
+}
+
+// da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; 4
+// elements per thread.
+template <class T>
+__device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id) {
+    const int64_t groups = A.ldz / 4;
+    id = id * 256 + threadIdx.x;
+    if (id >= groups * A.M) return;
+    const int64_t m = id / groups, n = (id - m * groups) * 4;
+    const int valid = A.N - n >= 4 ? 4 : A.N > n ? int(A.N - n) : 0;
+    float d[4], a[4], b[4], oa[4], ob[4];
+    load_row<T, 4>(static_cast<const T*>(A.dy) + m * A.lddy + n, valid, d);
+    load_row<T, 4>(static_cast<const T*>(A.pre) + m * A.ldp + n, valid, a);
+    load_row<T, 4>(static_cast<const T*>(A.up) + m * A.ldu + n, valid, b);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         float value, slope;
-        act_pair(act, a[i], value, slope);
+        act_pair(A.act, a[i], value, slope);
         oa[i] = d[i] * b[i] * slope;
         ob[i] = d[i] * value;
     }
-    store_row<T, 8>(da + m * ld + n, 8, oa);  // zeros in the padding
-    store_row<T, 8>(db + m * ld + n, 8, ob);
+    // zeros in the padding
+    store_row<T, 4>(static_cast<T*>(A.dz) + m * A.ldz + n, 4, oa);
+    store_row<T, 4>(static_cast<T*>(A.dz2) + m * A.ldz + n, 4, ob);
+}
+
+// Rows at any even address to rows on 16 bytes, zeros up to their ends; 8
+// elements per thread.
+__device__ __forceinline__ void repack_block(const Repack& r, int64_t id) {
+    id = id * 256 + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if (i >= r.count) return;
+        const int64_t per = (r.cols[i] + 7) / 8, have = per * r.rows[i];
+        if (id < have) {
+            const int64_t row = id / per, col = (id - row * per) * 8;
+            const uint16_t* p = static_cast<const uint16_t*>(r.from[i]) + row * r.ld[i] + col;
+            u32x4 v;
+            if (col + 8 <= r.cols[i]) {
+                v = reinterpret_cast<const Bytes16*>(p)->v;
+            } else {
+                uint16_t t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] = col + e < r.cols[i] ? p[e] : uint16_t(0);
+                __builtin_memcpy(&v, t, 16);
+            }
+            reinterpret_cast<u32x4*>(r.to[i])[id] = v;
+            return;
+        }
+        id -= have;
+    }
+}
+
+// What a call lays out before its products, in one launch.
+template <class T>
+__global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_blocks, Repack r) {
+    __shared__ float sums[4][512];
+    const int64_t id = blockIdx.x;
+    if (id >= slope_blocks)
+        repack_block(r, id - slope_blocks);
+    else if (A.up)
+        gate_slope_block<T>(A, id);
+    else
+        slope_block<T>(A, id, sums);
 }
 
 }  // namespace layers

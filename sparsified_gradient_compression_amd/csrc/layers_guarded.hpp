@@ -1,0 +1,221 @@
+// layers_guarded.hpp -- products whose operands' rows do not lie on 16 bytes:
+// 64 x 64 outputs per workgroup, any strides, alignment and sizes.
+//
+// Four groups of four waves share the outputs and take the steps of 64 of k in
+// turn, each with two LDS tiles of its own per side: the next one travels
+// through the registers, with loads that are checked against the matrix, while
+// this one is used.  Their sums meet in LDS.
+#pragma once
+
+#include "layers_elem.hpp"
+
+namespace dgc {
+namespace layers {
+
+// One side's pieces of a thread: 2 of the 512 of a tile of 64 rows by 64 k.
+template <class T, bool TR>
+struct Guarded {
+    const T* p[2];   // of the piece in the group's first tile
+    int have[2];     // TR: how many of its 8 columns exist; else 1 if its row does
+    int k_at[2];     // its first k in a tile
+
+    __device__ __forceinline__ void init(const T* base, int64_t ld, int64_t first, int64_t rows,
+                                         int tid) {
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+            const int c = tid + l * 256;
+            if constexpr (TR) {
+                k_at[l] = c >> 3;
+                const int64_t col = first + (c & 7) * 8;
+                have[l] = rows - col >= 8 ? 8 : rows > col ? int(rows - col) : 0;
+                p[l] = base + k_at[l] * ld + col;
+            } else {
+                k_at[l] = (c & 7) * 8;
+                have[l] = first + (c >> 3) < rows;
+                p[l] = base + (first + (c >> 3)) * ld + k_at[l];
+            }
+        }
+    }
+
+    // `ahead` elements behind the first tile, `left` steps of k from there on
+    __device__ __forceinline__ void load(int64_t ahead, int64_t left, u32x4* v) const {
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+            int n = have[l];
+            if constexpr (TR)
+                n = k_at[l] < left ? n : 0;
+            else
+                n = !n || k_at[l] >= left ? 0 : left - k_at[l] >= 8 ? 8 : int(left - k_at[l]);
+            const T* q = p[l] + ahead;
+            v[l] = u32x4{0, 0, 0, 0};
+            if (n == 8) {
+                v[l] = reinterpret_cast<const Bytes16*>(q)->v;
+            } else if (n > 0) {
+                uint16_t t[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    t[e] = e < n ? reinterpret_cast<const uint16_t*>(q)[e] : uint16_t(0);
+                __builtin_memcpy(&v[l], t, 16);
+            }
+        }
+    }
+
+    template <int NT, bool NSIDE>
+    static __device__ __forceinline__ void store(T* lds, int tid, const u32x4* v) {
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+            const int c = tid + l * 256;
+            *reinterpret_cast<u32x4*>(lds + piece_at<64, NT, TR, NSIDE>(c >> 3, c & 7)) = v[l];
+        }
+    }
+};
+
+constexpr int kGuardedGroups = 4;
+constexpr int kGuardedSide = 64 * kStep;
+
+template <class T, int FORM>
+__device__ __forceinline__ void guarded_tile(const TileArgs& A, int64_t id, T* smem) {
+    constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
+    constexpr int KG = kGuardedGroups, MT = 2, NTW = 2, NT = PAIR ? 1 : 2;
+    typedef typename Arith<T>::v8 v8;
+    const int tid = threadIdx.x & 255, lane = threadIdx.x & 63;
+    const int group = threadIdx.x >> 8, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    T* const sa = smem + group * 4 * kGuardedSide;  // two tiles of a, two of b
+    T* const sb = sa + 2 * kGuardedSide;
+
+    const int64_t tiles = A.mt * A.nt;
+    const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
+    const int split = int(id / per_split);
+    id -= split * per_split;
+    const int z = FORM == kDw ? int(id / tiles) : 0;
+    id -= z * tiles;
+    int64_t tm, tn;
+    place(id, A.mt, A.nt, tm, tn);
+    const int64_t m0 = tm * 64, n0 = tn * (PAIR ? 32 : 64);
+
+    const int64_t ksteps = (A.K + kStep - 1) / kStep;
+    const int64_t total = ksteps * (FORM == kDx ? A.parts : 1);
+    const int64_t first = split * A.per;
+    const int64_t last = first + A.per < total ? first + A.per : total;
+    const int64_t rounds = (last - first + KG - 1) / KG;
+
+    Frags<T, ATR, MT, false, 64> fa;
+    Frags<T, BTR, NT, true, 64> fb;
+    fa.init(lane, wm * 32);
+    fb.init(lane, wn * NT * 16);
+
+    // both terms of kDx have pieces of their own; a pair's b is two half tiles
+    Guarded<T, ATR> ga[FORM == kDx ? 2 : 1];
+    Guarded<T, BTR> gb[FORM == kDx ? 2 : 1];
+#pragma unroll
+    for (int w = 0; w < (FORM == kDx ? 2 : 1); ++w) {
+        if (w >= A.parts) break;
+        ga[w].init(static_cast<const T*>(A.a[FORM == kDw ? z : w]), A.lda[FORM == kDw ? z : w],
+                   m0, A.M, tid);
+        if constexpr (!PAIR)
+            gb[w].init(static_cast<const T*>(A.b[w]), A.ldb[w], n0, A.N, tid);
+    }
+    if constexpr (PAIR) {
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {  // load l is product l's 32 rows
+            const int row = tid >> 3;
+            gb[0].k_at[l] = (tid & 7) * 8;
+            gb[0].have[l] = n0 + row < A.N;
+            gb[0].p[l] = static_cast<const T*>(A.b[l]) + (n0 + row) * A.ldb[l] + gb[0].k_at[l];
+        }
+    }
+
+    u32x4 ra[2], rb[2];
+    auto fetch = [&](int64_t r) {
+        const int64_t t = first + r * KG + group;
+        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
+        const int64_t k0 = (t - seg * ksteps) * kStep;
+        const int64_t left = t < last ? A.K - k0 : 0;
+        if (FORM == kDx && seg) {
+            ga[FORM == kDx].load(k0, left, ra);
+            gb[FORM == kDx].load(k0 * A.ldb[1], left, rb);
+        } else {
+            ga[0].load(ATR ? k0 * A.lda[FORM == kDw ? z : 0] : k0, left, ra);
+            gb[0].load(BTR ? k0 * A.ldb[0] : k0, left, rb);
+        }
+    };
+    auto place_lds = [&](int buf) {
+        Guarded<T, ATR>::template store<MT, false>(sa + buf * kGuardedSide, tid, ra);
+        // a pair's halves are dealt to the matrix tiles within their 32 rows
+        Guarded<T, BTR>::template store<NT, true>(sb + buf * kGuardedSide, tid, rb);
+    };
+
+    f32x4 acc[MT][NTW];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    if (rounds > 0) {
+        fetch(0);
+        place_lds(0);
+    }
+    for (int64_t r = 0; r < rounds; ++r) {
+        const int buf = int(r & 1);
+        // tile r is in LDS, and nobody reads the other buffer any more
+        __syncthreads();
+        if (r + 1 < rounds) fetch(r + 1);
+        const T* la = sa + buf * kGuardedSide;
+        const T* lb = sb + buf * kGuardedSide;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            v8 va[MT], vb[NTW];
+#pragma unroll
+            for (int j = 0; j < NTW; ++j)
+                vb[j] = fb.get(lb + (PAIR ? j * 32 * kStep : 0), PAIR ? 0 : j, s);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) va[i] = fa.get(la, i, s);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NTW; ++j) acc[i][j] = Arith<T>::mma(vb[j], va[i], acc[i][j]);
+        }
+        if (r + 1 < rounds) place_lds(buf ^ 1);
+    }
+    __syncthreads();
+    constexpr int kOwn = MT * NTW * 256;
+    float* out = reinterpret_cast<float*>(smem) + wave * kOwn;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NTW; ++j)
+            put_tile<NTW, NT, BTR>(out + group * 4 * kOwn, mt, j / NT * NT * 16, j % NT, lane,
+                                   acc[mt][j]);
+    __syncthreads();
+    const int64_t mw = m0 + wm * 32, nw = n0 + wn * NT * 16;
+    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + 16, lane, out, group, KG,
+                               4 * kOwn);
+}
+
+constexpr int kGuardedThreads = 256 * kGuardedGroups;
+constexpr int kGuardedLds = kGuardedGroups * 4 * kGuardedSide;
+
+template <class T, int FORM>
+__global__ __launch_bounds__(kGuardedThreads) void k_guarded(TileArgs A) {
+    __shared__ __align__(16) T smem[kGuardedLds];
+    guarded_tile<T, FORM>(A, blockIdx.x, smem);
+}
+
+// Both gradients of a layer in one launch, and the column sums' last step.
+template <class T>
+__global__ __launch_bounds__(kGuardedThreads) void k_guarded_both(TileArgs dx, TileArgs dw,
+                                                                  int64_t dx_blocks,
+                                                                  int64_t dw_blocks, Sums sums) {
+    __shared__ __align__(16) T smem[kGuardedLds];
+    const int64_t id = blockIdx.x;
+    if (id < dx_blocks)
+        guarded_tile<T, kDx>(dx, id, smem);
+    else if (id < dx_blocks + dw_blocks)
+        guarded_tile<T, kDw>(dw, id - dx_blocks, smem);
+    else
+        sum_columns<T, kGuardedThreads>(sums, id - dx_blocks - dw_blocks,
+                                        reinterpret_cast<float*>(smem));
+}
+
+}  // namespace layers
+}  // namespace dgc

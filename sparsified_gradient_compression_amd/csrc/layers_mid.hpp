@@ -9,12 +9,35 @@
 #pragma once
 
 #include "layers_direct.hpp"
+#include "layers_elem.hpp"
 
 namespace dgc {
 namespace layers {
 
-template <class T, int FORM, int BM, int BN, int WM, int WN, int KG, int S>
-__global__ __launch_bounds__(WM* WN* KG * 64) void k_mid(TileArgs A) {
+// Shape of a workgroup: BM x BN outputs, KG groups of WM x WN waves, rings of
+// S tiles.
+template <int BM_, int BN_, int WM_, int WN_, int KG_, int S_>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KG = KG_, S = S_;
+    static constexpr int kThreads = WM * WN * KG * 64;
+    static constexpr int kRing = KG * (BM + BN) * kStep;  // elements of a ring's tile
+};
+typedef Shape<32, 64, 2, 2, 4, 3> Shape32;
+typedef Shape<64, 64, 2, 2, 2, 4> Shape64;
+typedef Shape<128, 128, 2, 4, 1, 4> Shape128;
+typedef Shape<128, 128, 2, 4, 1, 2> ShapePair;
+
+// The ring's tiles are arrays of their own, so that a read of one is known
+// not to wait for loads into another.
+#define DGC_RING(T, SH)                                                        \
+    __shared__ __align__(16) T s0[SH::kRing], s1[SH::kRing];                   \
+    __shared__ __align__(16) T s2[SH::S > 2 ? SH::kRing : 8];                  \
+    __shared__ __align__(16) T s3[SH::S > 3 ? SH::kRing : 8]
+
+template <class T, int FORM, class SH>
+__device__ __forceinline__ void mid_tile(const TileArgs& A, int64_t id, T* s0, T* s1, T* s2,
+                                         T* s3) {
+    constexpr int BM = SH::BM, BN = SH::BN, WM = SH::WM, WN = SH::WN, KG = SH::KG, S = SH::S;
     constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
     constexpr int W = WM * WN;
     constexpr int MT = BM / WM / 16, NTW = BN / WN / 16;  // 16 x 16 tiles of a wave
@@ -22,15 +45,12 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void k_mid(TileArgs A) {
     constexpr int RB = PAIR ? BN / 2 : BN;                // rows of a region of b
     constexpr int kTile = (BM + BN) * kStep;              // elements of both sides' tiles
     typedef typename Arith<T>::v8 v8;
-    __shared__ __align__(16) T s0[KG * kTile], s1[KG * kTile];
-    __shared__ __align__(16) T s2[S > 2 ? KG * kTile : 8], s3[S > 3 ? KG * kTile : 8];
     const int lane = threadIdx.x & 63;
     const int all = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wave = all % W, group = all / W;
     const int wm = wave / WN, wn = wave % WN;
 
     const int64_t tiles = A.mt * A.nt;
-    int64_t id = blockIdx.x;
     const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
     const int split = int(id / per_split);
     id -= split * per_split;
@@ -136,6 +156,28 @@ __global__ __launch_bounds__(WM* WN* KG * 64) void k_mid(TileArgs A) {
     const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
     put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out, group, KG,
                                kGroupStride);
+}
+
+template <class T, int FORM, class SH>
+__global__ __launch_bounds__(SH::kThreads) void k_mid(TileArgs A) {
+    DGC_RING(T, SH);
+    mid_tile<T, FORM, SH>(A, blockIdx.x, s0, s1, s2, s3);
+}
+
+// Both gradients of a layer in one launch, and the column sums' last step.
+template <class T, class SH>
+__global__ __launch_bounds__(SH::kThreads) void k_mid_both(TileArgs dx, TileArgs dw,
+                                                           int64_t dx_blocks, int64_t dw_blocks,
+                                                           Sums sums) {
+    DGC_RING(T, SH);
+    const int64_t id = blockIdx.x;
+    if (id < dx_blocks)
+        mid_tile<T, kDx, SH>(dx, id, s0, s1, s2, s3);
+    else if (id < dx_blocks + dw_blocks)
+        mid_tile<T, kDw, SH>(dw, id - dx_blocks, s0, s1, s2, s3);
+    else
+        sum_columns<T, SH::kThreads>(sums, id - dx_blocks - dw_blocks,
+                                     reinterpret_cast<float*>(s0));
 }
 
 }  // namespace layers

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(512) void k_thin(TileArgs A) {
             v2[4 * q + e] = t[P - 1][e];
         }
     }
-    finish_row<T, PAIR, 8>(A.fin, 0, r, n0 + c * 8, A.N, v, v2);
+    finish_one<T, PAIR, 8>(A.fin, 0, r, n0 + c * 8, A.N, v, v2);
 }
 
 }  // namespace layers

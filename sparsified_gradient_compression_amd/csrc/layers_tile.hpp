@@ -51,13 +51,40 @@ constexpr int kStep = 64;  // k per LDS tile
 
 // ------------------------------------------------------------ activations
 
+// All are z times a share of it that lies between 0 and 1: 1 / (1 + exp(-q))
+// or the normal distribution's integral.  The hardware's exp2 and reciprocal
+// are off by a step or two of binary32, and the integral by 8e-8 (Abramowitz
+// and Stegun, Handbook of Mathematical Functions, 7.1.26), far less than a
+// step of the 16-bit types; a finish takes a dozen instructions per element
+// instead of the fifty of the correctly rounded functions.
+
+__device__ __forceinline__ float sigmoid(float q) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(q * -1.44269504f));
+}
+
+// The integral of the normal density up to z, and exp(-z^2 / 2).
+__device__ __forceinline__ float normal_share(float z, float& e) {
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    e = __builtin_amdgcn_exp2f(x * x * -1.44269504f);
+    const float p =
+        t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float tail = 0.5f * p * e;
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// gelu_tanh: (1 + tanh(q)) / 2 = sigmoid(2 q)
+__device__ __forceinline__ float tanh_twice(float z) {
+    return 1.59576912f * (z + 0.044715f * z * z * z);
+}
+
 __device__ __forceinline__ float act_value(int act, float z) {
+    float e;
     switch (act) {
         case DGC_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-        case DGC_ACT_SILU: return z / (1.0f + expf(-z));
-        case DGC_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-        case DGC_ACT_GELU_TANH:
-            return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+        case DGC_ACT_SILU: return z * sigmoid(z);
+        case DGC_ACT_GELU: return z * normal_share(z, e);
+        case DGC_ACT_GELU_TANH: return z * sigmoid(tanh_twice(z));
         default: return z;
     }
 }
@@ -70,22 +97,22 @@ __device__ __forceinline__ void act_pair(int act, float z, float& value, float& 
             slope = z > 0.0f ? 1.0f : 0.0f;
             break;
         case DGC_ACT_SILU: {
-            const float s = 1.0f / (1.0f + expf(-z));
-            value = z * s;
-            slope = s * (1.0f + z * (1.0f - s));
+            const float p = sigmoid(z);
+            value = z * p;
+            slope = p * (1.0f + z * (1.0f - p));
             break;
         }
         case DGC_ACT_GELU: {
-            const float c = 0.5f * (1.0f + erff(z * 0.70710678f));
-            value = z * c;
-            slope = c + z * 0.39894228f * expf(-0.5f * z * z);
+            float e;
+            const float p = normal_share(z, e);
+            value = z * p;
+            slope = p + z * 0.39894228f * e;
             break;
         }
         case DGC_ACT_GELU_TANH: {
-            const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-            value = 0.5f * z * (1.0f + t);
-            slope = 0.5f * (1.0f + t) +
-                    0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+            const float p = sigmoid(tanh_twice(z));
+            value = z * p;
+            slope = p + value * (1.0f - p) * 1.59576912f * (1.0f + 0.134145f * z * z);
             break;
         }
         default: value = z; slope = 1.0f;
@@ -156,13 +183,13 @@ __device__ __forceinline__ void store_wide(float* p, int valid, const float* v) 
     }
 }
 
-// Finish C consecutive elements (m, n..n+C-1) of output `z` of a product.
-// v holds the 32-bit sums, v2 the second product's (kPair).
+// Finish C consecutive elements (m, n..n+C-1) of output `z` of a product, of
+// which `valid` exist.  v holds the 32-bit sums, v2 the second product's
+// (kPair); bias and residual are used if the finish has them.
 template <class T, bool PAIR, int C>
 __device__ __forceinline__ void finish_row(const Finish& f, int z, int64_t m, int64_t n,
-                                           int64_t N, float* v, float* v2) {
-    const int valid = N - n < C ? int(N - n) : C;
-    if (valid <= 0) return;
+                                           int valid, float* v, float* v2, const float* bias,
+                                           const float* residual) {
     if constexpr (PAIR) {
         if (f.pre[0]) store_row<T, C>(static_cast<T*>(f.pre[0]) + m * f.ldp[0] + n, valid, v);
         if (f.pre[1]) store_row<T, C>(static_cast<T*>(f.pre[1]) + m * f.ldp[1] + n, valid, v2);
@@ -172,11 +199,9 @@ __device__ __forceinline__ void finish_row(const Finish& f, int z, int64_t m, in
     } else if (f.wide) {
         store_wide<C>(static_cast<float*>(f.out[z]) + m * (z ? f.ldo2 : f.ldo) + n, valid, v);
     } else {
-        float t[C];
         if (f.bias) {
-            load_row<T, C>(static_cast<const T*>(f.bias) + n, valid, t);
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] += t[i];
+            for (int i = 0; i < C; ++i) v[i] += bias[i];
         }
         if (f.pre[0]) store_row<T, C>(static_cast<T*>(f.pre[0]) + m * f.ldp[0] + n, valid, v);
         if (f.act != DGC_ACT_NONE) {
@@ -184,12 +209,24 @@ __device__ __forceinline__ void finish_row(const Finish& f, int z, int64_t m, in
             for (int i = 0; i < C; ++i) v[i] = act_value(f.act, v[i]);
         }
         if (f.residual) {
-            load_row<T, C>(static_cast<const T*>(f.residual) + m * f.ldr + n, valid, t);
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] += t[i];
+            for (int i = 0; i < C; ++i) v[i] += residual[i];
         }
         store_row<T, C>(static_cast<T*>(f.out[z]) + m * (z ? f.ldo2 : f.ldo) + n, valid, v);
     }
+}
+
+// The same with the bias and residual read here.
+template <class T, bool PAIR, int C>
+__device__ __forceinline__ void finish_one(const Finish& f, int z, int64_t m, int64_t n,
+                                           int64_t N, float* v, float* v2) {
+    const int valid = N - n < C ? int(N - n) : C;
+    if (valid <= 0) return;
+    float bias[C], residual[C];
+    if (!PAIR && f.bias) load_row<T, C>(static_cast<const T*>(f.bias) + n, valid, bias);
+    if (!PAIR && f.residual)
+        load_row<T, C>(static_cast<const T*>(f.residual) + m * f.ldr + n, valid, residual);
+    finish_row<T, PAIR, C>(f, z, m, n, valid, v, v2, bias, residual);
 }
 
 // ------------------------------------------------------------- LDS layouts
@@ -224,8 +261,7 @@ __device__ __forceinline__ int k_key(int k) {
     return ((k & 3) | (((k >> 3) & 3) << 2)) & (R / 16 - 1);
 }
 
-// Element offset of the 16-byte piece with index c of a tile's load.
-//   TR false: row c / 8, piece c % 8;  TR true: k c / (R/8), piece c % (R/8)
+// Element offset of 16-byte piece `piece` of row (TR: step of k) `row`.
 template <int R, int NT, bool TR, bool NSIDE>
 __device__ __forceinline__ int piece_at(int row, int piece) {
     if constexpr (TR)
@@ -234,25 +270,46 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
         return row * kStep + (piece ^ row_key<NT, NSIDE>(row)) * 8;
 }
 
-// Eight elements of row `row` from column `col` of a matrix with `rows` rows
-// and `cols` columns; what lies outside reads as zero.
-template <class T>
-__device__ __forceinline__ u32x4 guarded(const T* p, int64_t ld, int64_t row, int64_t col,
-                                         int64_t rows, int64_t cols) {
-    u32x4 r = {0, 0, 0, 0};
-    if (row >= rows || col >= cols) return r;
-    const T* q = p + row * ld + col;
-    if (col + 8 <= cols) return reinterpret_cast<const Bytes16*>(q)->v;
-    uint16_t t[8];
+// Where a lane's fragments lie in a region, and their reads.
+template <class T, bool TR, int NT, bool NSIDE, int R>
+struct Frags {
+    typedef typename Arith<T>::v8 v8;
+    int frag[TR ? NT : 2];
+
+    // base: the wave's first row (column) in the region
+    __device__ __forceinline__ void init(int lane, int base) {
+        const int i = lane & 15, g = lane >> 4;
+        if constexpr (TR) {
+            const int kk = g * 8 + (i >> 2);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        t[i] = col + i < cols ? reinterpret_cast<const uint16_t*>(q)[i] : uint16_t(0);
-    __builtin_memcpy(&r, t, 16);
-    return r;
-}
+            for (int j = 0; j < NT; ++j)
+                frag[j] = kk * R + ((((base >> 4) + j) ^ k_key<R>(kk)) << 4) + (i & 3) * 4;
+        } else {
+            const int fr = base + (NSIDE ? n_row<NT>(i, 0) : i);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                frag[s] = fr * kStep + (((s * 4 + g) ^ row_key<NT, NSIDE>(fr)) << 3);
+        }
+    }
+
+    // Fragment j, steps 32 s .. 32 s + 31, of a region.
+    __device__ __forceinline__ v8 get(const T* lds, int j, int s) const {
+        if constexpr (TR) {
+            union { s16x4 h[2]; v8 v; } u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (DGC_LDS s16x4*)(const_cast<T*>(lds + frag[j] + s * 32 * R + h * 4 * R)));
+            return u.v;
+        } else {
+            return *reinterpret_cast<const v8*>(lds + frag[s] + j * (NSIDE ? 4 : 16) * kStep);
+        }
+    }
+};
 
 // --------------------------------------------------------------- the tiles
 
+// One product's tiles.
 struct TileArgs {
     const void* a[2];
     const void* b[2];
@@ -280,33 +337,6 @@ __device__ __forceinline__ void place(int64_t id, int64_t mt, int64_t nt, int64_
     tn = in / high;
 }
 
-// Fragment reads of one wave from a tile in LDS.
-template <class T, int R, int NT, bool TR, bool NSIDE>
-struct Frag {
-    typedef typename Arith<T>::v8 v8;
-    // tile j of 16 rows (or columns) from `base`, k from 32 * s
-    static __device__ __forceinline__ v8 get(const T* lds, int base, int j, int s, int lane) {
-        const int i = lane & 15, g = lane >> 4;
-        if constexpr (TR) {
-            const int k = s * 32 + g * 8 + (i >> 2);
-            const int blk = (base >> 4) + j;
-            union { s16x4 h[2]; v8 v; } u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const T* p = lds + (k + 4 * h) * R + ((blk ^ k_key<R>(k + 4 * h)) << 4) +
-                             (i & 3) * 4;
-                u.h[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (DGC_LDS s16x4*)(const_cast<T*>(p)));
-            }
-            return u.v;
-        } else {
-            const int r = base + (NSIDE ? n_row<NT>(i, j) : j * 16 + i);
-            return *reinterpret_cast<const v8*>(
-                lds + r * kStep + (((s * 4 + g) ^ row_key<NT, NSIDE>(r)) << 3));
-        }
-    }
-};
-
 // A wave's outputs leave through its own LDS (MT * 16 rows of NTW * 16
 // columns in binary32, NTW = 2 or 4): what finishes an element is then one
 // short loop whose lanes hold 8 consecutive columns each, instead of the
@@ -323,36 +353,54 @@ __device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, in
     constexpr int W = NTW * 16;                     // columns in LDS
     constexpr int kLanes = PAIR ? W / 16 : W / 8;   // lanes per row
     constexpr int kRows = 64 / kLanes;
+    constexpr int kAhead = 4;  // rows whose loads are under way together
     const int c = lane % kLanes;
     const int64_t n = c * 8 < W / 2 ? n0 + c * 8 : n1 + c * 8 - W / 2;
+    const int valid = A.N - n < 8 ? int(A.N - n) : 8;
+    if (valid <= 0) return;
+    const Finish& f = A.fin;
+    float bias[8];
+    if (!PAIR && f.bias) load_row<T, 8>(static_cast<const T*>(f.bias) + n, valid, bias);
+    const int rows = A.M - m0 < MT * 16 ? int(A.M - m0) : MT * 16;
+    const int step = kRows * groups;
 #pragma unroll 1
-    for (int r = group * kRows + lane / kLanes; r < MT * 16; r += kRows * groups) {
-        const int64_t m = m0 + r;
-        if (m >= A.M) break;
-        float v[8], v2[8];
-        const int key = (r & (W / 8 - 1)) << 1;
+    for (int first = group * kRows + lane / kLanes; first < rows; first += kAhead * step) {
+        float residual[kAhead][8];
+        if (!PAIR && f.residual) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float* p = lds + r * W + ((2 * c + q) ^ key) * 4;
-            const float* p2 = lds + r * W + ((2 * c + q + W / 8) ^ key) * 4;
-            f32x4 t = *reinterpret_cast<const f32x4*>(p), t2 = {0, 0, 0, 0};
-            if (PAIR) t2 = *reinterpret_cast<const f32x4*>(p2);
-            for (int w = 1; w < groups; ++w) {
-                t += *reinterpret_cast<const f32x4*>(p + w * stride);
-                if (PAIR) t2 += *reinterpret_cast<const f32x4*>(p2 + w * stride);
-            }
-            *reinterpret_cast<f32x4*>(v + 4 * q) = t;
-            *reinterpret_cast<f32x4*>(v2 + 4 * q) = t2;
+            for (int u = 0; u < kAhead; ++u)
+                if (first + u * step < rows)
+                    load_row<T, 8>(static_cast<const T*>(f.residual) +
+                                       (m0 + first + u * step) * f.ldr + n, valid, residual[u]);
         }
-        const int valid = A.N - n < 8 ? int(A.N - n) : 8;
-        if (valid <= 0) continue;
-        if (A.part) {
-            const int planes = PAIR ? 2 : A.outs;
-            float* o = A.part + (((int64_t(split) * planes + z) * A.M + m) * A.N + n);
-            store_wide<8>(o, valid, v);
-            if (PAIR) store_wide<8>(o + A.M * A.N, valid, v2);
-        } else {
-            finish_row<T, PAIR, 8>(A.fin, z, m, n, A.N, v, v2);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = first + u * step;
+            if (r >= rows) break;
+            float v[8], v2[8];
+            const int key = (r & (W / 8 - 1)) << 1;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float* p = lds + r * W + ((2 * c + q) ^ key) * 4;
+                const float* p2 = lds + r * W + ((2 * c + q + W / 8) ^ key) * 4;
+                f32x4 t = *reinterpret_cast<const f32x4*>(p), t2 = {0, 0, 0, 0};
+                if (PAIR) t2 = *reinterpret_cast<const f32x4*>(p2);
+                for (int w = 1; w < groups; ++w) {
+                    t += *reinterpret_cast<const f32x4*>(p + w * stride);
+                    if (PAIR) t2 += *reinterpret_cast<const f32x4*>(p2 + w * stride);
+                }
+                *reinterpret_cast<f32x4*>(v + 4 * q) = t;
+                *reinterpret_cast<f32x4*>(v2 + 4 * q) = t2;
+            }
+            const int64_t m = m0 + r;
+            if (A.part) {
+                const int planes = PAIR ? 2 : A.outs;
+                float* o = A.part + (((int64_t(split) * planes + z) * A.M + m) * A.N + n);
+                store_wide<8>(o, valid, v);
+                if (PAIR) store_wide<8>(o + A.M * A.N, valid, v2);
+            } else {
+                finish_row<T, PAIR, 8>(f, z, m, n, valid, v, v2, bias, residual[u]);
+            }
         }
     }
 }
@@ -365,129 +413,6 @@ __device__ __forceinline__ void put_tile(float* lds, int mt, int col, int j, int
     const int r = mt * 16 + (lane & 15), g = lane >> 4;
     const int c4 = col / 4 + (TR ? j * 4 + g : g * NT + j);
     *reinterpret_cast<f32x4*>(lds + r * W + (c4 ^ ((r & (W / 8 - 1)) << 1)) * 4) = v;
-}
-
-// BM x BN outputs per workgroup of WM x WN waves.  LDS holds two tiles of
-// each side; the next one travels through registers while this one is used.
-template <class T, int FORM, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64) void k_tile(TileArgs A) {
-    constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
-    constexpr int kThreads = WM * WN * 64;
-    constexpr int MT = BM / WM / 16, NTW = BN / WN / 16;  // 16 x 16 tiles of a wave
-    constexpr int NT = PAIR ? NTW / 2 : NTW;              // ... of one product
-    constexpr int kPiecesA = BM * 8 / kThreads, kPiecesB = BN * 8 / kThreads;
-    typedef typename Arith<T>::v8 v8;
-    __shared__ __align__(16) T smem[2 * (BM + BN) * kStep];
-    T (&sa)[2][BM * kStep] = *reinterpret_cast<T (*)[2][BM * kStep]>(smem);
-    T (&sb)[2][BN * kStep] = *reinterpret_cast<T (*)[2][BN * kStep]>(smem + 2 * BM * kStep);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave / WN, wn = wave % WN;
-
-    const int64_t tiles = A.mt * A.nt;
-    int64_t id = blockIdx.x;
-    const int split = int(id / (tiles * (FORM == kDw ? A.parts : 1)));
-    id -= split * (tiles * (FORM == kDw ? A.parts : 1));
-    const int z = FORM == kDw ? int(id / tiles) : 0;
-    id -= z * tiles;
-    int64_t tm, tn;
-    place(id, A.mt, A.nt, tm, tn);
-    const int64_t m0 = tm * BM, n0 = tn * (PAIR ? BN / 2 : BN);
-
-    const int64_t ksteps = (A.K + kStep - 1) / kStep;
-    const int64_t total = ksteps * (FORM == kDx ? A.parts : 1);
-    const int64_t first = split * A.per;
-    const int64_t last = first + A.per < total ? first + A.per : total;
-
-    u32x4 ra[kPiecesA], rb[kPiecesB];
-    auto fetch = [&](int64_t t) {
-        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
-        const int64_t k0 = (t - seg * ksteps) * kStep;
-        const T* pa = static_cast<const T*>(A.a[FORM == kDw ? z : seg]);
-        const int64_t lda = A.lda[FORM == kDw ? z : seg];
-#pragma unroll
-        for (int i = 0; i < kPiecesA; ++i) {
-            const int c = tid + i * kThreads;
-            ra[i] = ATR ? guarded(pa, lda, k0 + c / (BM / 8), m0 + c % (BM / 8) * 8, A.K, A.M)
-                        : guarded(pa, lda, m0 + c / 8, k0 + c % 8 * 8, A.M, A.K);
-        }
-#pragma unroll
-        for (int i = 0; i < kPiecesB; ++i) {
-            const int c = tid + i * kThreads;
-            if constexpr (PAIR) {  // rows of the first half are the gate's
-                const int r = c / 8, w = r >= BN / 2;
-                rb[i] = guarded(static_cast<const T*>(A.b[w]), A.ldb[w], n0 + r - w * (BN / 2),
-                                k0 + c % 8 * 8, A.N, A.K);
-            } else {
-                const T* pb = static_cast<const T*>(A.b[seg]);
-                rb[i] = BTR ? guarded(pb, A.ldb[seg], k0 + c / (BN / 8), n0 + c % (BN / 8) * 8,
-                                      A.K, A.N)
-                            : guarded(pb, A.ldb[seg], n0 + c / 8, k0 + c % 8 * 8, A.N, A.K);
-            }
-        }
-    };
-    auto place_lds = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < kPiecesA; ++i) {
-            const int c = tid + i * kThreads;
-            constexpr int kPer = ATR ? BM / 8 : 8;
-            *reinterpret_cast<u32x4*>(&sa[buf][piece_at<BM, 4, ATR, false>(c / kPer, c % kPer)]) =
-                ra[i];
-        }
-#pragma unroll
-        for (int i = 0; i < kPiecesB; ++i) {
-            const int c = tid + i * kThreads;
-            constexpr int kPer = BTR ? BN / 8 : 8;
-            *reinterpret_cast<u32x4*>(&sb[buf][piece_at<BN, NT, BTR, true>(c / kPer, c % kPer)]) =
-                rb[i];
-        }
-    };
-
-    f32x4 acc[MT][NTW];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NTW; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    if (first < last) {
-        fetch(first);
-        place_lds(0);
-    }
-    for (int64_t t = first; t < last; ++t) {
-        const int buf = int(t - first) & 1;
-        // tile t is in LDS, and nobody reads the other buffer any more
-        __syncthreads();
-        if (t + 1 < last) fetch(t + 1);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            v8 fb[NTW], fa[MT];
-#pragma unroll
-            for (int j = 0; j < NTW; ++j) {
-                const int base = PAIR ? (j >= NT ? BN / 2 : 0) + wn * NT * 16 : wn * NTW * 16;
-                fb[j] = Frag<T, BN, NT, BTR, true>::get(sb[buf], base, PAIR ? j % NT : j, s, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                fa[i] = Frag<T, BM, 4, ATR, false>::get(sa[buf], wm * MT * 16, i, s, lane);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NTW; ++j) acc[i][j] = Arith<T>::mma(fb[j], fa[i], acc[i][j]);
-        }
-        if (t + 1 < last) place_lds(buf ^ 1);
-    }
-
-    __syncthreads();
-    constexpr int kOwn = MT * NTW * 256;  // outputs of a wave
-    static_assert(WM * WN * kOwn * 4 <= int(sizeof(sa) + sizeof(sb)), "outputs fit the tiles' LDS");
-    float* out = reinterpret_cast<float*>(smem) + wave * kOwn;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < NTW; ++j)
-            put_tile<NTW, NT, BTR>(out, mt, j / NT * NT * 16, j % NT, lane, acc[mt][j]);
-    const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
-    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out, 0, 1,
-                               0);
 }
 
 // The sums of all splits, added in their order, then finished.  One thread
@@ -519,7 +444,7 @@ __global__ __launch_bounds__(256) void k_join(TileArgs A) {
             }
         }
     }
-    finish_row<T, PAIR, 4>(A.fin, z, m, n, A.N, v, v2);
+    finish_one<T, PAIR, 4>(A.fin, z, m, n, A.N, v, v2);
 }
 
 }  // namespace layers

@@ -135,10 +135,12 @@ def run_ffn_backward(m, d, f, dtype, act, wide, pad=0, shift=0, seed=4):
     mk.untouched()
 
 
-# m, n, k: empty, single, inside a tile, its edges, several tiles, long sums, many rows
+# m, n, k: empty, single, inside a tile, its edges, several tiles, few outputs of long sums (over k, n and m),
+# odd sizes whose operands are laid out anew
 SIZES = [(0, 5, 7), (5, 0, 7), (5, 7, 0), (1, 1, 1), (1, 64, 2048), (2, 1000, 333), (3, 5, 7), (16, 65, 129),
          (17, 130, 65), (33, 96, 4100), (64, 64, 64), (65, 200, 72), (128, 128, 128), (129, 257, 100),
-         (255, 256, 320), (257, 513, 64), (300, 72, 1031), (1000, 264, 520), (1025, 2056, 136), (2000, 2500, 70)]
+         (255, 256, 320), (257, 513, 64), (300, 72, 1031), (1000, 264, 520), (1025, 2056, 136), (2000, 2500, 70),
+         (1800, 1608, 1000), (70, 72, 8200), (70, 8200, 72), (8200, 70, 72), (40, 8201, 70), (515, 1001, 2003)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
