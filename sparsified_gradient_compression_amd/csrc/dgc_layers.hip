@@ -22,26 +22,42 @@ size_t round_up(size_t x) { return (x + kPad - 1) / kPad * kPad; }
 
 namespace {
 
-// What a kernel takes, measured on bf16 products of 64 to 8192 rows and
-// columns: a start, and so many microseconds per step of 64 of k for a round
-// of at most `round` workgroups, of which `light` or fewer have a compute unit
-// each to themselves.
-//   e.g. 333 x 1152 x 3456: kMid32 11.6, kMid64 13.6, kMid128 26.9 us;
-//   777 x 1000 x 2048: kMid32 14.5, kMid64 9.1, kMid128 17.0;
-//   2048 x 2048 x 2048: kMid64 34.3, kMid128 21.3, kPair128 28.5, kBig 46.5;
-//   2048 x 4096 x 2048: kMid128 41.5, kPair128 36.0, kBig 48.1;
-//   4096 x 4096 x 4096: kPair128 149, kBig 99
+// What a round of workgroups takes: a start (the first loads, the outputs'
+// way out) and so many microseconds per step of 64 of k, for `round`
+// workgroups at once and for `light` or fewer of them.  Measured on bf16
+// products of 64 to 8192 rows and columns, in microseconds:
+//                        kMid32 kMid64 kLight kMid128 kPair128 kBig  kGuarded
+//   64 x 704, k 704         5.6    5.5     6.4     8.0      8.6    19       7.2
+//   1024 x 1024, k 64        10    5.0     4.2     6.2      5.8    15       6.4
+//   1024 x 1024, k 1024      12    6.9     8.5      11       12    27       9.2
+//   2048 x 2048, k 2048      57     35      26      20       28    42        47
+//   4096 x 4096, k 64       120     51      18      20       14    17        67
+//   4096 x 4096, k 2048     221    132              75       66    53
+// Off 16 bytes a step of kGuarded takes half as long again.
 struct Cost {
     int tile;
     int64_t round, light;
-    double start, full_step, light_step;
+    double start, step, light_start, light_step;
 };
-constexpr Cost kCosts[] = {{kGuarded, 256, 256, 3.0, 0.22, 0.22}, {kMid32, 256, 256, 2.5, 0.17, 0.17},
-                           {kMid64, 256, 256, 2.5, 0.24, 0.24},   {kMid128, 256, 256, 3.0, 0.62, 0.62},
-                           {kPair128, 512, 256, 3.0, 1.08, 0.80}, {kBig, 256, 256, 5.0, 1.50, 1.50}};
+constexpr Cost kCosts[] = {
+    {kGuarded, 256, 256, 2.6, 0.40, 2.6, 0.40}, {kMid32, 256, 256, 3.4, 0.13, 3.4, 0.13},
+    {kMid64, 256, 256, 2.2, 0.21, 2.2, 0.21},   {kMid128, 256, 256, 3.8, 0.45, 3.8, 0.45},
+    {kPair128, 512, 256, 5.0, 0.84, 3.5, 0.70}, {kBig, 256, 128, 11.0, 1.28, 9.0, 1.05},
+    {kLight, 1280, 256, 4.0, 0.72, 2.0, 0.26}};
+constexpr double kLaunchUs = 2.5;  // of a launch, or between two
+
+double rounds_us(const Cost& c, int64_t blocks, double steps) {
+    const int64_t rest = blocks % c.round;
+    double us = double(blocks / c.round) * (c.start + c.step * steps);
+    if (rest > c.light)
+        us += c.start + c.step * steps;
+    else if (rest > 0)
+        us += c.light_start + c.light_step * steps;
+    return us;
+}
 
 // A second launch that adds the splits' sums, and its traffic.
-double join_us(double bytes) { return 6.0 + bytes / 3e6; }
+double join_us(double bytes) { return kLaunchUs + bytes / 5e6; }
 
 }  // namespace
 
@@ -60,10 +76,10 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
     const int64_t wide = form == kPair ? 2 * n : n;
     Cut best;
     best.us = 1e30;
-    // few rows: reading the weight is all there is to it (1 x 4096 x 4096: kThin
-    // 7.2, kMid32 10.7 us; 30 rows 13.0 and 11.8, 64 rows 20.8 and 12.2).  Where
-    // rows do not lie on 16 bytes it is worth twice the time.
-    if ((form == kRows || form == kPair) && m <= (direct ? 16 : 64)) {
+    // few rows: reading the weight is all there is to it (1 x 4096, k 4096:
+    // kThin 7.2, kMid32 10.7 us; 30 x 704, k 704: 4.2 and 5.7; 30 x 4096, k 4096:
+    // 13.0 and 12.2; 60 x 4096, k 4096: 20.8 and 12.2)
+    if ((form == kRows || form == kPair) && m <= 32) {
         best.tile = kThin;
         best.per = steps;
         best.us = 0;
@@ -77,10 +93,7 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
             // a split keeps 8 steps, and only fills up a round
             if (splits > 1 && (steps < 8 * splits || tiles * splits > c.round)) break;
             const int64_t per = cdiv64(steps, splits), work = tiles * splits;
-            const int64_t rest = work % c.round;
-            double us = double(work / c.round) * c.full_step;
-            if (rest > 0) us += rest <= c.light ? c.light_step : c.full_step;
-            us = c.start + us * double(per);
+            double us = rounds_us(c, work, double(per));
             if (splits > 1)
                 us += join_us(8.0 * double(splits) * double(m) * double(wide) * double(outs));
             if (us < best.us) {
@@ -96,8 +109,6 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
 
 namespace {
 
-constexpr double kLaunchUs = 3.0;  // between two launches
-
 // The kernel that takes both gradients of a layer in the least time, together.
 int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
     int tile = kGuarded;
@@ -109,11 +120,12 @@ int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
         const TileSize t = kTileSize[c.tile];
         const double nx = double(cdiv64(dx.m, t.m) * cdiv64(dx.n, t.n));
         const double nw = double(cdiv64(dw.m, t.m) * cdiv64(dw.n, t.n) * dw.parts);
-        // workgroups of both kinds fill up the rounds: as much as all of them
-        // take, at least as long as the longer kind's
-        const double all = (nx * sx + nw * sw) / double(c.round) * c.full_step;
-        const double us = c.start + std::max(all, std::max(sx, sw) * c.light_step) +
-                          (nx + nw > double(c.round) ? c.start / 2 : 0);
+        // workgroups of both kinds fill up the rounds, the last one in part
+        const double ux = c.start + c.step * sx, uw = c.start + c.step * sw;
+        const double us = nx + nw <= double(c.light)
+                              ? c.light_start + c.light_step * std::max(sx, sw)
+                              : std::max((nx * ux + nw * uw) / double(c.round) + c.start / 2,
+                                         std::max(ux, uw));
         if (us < best) {
             best = us;
             tile = c.tile;
@@ -174,7 +186,7 @@ size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts) {
 bool worth_repacking(int form, int64_t m, int64_t n, int64_t k, int parts, int64_t elements) {
     const Cut as_is = plan_product(form, m, n, k, parts, false);
     if (as_is.tile == kThin) return false;
-    return plan_product(form, m, n, k, parts, true).us + 3.0 + 4.0 * double(elements) / 3e6 <
+    return plan_product(form, m, n, k, parts, true).us + kLaunchUs + 4.0 * double(elements) / 6e6 <
            as_is.us;
 }
 
@@ -254,7 +266,7 @@ int run_gradients(int64_t type, const Product& dx, const Product& dw, const Sums
         const bool d = direct(dx) && direct(dw);
         const Cut cx = plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx));
         const Cut cw = plan_product(kDw, dw.m, dw.n, dw.k, dw.parts, direct(dw));
-        const double apart = cx.us + cw.us + (sums.out ? 2 : 1) * kLaunchUs;
+        const double apart = cx.us + cw.us + (sums.out ? 2 : 1) * kLaunchUs;  // without a first one
         double us = 0;
         const int tile = plan_both(dx, dw, d, us);
         if (us < apart)

@@ -59,16 +59,16 @@ struct Product {
 // The kernels.  Guarded and thin ones take any strides and alignment, the
 // others rows on 16 bytes.  Outputs per workgroup:
 //   kGuarded  64 x 64, four groups; kMid32  32 x 64, four groups of waves over k
-//   kThin     64 x 16     kMid64  64 x 64, two groups
+//   kThin     32 x 16; kMid64  64 x 64, two groups
 //   kBig      256 x 256   kMid128 128 x 128 with a ring of four tiles, one
 //                         workgroup per compute unit; kPair128 with two, and two
-enum Tile { kGuarded, kThin, kMid32, kMid64, kMid128, kPair128, kBig };
+enum Tile { kGuarded, kThin, kMid32, kMid64, kMid128, kPair128, kBig, kLight };
 
 struct TileSize {
     int64_t m, n;
 };
-constexpr TileSize kTileSize[] = {{64, 64},   {64, 16},   {32, 64},  {64, 64},
-                                  {128, 128}, {128, 128}, {256, 256}};
+constexpr TileSize kTileSize[] = {{64, 64},   {32, 16},   {32, 64},  {64, 64},
+                                  {128, 128}, {128, 128}, {256, 256}, {64, 64}};
 
 // Which kernel, and the split of a product over its long axis: `splits`
 // workgroups per tile, each over `per` steps of 64; their 32-bit sums meet in

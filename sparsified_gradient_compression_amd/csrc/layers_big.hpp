@@ -160,21 +160,26 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
 
     __syncthreads();  // nobody reads a region any more, and no load is under way
 
-    // 64 x 64 outputs of the wave at a time, in the 16 KB of one region (which the
-    // compiler need not tell apart any more)
-    T* const own = wave < 4 ? (wave < 2 ? (wave ? a01 : a00) : (wave & 1 ? a11 : a10))
-                            : (wave < 6 ? (wave & 1 ? b01 : b00) : (wave & 1 ? b11 : b10));
-    float* out = reinterpret_cast<float*>(own);
+    // 128 rows of outputs at a time, 16 in each region
+    const auto at = [&](int r) {
+        T* const lo = r < 32 ? (r < 16 ? a00 : a01) : (r < 48 ? a10 : a11);
+        T* const hi = r < 96 ? (r < 80 ? b00 : b01) : (r < 112 ? b10 : b11);
+        return reinterpret_cast<float*>(r < 64 ? lo : hi) + (r & 15) * 256;
+    };
 #pragma unroll
     for (int ha = 0; ha < 2; ++ha) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < 4; ++mt) {
+            const int r = wm * 64 + mt * 16 + (lane & 15);
+            float* row = at(wm * 64 + mt * 16) + (lane & 15) * 256;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                put_tile<4, 2, BTR>(out, mt, j / 2 * 32, j % 2, lane, acc[ha][j / 2][mt][j % 2]);
-        const int64_t n = n0 + wn * 32;
-        put_wave<T, FORM, 4, 4>(A, split, z, m0 + ha * 128 + wm * 64, n, PAIR ? n : n + 128, lane,
-                                out, 0, 1, 0);
+                put_tile<2, BTR>(row, r, j / 2 * 128 + wn * 32, j % 2, lane,
+                                 acc[ha][j / 2][mt][j % 2]);
+        }
+        __syncthreads();
+        put_rows<T, FORM, 128, 256, 512>(A, split, z, m0 + ha * 128, n0, 1, 0, at);
+        if (ha == 0) __syncthreads();
     }
 }
 

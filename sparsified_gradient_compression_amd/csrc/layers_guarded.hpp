@@ -178,18 +178,18 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int64_t id, T* s
         if (r + 1 < rounds) place_lds(buf ^ 1);
     }
     __syncthreads();
-    constexpr int kOwn = MT * NTW * 256;
-    float* out = reinterpret_cast<float*>(smem) + wave * kOwn;
+    float* const out = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = (wm * MT + mt) * 16 + (lane & 15);
 #pragma unroll
         for (int j = 0; j < NTW; ++j)
-            put_tile<NTW, NT, BTR>(out + group * 4 * kOwn, mt, j / NT * NT * 16, j % NT, lane,
-                                   acc[mt][j]);
+            put_tile<NT, BTR>(out + group * 4096 + r * 64, r, j / NT * 32 + wn * NT * 16, j % NT,
+                              lane, acc[mt][j]);
+    }
     __syncthreads();
-    const int64_t mw = m0 + wm * 32, nw = n0 + wn * NT * 16;
-    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + 16, lane, out, group, KG,
-                               4 * kOwn);
+    put_rows<T, FORM, 64, 64, 256 * KG>(A, split, z, m0, n0, KG, 4096,
+                                        [&](int r) { return out + r * 64; });
 }
 
 constexpr int kGuardedThreads = 256 * kGuardedGroups;

@@ -23,6 +23,7 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
         case kGuarded: k_guarded<T, FORM><<<grid, kGuardedThreads, 0, s>>>(a); break;
         case kMid32: k_mid<T, FORM, Shape32><<<grid, 1024, 0, s>>>(a); break;
         case kMid64: k_mid<T, FORM, Shape64><<<grid, 512, 0, s>>>(a); break;
+        case kLight: k_mid<T, FORM, ShapeLight><<<grid, 256, 0, s>>>(a); break;
         case kMid128: k_mid<T, FORM, Shape128><<<grid, 512, 0, s>>>(a); break;
         case kPair128: k_mid<T, FORM, ShapePair><<<grid, 512, 0, s>>>(a); break;
         case kBig: k_big<T, FORM><<<grid, 512, 0, s>>>(a); break;
@@ -31,10 +32,8 @@ int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
                 const dim3 rows(static_cast<unsigned>(cdiv64(a.N, 16)));
                 if (a.M <= 16)
                     k_thin<T, FORM == kPair, 1><<<rows, 512, 0, s>>>(a);
-                else if (a.M <= 32)
-                    k_thin<T, FORM == kPair, 2><<<rows, 512, 0, s>>>(a);
                 else
-                    k_thin<T, FORM == kPair, 4><<<rows, 512, 0, s>>>(a);
+                    k_thin<T, FORM == kPair, 2><<<rows, 512, 0, s>>>(a);
             }
     }
     DGC_LAYERS_CHECK();
@@ -76,12 +75,12 @@ int Launch<T>::product(const Product& p, const Cut& c, void* ws, hipStream_t s) 
         case kDw: rc = launch_tiles<T, kDw>(a, c, s); break;
     }
     if (rc != DGC_OK || c.splits == 1) return rc;
-    const int64_t blocks = cdiv64(cdiv64(p.n, 4) * p.m * a.outs, 256);
+    const int64_t blocks = cdiv64(cdiv64(p.n, 4) * p.m * a.outs, 64);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (p.form == kPair)
-        k_join<T, true><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
+        k_join<T, true><<<dim3(unsigned(blocks)), 64, 0, s>>>(a);
     else
-        k_join<T, false><<<dim3(unsigned(blocks)), 256, 0, s>>>(a);
+        k_join<T, false><<<dim3(unsigned(blocks)), 64, 0, s>>>(a);
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }
@@ -106,6 +105,7 @@ int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& 
             break;
         case kMid32: k_mid_both<T, Shape32><<<grid, 1024, 0, s>>>(x, w, nx, nw, sums); break;
         case kMid64: k_mid_both<T, Shape64><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
+        case kLight: k_mid_both<T, ShapeLight><<<grid, 256, 0, s>>>(x, w, nx, nw, sums); break;
         case kMid128: k_mid_both<T, Shape128><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
         case kPair128: k_mid_both<T, ShapePair><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
         default: return DGC_EINVAL;

@@ -24,6 +24,7 @@ struct Shape {
 };
 typedef Shape<32, 64, 2, 2, 4, 3> Shape32;
 typedef Shape<64, 64, 2, 2, 2, 4> Shape64;
+typedef Shape<64, 64, 2, 2, 1, 2> ShapeLight;
 typedef Shape<128, 128, 2, 4, 1, 4> Shape128;
 typedef Shape<128, 128, 2, 4, 1, 2> ShapePair;
 
@@ -139,23 +140,25 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int64_t id, T* s0, T
     __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
     __syncthreads();  // nobody reads the ring any more, and no load is under way
 
-    // the outputs' 32-bit sums through LDS: as many waves' as fit in a tile of
-    // the ring, the others' in the next
-    constexpr int kOwn = MT * NTW * 256;
-    constexpr int kFit = KG * kTile * int(sizeof(T)) / (kOwn * 4);
-    constexpr int kGroupStride = W * kOwn;
-    static_assert(KG == 1 ? 2 * kFit >= W : kFit >= KG * W, "outputs fit the ring");
-    float* out = reinterpret_cast<float*>(wave < kFit ? s0 : s1) + wave % kFit * kOwn;
+    // the outputs' 32-bit sums through LDS: as many rows as fit in a tile of
+    // the ring, the others in the next
+    constexpr int kFit = SH::kRing * int(sizeof(T)) / (BN * 4) / KG < BM
+                             ? SH::kRing * int(sizeof(T)) / (BN * 4) / KG : BM;
+    static_assert(KG == 1 ? 2 * kFit >= BM : kFit >= BM, "outputs fit the ring");
+    constexpr int kGroupStride = BM * BN;
+    const auto at = [&](int r) {
+        return reinterpret_cast<float*>(r < kFit ? s0 : s1) + r % kFit * BN;
+    };
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = (wm * MT + mt) * 16 + (lane & 15);
+        float* row = at(r) + group * kGroupStride;
 #pragma unroll
         for (int j = 0; j < NTW; ++j)
-            put_tile<NTW, NT, BTR>(out + group * kGroupStride, mt, j / NT * NT * 16, j % NT, lane,
-                                   acc[mt][j]);
-    if (KG > 1) __syncthreads();
-    const int64_t mw = m0 + wm * MT * 16, nw = n0 + wn * NT * 16;
-    put_wave<T, FORM, MT, NTW>(A, split, z, mw, nw, PAIR ? nw : nw + NTW * 8, lane, out, group, KG,
-                               kGroupStride);
+            put_tile<NT, BTR>(row, r, j / NT * (BN / 2) + wn * NT * 16, j % NT, lane, acc[mt][j]);
+    }
+    __syncthreads();
+    put_rows<T, FORM, BM, BN, SH::kThreads>(A, split, z, m0, n0, KG, kGroupStride, at);
 }
 
 template <class T, int FORM, class SH>

@@ -1,4 +1,4 @@
-// layers_thin.hpp -- layer outputs of up to 64 rows: bound by reading the
+// layers_thin.hpp -- layer outputs of up to 32 rows: bound by reading the
 // weight once.
 //
 // A workgroup takes 16 rows of the weight (16 columns of the output; of both
@@ -17,7 +17,7 @@ namespace layers {
 template <class T, bool PAIR, int MT>
 __global__ __launch_bounds__(512) void k_thin(TileArgs A) {
     typedef typename Arith<T>::v8 v8;
-    constexpr int P = PAIR ? 2 : 1, kWaves = 8, kAhead = MT > 2 ? 2 : 4;
+    constexpr int P = PAIR ? 2 : 1, kWaves = 8, kAhead = 4;
     // [wave][product][row][16 columns], columns in fours XORed with the row
     __shared__ __align__(16) float sums[kWaves][P][MT * 16][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -337,52 +337,53 @@ __device__ __forceinline__ void place(int64_t id, int64_t mt, int64_t nt, int64_
     tn = in / high;
 }
 
-// A wave's outputs leave through its own LDS (MT * 16 rows of NTW * 16
-// columns in binary32, NTW = 2 or 4): what finishes an element is then one
-// short loop whose lanes hold 8 consecutive columns each, instead of the
-// whole of it unrolled over every register.
-//   columns of the first and the second half of the wave's start at n0, n1
-//   (kPair: of the first and the second product, the same ones)
-//   groups: so many waves hold sums of the same outputs, `stride` floats
-//   apart, to be added in that order; each finishes its share of the rows
-template <class T, int FORM, int MT, int NTW>
-__device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, int64_t m0,
-                                         int64_t n0, int64_t n1, int lane, const float* lds,
-                                         int group, int groups, int stride) {
+// A workgroup's outputs leave through LDS: rows of COLS columns in binary32
+// (kPair: the first product's columns, then the second's), so that the lanes
+// that finish a row hold 8 consecutive columns each and store whole lines, in
+// one short loop.  Columns lie in fours, XORed with the row: lanes that write
+// a matrix tile hold the same columns of 16 rows.
+__device__ __forceinline__ int out_at(int r, int col4) { return (col4 ^ ((r & 7) << 1)) * 4; }
+
+// Finishes rows 0 .. ROWS - 1, outputs m0 + row, n0 + column.
+//   at(r): where row r lies; groups: so many sums of every output, `stride`
+//   floats apart, are added in that order
+template <class T, int FORM, int ROWS, int COLS, int THREADS, class At>
+__device__ __forceinline__ void put_rows(const TileArgs& A, int split, int z, int64_t m0,
+                                         int64_t n0, int groups, int stride, At at) {
     constexpr bool PAIR = FORM == kPair;
-    constexpr int W = NTW * 16;                     // columns in LDS
-    constexpr int kLanes = PAIR ? W / 16 : W / 8;   // lanes per row
-    constexpr int kRows = 64 / kLanes;
-    constexpr int kAhead = 4;  // rows whose loads are under way together
-    const int c = lane % kLanes;
-    const int64_t n = c * 8 < W / 2 ? n0 + c * 8 : n1 + c * 8 - W / 2;
+    constexpr int kCols = PAIR ? COLS / 2 : COLS;
+    constexpr int kLanes = kCols / 8, kStepRows = THREADS / kLanes;
+    constexpr int kSteps = (ROWS + kStepRows - 1) / kStepRows;
+    constexpr int kAhead = kSteps < 4 ? kSteps : 4;  // rows whose loads are under way together
+    const int c = threadIdx.x % kLanes;
+    const int64_t n = n0 + c * 8;
     const int valid = A.N - n < 8 ? int(A.N - n) : 8;
     if (valid <= 0) return;
     const Finish& f = A.fin;
     float bias[8];
     if (!PAIR && f.bias) load_row<T, 8>(static_cast<const T*>(f.bias) + n, valid, bias);
-    const int rows = A.M - m0 < MT * 16 ? int(A.M - m0) : MT * 16;
-    const int step = kRows * groups;
+    const int rows = A.M - m0 < ROWS ? int(A.M - m0) : ROWS;
 #pragma unroll 1
-    for (int first = group * kRows + lane / kLanes; first < rows; first += kAhead * step) {
+    for (int first = threadIdx.x / kLanes; first < rows; first += kAhead * kStepRows) {
         float residual[kAhead][8];
         if (!PAIR && f.residual) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
-                if (first + u * step < rows)
+                if (first + u * kStepRows < rows)
                     load_row<T, 8>(static_cast<const T*>(f.residual) +
-                                       (m0 + first + u * step) * f.ldr + n, valid, residual[u]);
+                                       (m0 + first + u * kStepRows) * f.ldr + n, valid,
+                                   residual[u]);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int r = first + u * step;
+            const int r = first + u * kStepRows;
             if (r >= rows) break;
             float v[8], v2[8];
-            const int key = (r & (W / 8 - 1)) << 1;
+            const float* row = at(r);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float* p = lds + r * W + ((2 * c + q) ^ key) * 4;
-                const float* p2 = lds + r * W + ((2 * c + q + W / 8) ^ key) * 4;
+                const float* p = row + out_at(r, 2 * c + q);
+                const float* p2 = row + out_at(r, 2 * c + q + COLS / 8);
                 f32x4 t = *reinterpret_cast<const f32x4*>(p), t2 = {0, 0, 0, 0};
                 if (PAIR) t2 = *reinterpret_cast<const f32x4*>(p2);
                 for (int w = 1; w < groups; ++w) {
@@ -405,22 +406,21 @@ __device__ __forceinline__ void put_wave(const TileArgs& A, int split, int z, in
     }
 }
 
-// Matrix tile j (of NT that share their columns by n_row<NT>, or TR: that lie
-// side by side) of rows 16 mt, at column `col`, into that LDS.
-template <int NTW, int NT, bool TR>
-__device__ __forceinline__ void put_tile(float* lds, int mt, int col, int j, int lane, f32x4 v) {
-    constexpr int W = NTW * 16;
-    const int r = mt * 16 + (lane & 15), g = lane >> 4;
+// Columns that a lane holds of matrix tile j of the NT from column `col` on
+// (dealt by n_row<NT>; TR: side by side), into row r of that LDS.
+template <int NT, bool TR>
+__device__ __forceinline__ void put_tile(float* row, int r, int col, int j, int lane, f32x4 v) {
+    const int g = lane >> 4;
     const int c4 = col / 4 + (TR ? j * 4 + g : g * NT + j);
-    *reinterpret_cast<f32x4*>(lds + r * W + (c4 ^ ((r & (W / 8 - 1)) << 1)) * 4) = v;
+    *reinterpret_cast<f32x4*>(row + out_at(r, c4)) = v;
 }
 
 // The sums of all splits, added in their order, then finished.  One thread
 // per 4 columns of a row.
 template <class T, bool PAIR>
-__global__ __launch_bounds__(256) void k_join(TileArgs A) {
+__global__ __launch_bounds__(64) void k_join(TileArgs A) {
     const int64_t groups = (A.N + 3) / 4, z_count = A.outs;
-    int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    int64_t id = int64_t(blockIdx.x) * 64 + threadIdx.x;
     if (id >= groups * A.M * z_count) return;
     const int z = int(id / (groups * A.M));
     id -= z * groups * A.M;
@@ -430,17 +430,28 @@ __global__ __launch_bounds__(256) void k_join(TileArgs A) {
     const int64_t plane = A.M * A.N;
     float v[4] = {0, 0, 0, 0}, v2[4] = {0, 0, 0, 0};
     struct __attribute__((packed, aligned(4), may_alias)) B { f32x4 v; };
-    for (int s = 0; s < A.splits; ++s) {
-        const float* p = A.part + (int64_t(s) * planes + z) * plane + m * A.N + n;
+    constexpr int P = PAIR ? 2 : 1;
+    for (int s0 = 0; s0 < A.splits; s0 += 8) {  // 8 splits' loads are under way together
+        f32x4 t[8][P];
 #pragma unroll
-        for (int w = 0; w < (PAIR ? 2 : 1); ++w, p += plane) {
-            float* o = w ? v2 : v;
-            if (valid == 4) {
-                const f32x4 t = reinterpret_cast<const B*>(p)->v;
+        for (int s = 0; s < 8; ++s) {
+            if (s0 + s >= A.splits) break;
+            const float* p = A.part + (int64_t(s0 + s) * planes + z) * plane + m * A.N + n;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] += t[e];
-            } else {
-                for (int e = 0; e < valid; ++e) o[e] += p[e];
+            for (int w = 0; w < P; ++w, p += plane) {
+                if (valid == 4)
+                    t[s][w] = reinterpret_cast<const B*>(p)->v;
+                else
+                    for (int e = 0; e < 4; ++e) t[s][w][e] = e < valid ? p[e] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s0 + s >= A.splits) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += t[s][0][e];
+                v2[e] += t[s][P - 1][e];
             }
         }
     }
