@@ -31,6 +31,9 @@ namespace {
 //   1024 x 1024, k 64        10    5.0     4.2     6.2      5.8    15       6.4
 //   1024 x 1024, k 1024      12    6.9     8.5      11       12    27       9.2
 //   2048 x 2048, k 2048      57     35      26      20       28    42        47
+//   3000 x 1500, k 3000      97     78      70      62       51    65
+//   858 x 696, k 14336       89     54     119     100      175   279
+//     split in 4 and joined  72     51      44      35       50    84
 //   4096 x 4096, k 64       120     51      18      20       14    17        67
 //   4096 x 4096, k 2048     221    132              75       66    53
 // Off 16 bytes a step of kGuarded takes half as long again.
@@ -43,7 +46,7 @@ constexpr Cost kCosts[] = {
     {kGuarded, 256, 256, 2.6, 0.40, 2.6, 0.40}, {kMid32, 256, 256, 3.4, 0.13, 3.4, 0.13},
     {kMid64, 256, 256, 2.2, 0.21, 2.2, 0.21},   {kMid128, 256, 256, 3.8, 0.45, 3.8, 0.45},
     {kPair128, 512, 256, 5.0, 0.84, 3.5, 0.70}, {kBig, 256, 128, 11.0, 1.28, 9.0, 1.05},
-    {kLight, 1280, 256, 4.0, 0.72, 2.0, 0.26}};
+    {kLight, 1280, 640, 4.0, 1.25, 2.5, 0.45}};
 constexpr double kLaunchUs = 2.5;  // of a launch, or between two
 
 double rounds_us(const Cost& c, int64_t blocks, double steps) {

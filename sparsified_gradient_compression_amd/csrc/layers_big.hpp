@@ -43,16 +43,9 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = wave >> 2, wn = wave & 3;
 
-    const int64_t tiles = A.mt * A.nt;
-    int64_t id = blockIdx.x;
-    const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
-    const int split = int(id / per_split);
-    id -= split * per_split;
-    const int z = FORM == kDw ? int(id / tiles) : 0;
-    id -= z * tiles;
-    int64_t tm, tn;
-    place(id, A.mt, A.nt, tm, tn);
-    const int64_t m0 = tm * 256, n0 = tn * (PAIR ? 128 : 256);
+    const Spot at_tile = spot<FORM>(A, int(blockIdx.x));
+    const int split = at_tile.split, z = at_tile.z;
+    const int64_t m0 = at_tile.tm * 256, n0 = at_tile.tn * (PAIR ? 128 : 256);
 
     const int ksteps = int((A.K + kStep - 1) / kStep);
     const int total = ksteps * (FORM == kDx ? A.parts : 1);

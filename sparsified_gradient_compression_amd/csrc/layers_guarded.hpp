@@ -74,7 +74,7 @@ constexpr int kGuardedGroups = 4;
 constexpr int kGuardedSide = 64 * kStep;
 
 template <class T, int FORM>
-__device__ __forceinline__ void guarded_tile(const TileArgs& A, int64_t id, T* smem) {
+__device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem) {
     constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
     constexpr int KG = kGuardedGroups, MT = 2, NTW = 2, NT = PAIR ? 1 : 2;
     typedef typename Arith<T>::v8 v8;
@@ -84,15 +84,9 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int64_t id, T* s
     T* const sa = smem + group * 4 * kGuardedSide;  // two tiles of a, two of b
     T* const sb = sa + 2 * kGuardedSide;
 
-    const int64_t tiles = A.mt * A.nt;
-    const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
-    const int split = int(id / per_split);
-    id -= split * per_split;
-    const int z = FORM == kDw ? int(id / tiles) : 0;
-    id -= z * tiles;
-    int64_t tm, tn;
-    place(id, A.mt, A.nt, tm, tn);
-    const int64_t m0 = tm * 64, n0 = tn * (PAIR ? 32 : 64);
+    const Spot at_tile = spot<FORM>(A, id);
+    const int split = at_tile.split, z = at_tile.z;
+    const int64_t m0 = at_tile.tm * 64, n0 = at_tile.tn * (PAIR ? 32 : 64);
 
     const int64_t ksteps = (A.K + kStep - 1) / kStep;
     const int64_t total = ksteps * (FORM == kDx ? A.parts : 1);
@@ -204,17 +198,17 @@ __global__ __launch_bounds__(kGuardedThreads) void k_guarded(TileArgs A) {
 // Both gradients of a layer in one launch, and the column sums' last step.
 template <class T>
 __global__ __launch_bounds__(kGuardedThreads) void k_guarded_both(TileArgs dx, TileArgs dw,
-                                                                  int64_t dx_blocks,
-                                                                  int64_t dw_blocks, Sums sums) {
+                                                                  int dx_blocks, int dw_blocks,
+                                                                  Sums sums) {
     __shared__ __align__(16) T smem[kGuardedLds];
-    const int64_t id = blockIdx.x;
+    // each kind begins with the first die's workgroup
+    const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
         guarded_tile<T, kDx>(dx, id, smem);
-    else if (id < dx_blocks + dw_blocks)
-        guarded_tile<T, kDw>(dw, id - dx_blocks, smem);
-    else
-        sum_columns<T, kGuardedThreads>(sums, id - dx_blocks - dw_blocks,
-                                        reinterpret_cast<float*>(smem));
+    else if (id >= dw0 && id < sum0)
+        guarded_tile<T, kDw>(dw, id - dw0, smem);
+    else if (id >= sum0)
+        sum_columns<T, kGuardedThreads>(sums, id - sum0, reinterpret_cast<float*>(smem));
 }
 
 }  // namespace layers

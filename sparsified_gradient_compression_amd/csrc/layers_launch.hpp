@@ -95,19 +95,19 @@ int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& 
     c.per = cdiv64(dw.k, kStep);
     const TileArgs w = tile_args(dw, c, nullptr);
     const int64_t nx = x.mt * x.nt, nw = w.mt * w.nt * w.parts;
-    const int64_t blocks = nx + nw + (sums.out ? cdiv64(sums.N, 32) : 0);
+    const int64_t blocks = (nx + 7) / 8 * 8 + nw + (sums.out ? cdiv64(sums.N, 32) : 0);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (blocks == 0) return DGC_OK;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (tile) {
         case kGuarded:
-            k_guarded_both<T><<<grid, kGuardedThreads, 0, s>>>(x, w, nx, nw, sums);
+            k_guarded_both<T><<<grid, kGuardedThreads, 0, s>>>(x, w, int(nx), int(nw), sums);
             break;
-        case kMid32: k_mid_both<T, Shape32><<<grid, 1024, 0, s>>>(x, w, nx, nw, sums); break;
-        case kMid64: k_mid_both<T, Shape64><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
-        case kLight: k_mid_both<T, ShapeLight><<<grid, 256, 0, s>>>(x, w, nx, nw, sums); break;
-        case kMid128: k_mid_both<T, Shape128><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
-        case kPair128: k_mid_both<T, ShapePair><<<grid, 512, 0, s>>>(x, w, nx, nw, sums); break;
+        case kMid32: k_mid_both<T, Shape32><<<grid, 1024, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid64: k_mid_both<T, Shape64><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kLight: k_mid_both<T, ShapeLight><<<grid, 256, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid128: k_mid_both<T, Shape128><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kPair128: k_mid_both<T, ShapePair><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
         default: return DGC_EINVAL;
     }
     DGC_LAYERS_CHECK();

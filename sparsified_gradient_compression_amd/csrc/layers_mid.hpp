@@ -36,7 +36,7 @@ typedef Shape<128, 128, 2, 4, 1, 2> ShapePair;
     __shared__ __align__(16) T s3[SH::S > 3 ? SH::kRing : 8]
 
 template <class T, int FORM, class SH>
-__device__ __forceinline__ void mid_tile(const TileArgs& A, int64_t id, T* s0, T* s1, T* s2,
+__device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1, T* s2,
                                          T* s3) {
     constexpr int BM = SH::BM, BN = SH::BN, WM = SH::WM, WN = SH::WN, KG = SH::KG, S = SH::S;
     constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
@@ -51,15 +51,9 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int64_t id, T* s0, T
     const int wave = all % W, group = all / W;
     const int wm = wave / WN, wn = wave % WN;
 
-    const int64_t tiles = A.mt * A.nt;
-    const int64_t per_split = tiles * (FORM == kDw ? A.parts : 1);
-    const int split = int(id / per_split);
-    id -= split * per_split;
-    const int z = FORM == kDw ? int(id / tiles) : 0;
-    id -= z * tiles;
-    int64_t tm, tn;
-    place(id, A.mt, A.nt, tm, tn);
-    const int64_t m0 = tm * BM, n0 = tn * RB;
+    const Spot at_tile = spot<FORM>(A, id);
+    const int split = at_tile.split, z = at_tile.z;
+    const int64_t m0 = at_tile.tm * BM, n0 = at_tile.tn * RB;
 
     const int ksteps = int((A.K + kStep - 1) / kStep);
     const int total = ksteps * (FORM == kDx ? A.parts : 1);
@@ -170,17 +164,16 @@ __global__ __launch_bounds__(SH::kThreads) void k_mid(TileArgs A) {
 // Both gradients of a layer in one launch, and the column sums' last step.
 template <class T, class SH>
 __global__ __launch_bounds__(SH::kThreads) void k_mid_both(TileArgs dx, TileArgs dw,
-                                                           int64_t dx_blocks, int64_t dw_blocks,
-                                                           Sums sums) {
+                                                           int dx_blocks, int dw_blocks, Sums sums) {
     DGC_RING(T, SH);
-    const int64_t id = blockIdx.x;
+    // each kind begins with the first die's workgroup
+    const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
         mid_tile<T, kDx, SH>(dx, id, s0, s1, s2, s3);
-    else if (id < dx_blocks + dw_blocks)
-        mid_tile<T, kDw, SH>(dw, id - dx_blocks, s0, s1, s2, s3);
-    else
-        sum_columns<T, SH::kThreads>(sums, id - dx_blocks - dw_blocks,
-                                     reinterpret_cast<float*>(s0));
+    else if (id >= dw0 && id < sum0)
+        mid_tile<T, kDw, SH>(dw, id - dw0, s0, s1, s2, s3);
+    else if (id >= sum0)
+        sum_columns<T, SH::kThreads>(sums, id - sum0, reinterpret_cast<float*>(s0));
 }
 
 }  // namespace layers

@@ -322,19 +322,32 @@ struct TileArgs {
     Finish fin;
 };
 
-// Where workgroup `id` works.  Workgroups go to the 8 dies in turn, each
-// with an L2 of its own: die x takes the x-th eighth of the tiles, and walks
-// them in bands of 8 rows, so that what runs there at once shares operands.
-__device__ __forceinline__ void place(int64_t id, int64_t mt, int64_t nt, int64_t& tm,
-                                      int64_t& tn) {
-    const int64_t total = mt * nt, per = total / 8, rem = total % 8;
-    const int64_t x = id % 8, i = id / 8;
-    const int64_t t = x * per + (x < rem ? x : rem) + i;
-    constexpr int64_t kBand = 8;
-    const int64_t band = t / (kBand * nt), in = t - band * kBand * nt;
-    const int64_t high = mt - band * kBand < kBand ? mt - band * kBand : kBand;
-    tm = band * kBand + in % high;
-    tn = in / high;
+// Where workgroup `id` of a product works.  Workgroups go to the 8 dies in
+// turn, each with an L2 of its own: die x takes the x-th eighth of the splits,
+// outputs and tiles, and walks the tiles in bands of 8 rows, so that what runs
+// there at once shares operands.
+struct Spot {
+    int split, z;
+    int64_t tm, tn;
+};
+
+template <int FORM>
+__device__ __forceinline__ Spot spot(const TileArgs& A, int id) {
+    const int mt = int(A.mt), nt = int(A.nt), tiles = mt * nt;
+    const int outs = FORM == kDw ? A.outs : 1, all = tiles * outs * A.splits;
+    const int x = id % 8, rem = all % 8;
+    int t = x * (all / 8) + (x < rem ? x : rem) + id / 8;
+    Spot s;
+    s.split = t / (tiles * outs);
+    t -= s.split * tiles * outs;
+    s.z = FORM == kDw ? t / tiles : 0;
+    t -= s.z * tiles;
+    constexpr int kBand = 8;
+    const int band = t / (kBand * nt), in = t - band * kBand * nt;
+    const int high = mt - band * kBand < kBand ? mt - band * kBand : kBand;
+    s.tm = band * kBand + in % high;
+    s.tn = in / high;
+    return s;
 }
 
 // A workgroup's outputs leave through LDS: rows of COLS columns in binary32
