@@ -467,6 +467,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     SlopeArgs sl;
     sl.M = m;
     sl.N = f;
+    sl.per = m * f < (int64_t(1) << 21) ? 4 : 8;  // fewer than 8 waves on each SIMD: shorter ones
     sl.dy = a->dh;
     sl.lddy = a->lddh;
     sl.pre = a->gate;

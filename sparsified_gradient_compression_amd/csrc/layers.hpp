@@ -88,7 +88,8 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
 
 // dz = dy * act'(pre), its rows padded with zeros to ldz, and the sums of its
 // columns over `per` rows each into `part` (either null: not wanted); with
-// `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums.
+// `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums, `per` (4
+// or 8) elements per thread.
 struct SlopeArgs {
     int64_t M = 0, N = 0, per = 0;
     const void *dy = nullptr, *pre = nullptr, *up = nullptr;

@@ -35,9 +35,9 @@ __device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, floa
 #pragma unroll
             for (int r = 0; r < 2; ++r)
                 if (m + 4 * r < m1) {
-                    load_row<T, 8>(dy + (m + 4 * r) * A.lddy + n, valid, d[r]);
+                    load_row<T, 8, true>(dy + (m + 4 * r) * A.lddy + n, valid, d[r]);
                     if (A.act != DGC_ACT_NONE)
-                        load_row<T, 8>(pre + (m + 4 * r) * A.ldp + n, valid, z[r]);
+                        load_row<T, 8, true>(pre + (m + 4 * r) * A.ldp + n, valid, z[r]);
                 }
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -96,29 +96,29 @@ __global__ __launch_bounds__(256) void k_sum_columns(Sums A) {
     sum_columns<T, 256>(A, blockIdx.x, lds);
 }
 
-// da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; 4
-// elements per thread.
-template <class T>
+// da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; C (4
+// or 8) elements per thread.
+template <class T, int C>
 __device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id) {
-    const int64_t groups = A.ldz / 4;
+    const int64_t groups = A.ldz / C;
     id = id * 256 + threadIdx.x;
     if (id >= groups * A.M) return;
-    const int64_t m = id / groups, n = (id - m * groups) * 4;
-    const int valid = A.N - n >= 4 ? 4 : A.N > n ? int(A.N - n) : 0;
-    float d[4], a[4], b[4], oa[4], ob[4];
-    load_row<T, 4>(static_cast<const T*>(A.dy) + m * A.lddy + n, valid, d);
-    load_row<T, 4>(static_cast<const T*>(A.pre) + m * A.ldp + n, valid, a);
-    load_row<T, 4>(static_cast<const T*>(A.up) + m * A.ldu + n, valid, b);
+    const int64_t m = id / groups, n = (id - m * groups) * C;
+    const int valid = A.N - n >= C ? C : A.N > n ? int(A.N - n) : 0;
+    float d[C], a[C], b[C], oa[C], ob[C];
+    load_row<T, C, true>(static_cast<const T*>(A.dy) + m * A.lddy + n, valid, d);
+    load_row<T, C, true>(static_cast<const T*>(A.pre) + m * A.ldp + n, valid, a);
+    load_row<T, C, true>(static_cast<const T*>(A.up) + m * A.ldu + n, valid, b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < C; ++i) {
         float value, slope;
         act_pair(A.act, a[i], value, slope);
         oa[i] = d[i] * b[i] * slope;
         ob[i] = d[i] * value;
     }
     // zeros in the padding
-    store_row<T, 4>(static_cast<T*>(A.dz) + m * A.ldz + n, 4, oa);
-    store_row<T, 4>(static_cast<T*>(A.dz2) + m * A.ldz + n, 4, ob);
+    store_row<T, C>(static_cast<T*>(A.dz) + m * A.ldz + n, C, oa);
+    store_row<T, C>(static_cast<T*>(A.dz2) + m * A.ldz + n, C, ob);
 }
 
 // Rows at any even address to rows on 16 bytes, zeros up to their ends; 8
@@ -155,8 +155,10 @@ __global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_bloc
     const int64_t id = blockIdx.x;
     if (id >= slope_blocks)
         repack_block(r, id - slope_blocks);
+    else if (A.up && A.per == 4)
+        gate_slope_block<T, 4>(A, id);
     else if (A.up)
-        gate_slope_block<T>(A, id);
+        gate_slope_block<T, 8>(A, id);
     else
         slope_block<T>(A, id, sums);
 }

@@ -118,7 +118,7 @@ template <class T>
 int Launch<T>::prepare(const SlopeArgs& a, const Repack& r, hipStream_t s) {
     int64_t slopes = 0, pieces = 0;
     if (a.M > 0 && a.N > 0)
-        slopes = a.up ? cdiv64(a.ldz / 4 * a.M, 256) : cdiv64(a.N, 512) * cdiv64(a.M, a.per);
+        slopes = a.up ? cdiv64(a.ldz / a.per * a.M, 256) : cdiv64(a.N, 512) * cdiv64(a.M, a.per);
     for (int i = 0; i < r.count; ++i) pieces += r.rows[i] * cdiv64(r.cols[i], 8);
     const int64_t blocks = slopes + cdiv64(pieces, 256);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;

@@ -122,19 +122,26 @@ __device__ __forceinline__ void act_pair(int act, float z, float& value, float& 
 // ----------------------------------------------------- rows of few elements
 
 // C consecutive elements of a row, of which the first `valid` exist.
-template <class T, int C>
+// ONCE: past the caches, for what is not read again soon.
+template <class T, int C, bool ONCE = false>
 __device__ __forceinline__ void load_row(const T* p, int valid, float* v) {
     if (valid >= C) {
         T t[C];
         if constexpr (C % 8 == 0) {
+            typedef u32x4 V __attribute__((aligned(2), may_alias));
 #pragma unroll
-            for (int i = 0; i < C / 8; ++i)
-                *reinterpret_cast<Bytes16*>(t + 8 * i) =
-                    *reinterpret_cast<const Bytes16*>(p + 8 * i);
+            for (int i = 0; i < C / 8; ++i) {
+                const V* q = reinterpret_cast<const V*>(p + 8 * i);
+                const u32x4 w = ONCE ? __builtin_nontemporal_load(q) : *q;
+                __builtin_memcpy(t + 8 * i, &w, 16);
+            }
         } else {
-            struct __attribute__((packed, aligned(2), may_alias)) B { uint64_t v; };
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef u32x2 V __attribute__((aligned(2), may_alias));
             static_assert(C == 4, "rows of 4 or of eights");
-            *reinterpret_cast<B*>(t) = *reinterpret_cast<const B*>(p);
+            const V* q = reinterpret_cast<const V*>(p);
+            const u32x2 w = ONCE ? __builtin_nontemporal_load(q) : *q;
+            __builtin_memcpy(t, &w, 8);
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = float(t[i]);
