@@ -594,7 +594,8 @@ typedef struct dgc_linear_args {
  * the column sums of dz.  Each of dx, dw, dbias may be NULL.  dw and dbias
  * are of grad_type: `type`, or DGC_FP32 (a learner's flat gradient).  pre is
  * not read for DGC_ACT_NONE; for other activations dz is rounded to `type`
- * before the products, not before the column sums. */
+ * before the products (up to 32 rows: to the sum of two numbers of `type`),
+ * not before the column sums. */
 typedef struct dgc_linear_backward_args {
     int64_t type, grad_type, act, m, n, k;
     const void* dy;
@@ -631,7 +632,7 @@ typedef struct dgc_gated_ffn_args {
 } dgc_gated_ffn_args;
 
 /* With da = dh * up * act'(gate) and db = dh * act(gate), both rounded to
- * `type`: dx[m][d] = da w_gate + db w_up, dw_gate[f][d] = da^T x,
+ * `type` (up to 32 rows: to the sum of two numbers of `type`): dx[m][d] = da w_gate + db w_up, dw_gate[f][d] = da^T x,
  * dw_up = db^T x.  dx may be NULL, and dw_gate and dw_up together. */
 typedef struct dgc_gated_ffn_backward_args {
     int64_t type, grad_type, act, m, d, f;

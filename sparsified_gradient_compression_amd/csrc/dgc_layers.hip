@@ -73,7 +73,10 @@ bool direct(const Product& p) {
     return !two_b || (direct(p.b[1], cb) && p.b[1].ld == p.b[0].ld);
 }
 
-Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct) {
+// The rows that a kernel's tile has have to take both halves of dz.
+bool takes(const TileSize& t, int form, int fold) { return form != kDx || t.m >= 2 * fold; }
+
+Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct, int fold) {
     const int64_t outs = form == kDw ? parts : 1;
     const int64_t steps = std::max<int64_t>(cdiv64(k, 64) * (form == kDx ? parts : 1), 1);
     const int64_t wide = form == kPair ? 2 * n : n;
@@ -91,6 +94,7 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
     for (const Cost& c : kCosts) {
         if ((c.tile == kGuarded) == direct) continue;
         const TileSize t = kTileSize[c.tile];
+        if (!takes(t, form, fold)) continue;
         const int64_t tiles = cdiv64(m, t.m) * cdiv64(wide, t.n) * outs;
         for (int64_t splits = 1; splits <= 8; splits *= 2) {
             // a split keeps 8 steps, and only fills up a round
@@ -121,6 +125,7 @@ int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
     for (const Cost& c : kCosts) {
         if ((c.tile == kGuarded) == direct || c.tile == kBig) continue;
         const TileSize t = kTileSize[c.tile];
+        if (!takes(t, kDx, dx.fold)) continue;
         const double nx = double(cdiv64(dx.m, t.m) * cdiv64(dx.n, t.n));
         const double nw = double(cdiv64(dw.m, t.m) * cdiv64(dw.n, t.n) * dw.parts);
         // workgroups of both kinds fill up the rounds, the last one in part
@@ -173,13 +178,16 @@ int space_ok(const void* ws, size_t have, size_t need) {
 int64_t pad8(int64_t x) { return (x + 7) / 8 * 8; }
 
 // A product's splits, in the workspace.
-size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts) {
+size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts, int fold = 0) {
     const int64_t planes = form == kPair ? 2 : form == kDw ? parts : 1;
     size_t most = 0;
     for (const bool d : {false, true}) {
-        const Cut c = plan_product(form, m, n, k, parts, d);
-        if (c.splits > 1)
-            most = std::max(most, size_t(c.splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
+        for (const int fo : {0, fold}) {  // 0 too: without an activation
+            const Cut c = plan_product(form, m, n, k, parts, d, fo);
+            if (c.splits > 1)
+                most = std::max(most,
+                                size_t(c.splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
+        }
     }
     return round_up(most);
 }
@@ -197,10 +205,16 @@ size_t row_bytes(int64_t rows, int64_t cols) {
     return round_up(size_t(rows) * size_t(pad8(cols)) * 2);
 }
 
+// Rows up to which dz is kept in two halves: as many as leave half of a tile
+// of 64 empty.  One row's 64 gradients had errors of 1.6 times the rounding of
+// their own without, where many rows' have 1.4.
+constexpr int64_t kFineRows = 32;
+
 // Where a call keeps what it lays out: dz (da, db), column sums, operands that
 // are repacked, and splits.  From the sizes alone.
 struct Space {
     bool pack = false;
+    int32_t fold = 0;  // rows of dz, where it is kept in two halves
     size_t dz = 0, sums = 0, x = 0, w = 0, w2 = 0, part = 0, total = 0;
 };
 
@@ -215,11 +229,13 @@ Space space(bool gated, bool backward, int64_t m, int64_t n, int64_t k) {
         return was;
     };
     if (backward) {
-        s.dz = take(two * row_bytes(m, n));
+        s.fold = m <= kFineRows ? int32_t(m) : 0;
+        s.dz = take(two * row_bytes(m + s.fold, n));
         s.sums = take(gated ? 0 : round_up(size_t(cdiv64(m, sum_rows(m, n))) * size_t(n) * 4));
         s.pack = worth_repacking(kDx, m, k, n, two, weights) ||
                  worth_repacking(kDw, n, k, m, two, m * k);
-        part = std::max(part_bytes(kDx, m, k, n, two), part_bytes(kDw, n, k, m, two));
+        part = std::max(part_bytes(kDx, m, k, n, two, s.fold),
+                        part_bytes(kDw, n, k, m + s.fold, two));
     } else {
         s.pack = worth_repacking(gated ? kPair : kRows, m, n, k, 1, weights + m * k);
         part = part_bytes(gated ? kPair : kRows, m, n, k, 1);
@@ -247,7 +263,7 @@ Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
 }
 
 int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
-    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p));
+    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p), p.fold);
     return type == DGC_BF16 ? Launch<__bf16>::product(p, c, ws, s)
                             : Launch<_Float16>::product(p, c, ws, s);
 }
@@ -267,7 +283,7 @@ int run_gradients(int64_t type, const Product& dx, const Product& dw, const Sums
     int rc = DGC_OK;
     if (has_dx && has_dw) {
         const bool d = direct(dx) && direct(dw);
-        const Cut cx = plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx));
+        const Cut cx = plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx), dx.fold);
         const Cut cw = plan_product(kDw, dw.m, dw.n, dw.k, dw.parts, direct(dw));
         const double apart = cx.us + cw.us + (sums.out ? 2 : 1) * kLaunchUs;  // without a first one
         double us = 0;
@@ -363,6 +379,7 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     if (copied) dz = {ws + sp.dz, pad8(n), true};
     SlopeArgs sl;
     Sums sums;
+    int32_t fold = 0;  // dz in two halves: where a slope made it
     if (copied || a->dbias) {
         sl.M = m;
         sl.N = n;
@@ -374,6 +391,8 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
         sl.act = int32_t(a->act);
         sl.dz = copied ? ws + sp.dz : nullptr;
         sl.ldz = pad8(n);
+        if (sloped && copied) fold = sp.fold;
+        sl.low = fold * sl.ldz;
         sl.part = a->dbias ? reinterpret_cast<float*>(ws + sp.sums) : nullptr;
         sums.rows = cdiv64(m, sl.per);
         sums.N = n;
@@ -390,12 +409,13 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     dx.k = n;
     dx.a[0] = dz;
     dx.b[0] = w;
+    dx.fold = dw.fold = fold;
     dx.fin.out[0] = a->dx;
     dx.fin.ldo = a->lddx;
     dw.form = kDw;
     dw.m = n;
     dw.n = k;
-    dw.k = m;
+    dw.k = m + fold;
     dw.a[0] = dz;
     dw.b[0] = x;
     dw.fin.out[0] = a->dw;
@@ -476,8 +496,9 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     sl.ldu = a->ldup;
     sl.act = int32_t(a->act);
     sl.dz = ws + sp.dz;
-    sl.dz2 = ws + sp.dz + row_bytes(m, f);
+    sl.dz2 = ws + sp.dz + row_bytes(m + sp.fold, f);
     sl.ldz = ld;
+    sl.low = sp.fold * ld;
     rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
     Product dx, dw;
@@ -486,6 +507,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     dx.m = m;
     dx.n = d;
     dx.k = f;
+    dx.fold = dw.fold = sp.fold;
     dx.b[0] = wg;
     dx.b[1] = wu;
     dx.fin.out[0] = a->dx;
@@ -494,7 +516,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     dw.parts = 2;
     dw.m = f;
     dw.n = d;
-    dw.k = m;
+    dw.k = m + sp.fold;
     dw.b[0] = x;
     dw.fin.out[0] = a->dw_gate;
     dw.fin.ldo = a->lddw_gate;

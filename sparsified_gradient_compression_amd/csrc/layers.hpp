@@ -53,6 +53,11 @@ struct Product {
     int64_t m = 0, n = 0, k = 0;
     int parts = 1;  // terms of kDx, outputs of kDw
     Mat a[2], b[2];
+    // Not 0: so many rows of dz, at most 32, come in two halves, all first halves
+    // before all second ones.  kDx: m = fold, a has 2 fold rows (those of a tile),
+    // and sums `fold` rows apart are added.  kDw: k = 2 fold (one step of 64), and
+    // b's fold rows are taken for either half.
+    int32_t fold = 0;
     Finish fin;
 };
 
@@ -84,14 +89,16 @@ struct Cut {
 bool direct(const Product& p);
 
 // From the sizes, and whether the operands' rows lie on 16 bytes.
-Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct);
+Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct,
+                 int fold = 0);
 
 // dz = dy * act'(pre), its rows padded with zeros to ldz, and the sums of its
 // columns over `per` rows each into `part` (either null: not wanted); with
 // `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums, `per` (4
-// or 8) elements per thread.
+// or 8) elements per thread.  low (not 0): what rounding dz and dz2 loses, so
+// many elements on.
 struct SlopeArgs {
-    int64_t M = 0, N = 0, per = 0;
+    int64_t M = 0, N = 0, per = 0, low = 0;
     const void *dy = nullptr, *pre = nullptr, *up = nullptr;
     int64_t lddy = 0, ldp = 0, ldu = 0, ldz = 0;
     void *dz = nullptr, *dz2 = nullptr;

@@ -56,8 +56,9 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     Side<T, BTR, 2, true, 128, 8> sb[2];
     const int64_t lda = A.lda[0], ldb = A.ldb[0];
     for (int h = 0; h < 2; ++h) {
-        sa[h].init(lda, A.M - m0 - h * 128, wave, lane, wm * 64);
-        sb[h].init(ldb, A.N - n0 - (PAIR ? 0 : h * 128), wave, lane, wn * 32);
+        sa[h].init(lda, a_rows<FORM>(A) - m0 - h * 128, wave, lane, wm * 64);
+        sb[h].init(ldb, A.N - n0 - (PAIR ? 0 : h * 128), wave, lane, wn * 32,
+                   FORM == kDw ? A.fold : 0);
     }
 
     // Half h of tile t.  Beyond the last tile nothing is read, but the loads

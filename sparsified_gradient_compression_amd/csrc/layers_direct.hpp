@@ -29,7 +29,9 @@ struct Side : Frags<T, TR, NT, NSIDE, R> {
     int k_at;             // first k of the lane's piece (TR: of load 0)
 
     // have: how many rows (columns) there are from the region's first on
-    __device__ __forceinline__ void init(int64_t ld, int64_t have, int wave, int lane, int base) {
+    // fold (TR): steps of k from there on are the first ones again
+    __device__ __forceinline__ void init(int64_t ld, int64_t have, int wave, int lane, int base,
+                                         int fold = 0) {
         Frags<T, TR, NT, NSIDE, R>::init(lane, base);
         if constexpr (TR) {
             constexpr int kPer = R / 8;  // pieces of a step of k
@@ -37,10 +39,11 @@ struct Side : Frags<T, TR, NT, NSIDE, R> {
             const int piece = (((p >> 1) ^ k_key<R>(k)) << 1) | (p & 1);
             k_at = k;
 #pragma unroll
-            for (int l = 0; l < kLoads; ++l)
-                at[l] = piece * 8 < have
-                            ? uint32_t((int64_t(k + kRowsK * l) * ld + piece * 8) * 2)
-                            : kOutside;
+            for (int l = 0; l < kLoads; ++l) {
+                const int row = k + kRowsK * l, from = fold && row >= fold ? row - fold : row;
+                at[l] = piece * 8 < have ? uint32_t((int64_t(from) * ld + piece * 8) * 2)
+                                         : kOutside;
+            }
         } else {
             const int r = wave * 8 + (lane >> 3);
             const int piece = (lane & 7) ^ row_key<NT, NSIDE>(r);

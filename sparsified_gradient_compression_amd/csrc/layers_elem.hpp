@@ -3,9 +3,13 @@
 // laid out anew.
 //
 // The products that follow take 16-bit operands, so dz (da, db) is rounded
-// once to the elements' own type here, as the incoming gradient was: a
-// relative 2^-9 (bf16) or 2^-12 (fp16) at random per element, no more than
-// the rounding of the output that it is summed into.
+// once to the elements' own type here, as the incoming gradient was: half a
+// step at most, 2^-8 (bf16) or 2^-11 (fp16) of the element, as much as the
+// rounding of the output that it is summed into; together 1.4 times one of
+// them.  For few rows, where the products are bound by reading the weight and
+// few roundings have to even out, what is lost is kept in a second half of 16
+// bits (`low` elements on) and multiplied too, in places of the same tiles
+// that would be empty.
 #pragma once
 
 #include "layers_tile.hpp"
@@ -13,10 +17,31 @@
 namespace dgc {
 namespace layers {
 
+// C values rounded to T, and with HALVES what that loses of each, `low` elements
+// on: nothing of a value that has become infinite.  The rounded value is made
+// once for both: made again from the product before it, it may be another.
+// (A template: the few rows' registers would cost the many 3% of their rate.)
+template <class T, int C, bool HALVES>
+__device__ __forceinline__ void store_halves(T* p, int64_t low, const float* v) {
+    if constexpr (!HALVES) {
+        store_row<T, C>(p, C, v);
+        return;
+    }
+    float high[C], rest[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        high[i] = float(T(v[i]));
+        asm("" : "+v"(high[i]));
+        rest[i] = fabsf(high[i]) < __builtin_inff() ? v[i] - high[i] : 0.0f;
+    }
+    store_row<T, C>(p, C, high);
+    store_row<T, C>(p + low, C, rest);
+}
+
 // dz = dy * act'(pre) and the sums of dz's columns (before it is rounded) over
 // `per` rows each.  A block of 256 threads covers 512 columns (64 threads, 8
 // columns each) by `per` rows (4 rows of threads).
-template <class T>
+template <class T, bool HALVES>
 __device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, float (*sums)[512]) {
     const int64_t across = (A.N + 511) / 512;
     const int64_t by = id / across, bx = id - by * across;
@@ -51,7 +76,7 @@ __device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, floa
                         }
                     }
                     // zeros in the padding
-                    if (dz) store_row<T, 8>(dz + (m + 4 * r) * A.ldz + n, 8, d[r]);
+                    if (dz) store_halves<T, 8, HALVES>(dz + (m + 4 * r) * A.ldz + n, A.low, d[r]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += d[r][i];
                 }
@@ -98,7 +123,7 @@ __global__ __launch_bounds__(256) void k_sum_columns(Sums A) {
 
 // da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; C (4
 // or 8) elements per thread.
-template <class T, int C>
+template <class T, int C, bool HALVES>
 __device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id) {
     const int64_t groups = A.ldz / C;
     id = id * 256 + threadIdx.x;
@@ -117,8 +142,8 @@ __device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id)
         ob[i] = d[i] * value;
     }
     // zeros in the padding
-    store_row<T, C>(static_cast<T*>(A.dz) + m * A.ldz + n, C, oa);
-    store_row<T, C>(static_cast<T*>(A.dz2) + m * A.ldz + n, C, ob);
+    store_halves<T, C, HALVES>(static_cast<T*>(A.dz) + m * A.ldz + n, A.low, oa);
+    store_halves<T, C, HALVES>(static_cast<T*>(A.dz2) + m * A.ldz + n, A.low, ob);
 }
 
 // Rows at any even address to rows on 16 bytes, zeros up to their ends; 8
@@ -149,18 +174,18 @@ __device__ __forceinline__ void repack_block(const Repack& r, int64_t id) {
 }
 
 // What a call lays out before its products, in one launch.
-template <class T>
+template <class T, bool HALVES>
 __global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_blocks, Repack r) {
     __shared__ float sums[4][512];
     const int64_t id = blockIdx.x;
     if (id >= slope_blocks)
         repack_block(r, id - slope_blocks);
     else if (A.up && A.per == 4)
-        gate_slope_block<T, 4>(A, id);
+        gate_slope_block<T, 4, HALVES>(A, id);
     else if (A.up)
-        gate_slope_block<T, 8>(A, id);
+        gate_slope_block<T, 8, HALVES>(A, id);
     else
-        slope_block<T>(A, id, sums);
+        slope_block<T, HALVES>(A, id, sums);
 }
 
 }  // namespace layers

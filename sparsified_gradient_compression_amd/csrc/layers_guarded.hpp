@@ -19,8 +19,9 @@ struct Guarded {
     int have[2];     // TR: how many of its 8 columns exist; else 1 if its row does
     int k_at[2];     // its first k in a tile
 
+    // fold (TR): steps of k from there on are the first ones again
     __device__ __forceinline__ void init(const T* base, int64_t ld, int64_t first, int64_t rows,
-                                         int tid) {
+                                         int tid, int fold = 0) {
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
             const int c = tid + l * 256;
@@ -28,7 +29,7 @@ struct Guarded {
                 k_at[l] = c >> 3;
                 const int64_t col = first + (c & 7) * 8;
                 have[l] = rows - col >= 8 ? 8 : rows > col ? int(rows - col) : 0;
-                p[l] = base + k_at[l] * ld + col;
+                p[l] = base + (fold && k_at[l] >= fold ? k_at[l] - fold : k_at[l]) * ld + col;
             } else {
                 k_at[l] = (c & 7) * 8;
                 have[l] = first + (c >> 3) < rows;
@@ -106,9 +107,10 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem)
     for (int w = 0; w < (FORM == kDx ? 2 : 1); ++w) {
         if (w >= A.parts) break;
         ga[w].init(static_cast<const T*>(A.a[FORM == kDw ? z : w]), A.lda[FORM == kDw ? z : w],
-                   m0, A.M, tid);
+                   m0, a_rows<FORM>(A), tid);
         if constexpr (!PAIR)
-            gb[w].init(static_cast<const T*>(A.b[w]), A.ldb[w], n0, A.N, tid);
+            gb[w].init(static_cast<const T*>(A.b[w]), A.ldb[w], n0, A.N, tid,
+                       FORM == kDw ? A.fold : 0);
     }
     if constexpr (PAIR) {
 #pragma unroll

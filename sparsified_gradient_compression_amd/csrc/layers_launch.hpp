@@ -58,6 +58,7 @@ inline TileArgs tile_args(const Product& p, const Cut& c, void* ws) {
     a.splits = c.splits;
     a.parts = p.parts;
     a.outs = p.form == kDw ? p.parts : 1;
+    a.fold = p.fold;
     a.part = c.splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.fin = p.fin;
     return a;
@@ -123,7 +124,8 @@ int Launch<T>::prepare(const SlopeArgs& a, const Repack& r, hipStream_t s) {
     const int64_t blocks = slopes + cdiv64(pieces, 256);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (blocks == 0) return DGC_OK;
-    k_prepare<T><<<dim3(static_cast<unsigned>(blocks)), 256, 0, s>>>(a, slopes, r);
+    const auto kernel = a.low ? k_prepare<T, true> : k_prepare<T, false>;
+    kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, s>>>(a, slopes, r);
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }

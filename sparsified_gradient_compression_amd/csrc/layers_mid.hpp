@@ -64,8 +64,8 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1
     Side<T, ATR, MT, false, BM, W> sa;
     Side<T, BTR, NT, true, RB, W> sb;
     const int64_t lda = A.lda[0], ldb = A.ldb[0];
-    sa.init(lda, A.M - m0, wave, lane, wm * MT * 16);
-    sb.init(ldb, A.N - n0, wave, lane, wn * NT * 16);
+    sa.init(lda, a_rows<FORM>(A) - m0, wave, lane, wm * MT * 16);
+    sb.init(ldb, A.N - n0, wave, lane, wn * NT * 16, FORM == kDw ? A.fold : 0);
     constexpr int kLoads = decltype(sa)::kLoads + (PAIR ? 2 : 1) * decltype(sb)::kLoads;
 
     // The group's tile of round r; nothing is read beyond the last one.

@@ -53,23 +53,29 @@ constexpr int kStep = 64;  // k per LDS tile
 
 // All are z times a share of it that lies between 0 and 1: 1 / (1 + exp(-q))
 // or the normal distribution's integral.  The hardware's exp2 and reciprocal
-// are off by a step or two of binary32, and the integral by 8e-8 (Abramowitz
-// and Stegun, Handbook of Mathematical Functions, 7.1.26), far less than a
-// step of the 16-bit types; a finish takes a dozen instructions per element
-// instead of the fifty of the correctly rounded functions.
+// are off by a step or two of binary32, far less than a step of the 16-bit
+// types; a finish takes a dozen instructions per element instead of the fifty
+// of the correctly rounded functions.
 
 __device__ __forceinline__ float sigmoid(float q) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(q * -1.44269504f));
 }
 
-// The integral of the normal density up to z, and exp(-z^2 / 2).
+// The integral of the normal density up to z, and exp(-z^2 / 2).  The tail
+// beyond |z| is exp(-x^2) times a slow function of x = |z| / sqrt(2), here a
+// polynomial of 1 / (1 + c x) without a constant: all seven numbers by a
+// minimax fit of the relative error for x up to 14, weighted 30 times higher
+// up to x = 1 than from 2.5 on.  Off by 6e-7 of 1, and by 3e-5 of the tail
+// itself, so that gelu's small values far below 0 keep a 16-bit type's
+// precision.
 __device__ __forceinline__ float normal_share(float z, float& e) {
     const float x = fabsf(z) * 0.70710678f;
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.42687309f * x);
     e = __builtin_amdgcn_exp2f(x * x * -1.44269504f);
     const float p =
-        t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * p * e;
+        t * (0.12072082f + t * (0.11535566f + t * (0.14152817f + t * (-0.011156623f +
+             t * (0.21107882f + t * -0.077527322f)))));
+    const float tail = p * e;
     return z < 0.0f ? tail : 1.0f - tail;
 }
 
@@ -112,7 +118,9 @@ __device__ __forceinline__ void act_pair(int act, float z, float& value, float& 
         case DGC_ACT_GELU_TANH: {
             const float p = sigmoid(tanh_twice(z));
             value = z * p;
-            slope = p + value * (1.0f - p) * 1.59576912f * (1.0f + 0.134145f * z * z);
+            // bounded, so that a 0 before it makes it 0 for the largest z too
+            const float square = fminf(z * z, 1e30f);
+            slope = p + value * (1.0f - p) * 1.59576912f * (1.0f + 0.134145f * square);
             break;
         }
         default: value = z; slope = 1.0f;
@@ -325,9 +333,16 @@ struct TileArgs {
     int64_t mt, nt;        // tiles over m and n
     int64_t per;           // steps of 64 per workgroup along the long axis
     int32_t splits, parts, outs;  // outs: outputs of kDw, else 1
+    int32_t fold;          // rows of dz in two halves (Product), or 0
     float* part;           // the splits' sums, or null
     Finish fin;
 };
+
+// How many rows a has (kDw: columns).
+template <int FORM>
+__device__ __forceinline__ int64_t a_rows(const TileArgs& A) {
+    return FORM == kDx && A.fold ? 2 * A.fold : A.M;
+}
 
 // Where workgroup `id` of a product works.  Workgroups go to the 8 dies in
 // turn, each with an L2 of its own: die x takes the x-th eighth of the splits,
@@ -383,6 +398,13 @@ __device__ __forceinline__ void put_rows(const TileArgs& A, int split, int z, in
     float bias[8];
     if (!PAIR && f.bias) load_row<T, 8>(static_cast<const T*>(f.bias) + n, valid, bias);
     const int rows = A.M - m0 < ROWS ? int(A.M - m0) : ROWS;
+    const int fold = FORM == kDx ? A.fold : 0;
+    const auto sum = [&](int r, int col4) {
+        const float* p = at(r) + out_at(r, col4);
+        f32x4 t = *reinterpret_cast<const f32x4*>(p);
+        for (int w = 1; w < groups; ++w) t += *reinterpret_cast<const f32x4*>(p + w * stride);
+        return t;
+    };
 #pragma unroll 1
     for (int first = threadIdx.x / kLanes; first < rows; first += kAhead * kStepRows) {
         float residual[kAhead][8];
@@ -399,17 +421,11 @@ __device__ __forceinline__ void put_rows(const TileArgs& A, int split, int z, in
             const int r = first + u * kStepRows;
             if (r >= rows) break;
             float v[8], v2[8];
-            const float* row = at(r);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const float* p = row + out_at(r, 2 * c + q);
-                const float* p2 = row + out_at(r, 2 * c + q + COLS / 8);
-                f32x4 t = *reinterpret_cast<const f32x4*>(p), t2 = {0, 0, 0, 0};
-                if (PAIR) t2 = *reinterpret_cast<const f32x4*>(p2);
-                for (int w = 1; w < groups; ++w) {
-                    t += *reinterpret_cast<const f32x4*>(p + w * stride);
-                    if (PAIR) t2 += *reinterpret_cast<const f32x4*>(p2 + w * stride);
-                }
+                f32x4 t = sum(r, 2 * c + q), t2 = {0, 0, 0, 0};
+                if (PAIR) t2 = sum(r, 2 * c + q + COLS / 8);
+                if (fold) t += sum(r + fold, 2 * c + q);
                 *reinterpret_cast<f32x4*>(v + 4 * q) = t;
                 *reinterpret_cast<f32x4*>(v2 + 4 * q) = t2;
             }
