@@ -582,13 +582,14 @@ def _torch_calls():
 
 
 def _stream_on(x, stream) -> int:
-    """The handle of `stream`, or of the current stream of x's device."""
-    if stream is None:
-        import torch
-        if not x.is_cuda:
-            return 0  # refused by the call itself
-        return torch._C._cuda_getCurrentRawStream(x.get_device())
-    return _stream(stream)
+    """The handle of `stream`, or of the current stream of x's device, which has to be the current one: kernels go there."""
+    import torch
+    if not x.is_cuda:
+        return 0  # refused by the call itself
+    device = x.get_device()
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {device}, the current device is {torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _fresh(size: int, x, stream):
@@ -725,6 +726,13 @@ class GradSet:
                                       self.workspace.numel(), _stream(stream)), "dgc_gradset_init")
         self.set = handle
 
+    def _on(self, stream) -> int:
+        """The handle of `stream`, which the set's own tensors are held for."""
+        handle = _stream_on(self.total, stream)
+        for t in (self.workspace, self.total, self.scale):
+            _hold(t, stream)
+        return handle
+
     @staticmethod
     def _norm(norm: str) -> int:
         code = NORMS.get(norm)
@@ -735,7 +743,7 @@ class GradSet:
     def norm(self, grads: Sequence, norm: str = "l2", unscale: float = 1.0, stream=None):
         """unscale * the norm over all gradients, as a float64 tensor of one element."""
         _check(_torch_calls().set_norm(self.set.value, *self._layout, grads, self._norm(norm), unscale, self.total,
-                                       _stream_on(self.total, stream)), "dgc_gradset_norm")
+                                       self._on(stream)), "dgc_gradset_norm")
         return self.total
 
     def clip(self, grads: Sequence, clip: float, out: Optional[Sequence] = None, norm: str = "l2",
@@ -743,14 +751,14 @@ class GradSet:
         """out[t] = grads[t] * scale (in place without `out`), scale = unscale * min(1, clip / norm), for
         clip > 0.  Returns the norm."""
         _check(_torch_calls().set_clip(self.set.value, *self._layout, grads, out, clip, self._norm(norm), unscale,
-                                       self.total, self.scale, _stream_on(self.total, stream)), "dgc_gradset_clip")
+                                       self.total, self.scale, self._on(stream)), "dgc_gradset_clip")
         return self.total
 
     def pack(self, grads: Sequence, flat, clip: float, norm: str = "l2", unscale: float = 1.0, stream=None):
         """The clipped gradients in float32, end to end in `flat`: what Learner.compress takes (with its own
         clip 0).  Returns the norm."""
         _check(_torch_calls().set_pack(self.set.value, *self._layout, grads, flat, clip, self._norm(norm), unscale,
-                                       self.total, self.scale, _stream_on(self.total, stream)), "dgc_gradset_pack")
+                                       self.total, self.scale, self._on(stream)), "dgc_gradset_pack")
         return self.total
 
     def close(self):

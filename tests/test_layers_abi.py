@@ -181,3 +181,18 @@ def test_host_code_under_asan_ubsan(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=600)
     assert r.returncode == 0, (r.stdout[-1000:], r.stderr[-3000:])
     assert "host check: ok" in r.stdout
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    """Kernels are launched on the current device: tensors of another are not handed to it."""
+    class Elsewhere:
+        is_cuda = True
+
+        @staticmethod
+        def get_device():
+            return 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for stream in (None, 0):
+        with pytest.raises(ValueError, match="device 1, the current device is 0"):
+            dgc._stream_on(Elsewhere(), stream)
