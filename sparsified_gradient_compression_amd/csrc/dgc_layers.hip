@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "layers.hpp"
 
@@ -28,14 +29,14 @@ namespace {
 // products of 64 to 8192 rows and columns, in microseconds:
 //                        kMid32 kMid64 kLight kMid128 kPair128 kBig  kGuarded
 //   64 x 704, k 704         5.6    5.5     6.4     8.0      8.6    19       7.2
-//   1024 x 1024, k 64        10    5.0     4.2     6.2      5.8    15       6.4
-//   1024 x 1024, k 1024      12    6.9     8.5      11       12    27       9.2
-//   2048 x 2048, k 2048      57     35      26      20       28    42        47
-//   3000 x 1500, k 3000      97     78      70      62       51    65
+//   1024 x 1024, k 64        10    5.0     4.2     6.2      4.9    15       6.4
+//   1024 x 1024, k 1024      12    6.9     8.5      11       14    27       9.2
+//   2048 x 2048, k 2048      57     35      26      20       26    42        47
+//   3000 x 1500, k 3000      97     78      70      62       46    65
 //   858 x 696, k 14336       89     54     119     100      175   279
 //     split in 4 and joined  72     51      44      35       50    84
-//   4096 x 4096, k 64       120     51      18      20       14    17        67
-//   4096 x 4096, k 2048     221    132              75       66    53
+//   4096 x 4096, k 64       120     51      18      20       13    17        67
+//   4096 x 4096, k 2048     221    132      95      75       64    53
 // Off 16 bytes a step of kGuarded takes half as long again.
 struct Cost {
     int tile;
@@ -45,7 +46,7 @@ struct Cost {
 constexpr Cost kCosts[] = {
     {kGuarded, 256, 256, 2.6, 0.40, 2.6, 0.40}, {kMid32, 256, 256, 3.4, 0.13, 3.4, 0.13},
     {kMid64, 256, 256, 2.2, 0.21, 2.2, 0.21},   {kMid128, 256, 256, 3.8, 0.45, 3.8, 0.45},
-    {kPair128, 512, 256, 5.0, 0.84, 3.5, 0.70}, {kBig, 256, 128, 11.0, 1.28, 9.0, 1.05},
+    {kPair128, 512, 256, 5.0, 0.80, 3.5, 0.62}, {kBig, 256, 128, 11.0, 1.28, 9.0, 1.05},
     {kLight, 1280, 640, 4.0, 1.25, 2.5, 0.45}};
 constexpr double kLaunchUs = 2.5;  // of a launch, or between two
 
@@ -116,6 +117,51 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
 
 namespace {
 
+// When the last of nx workgroups of ux microseconds each, and behind them nw of
+// uw, ends on `slots` places.
+double queue_us(int64_t slots, int64_t nx, double ux, int64_t nw, double uw) {
+    const double full = double(nx / slots) * ux;
+    const int64_t ex = nx % slots, free = slots - ex;
+    double end = full + (ex > 0 ? ux : 0);
+    if (nw == 0) return end;
+    // the first time by which all nw have ended: a multiple of uw from either
+    // moment at which places become free
+    const auto ended = [&](double t) {
+        const auto each = [&](double from) { return int64_t(std::max(0.0, (t - from) / uw + 1e-6)); };
+        return free * each(full) + ex * each(full + ux);
+    };
+    const auto first = [&](double from, int64_t places) {
+        if (places == 0) return 1e30;
+        int64_t low = std::max<int64_t>(nw / slots - int64_t(ux / uw) - 1, 0);
+        int64_t high = std::max(cdiv64(nw, places), low);
+        while (low < high) {
+            const int64_t mid = low + (high - low) / 2;
+            if (ended(from + double(mid) * uw) >= nw)
+                high = mid;
+            else
+                low = mid + 1;
+        }
+        return from + double(low) * uw;
+    };
+    return std::max(end, std::min(first(full, free), first(full + ux, ex)));
+}
+
+// Both gradients in one launch, dx's workgroups first: sx and sw steps each.
+// Gates' gradients (1531 x 3840 x 1280, 120 and 300 tiles of 128; expected and
+// measured): kMid128 48.6 and 48.2, kPair128 46.5 and 46.7.
+double both_us(const Cost& c, int64_t nx, double sx, int64_t nw, double sw) {
+    if (nx + nw <= c.light) return c.light_start + c.light_step * std::max(sx, sw);
+    if (nx + nw <= c.round) {  // all at once, and then the longer ones alone
+        const int64_t longer = sx > sw ? nx : nw;
+        return c.start + c.step * std::min(sx, sw) +
+               std::fabs(sx - sw) * (longer <= c.light ? c.light_step : c.step);
+    }
+    // operands that are turned on their way to the registers: 2048 x 2048, k
+    // 8192 takes 73 us with neither, 74-85 as a dx and 81-97 as a dw
+    const double step = c.tile == kMid128 ? 1.15 * c.step : c.step;
+    return queue_us(c.round, nx, c.start + step * sx, nw, c.start + step * sw);
+}
+
 // The kernel that takes both gradients of a layer in the least time, together.
 int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
     int tile = kGuarded;
@@ -126,14 +172,8 @@ int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
         if ((c.tile == kGuarded) == direct || c.tile == kBig) continue;
         const TileSize t = kTileSize[c.tile];
         if (!takes(t, kDx, dx.fold)) continue;
-        const double nx = double(cdiv64(dx.m, t.m) * cdiv64(dx.n, t.n));
-        const double nw = double(cdiv64(dw.m, t.m) * cdiv64(dw.n, t.n) * dw.parts);
-        // workgroups of both kinds fill up the rounds, the last one in part
-        const double ux = c.start + c.step * sx, uw = c.start + c.step * sw;
-        const double us = nx + nw <= double(c.light)
-                              ? c.light_start + c.light_step * std::max(sx, sw)
-                              : std::max((nx * ux + nw * uw) / double(c.round) + c.start / 2,
-                                         std::max(ux, uw));
+        const double us = both_us(c, cdiv64(dx.m, t.m) * cdiv64(dx.n, t.n), sx,
+                                  cdiv64(dw.m, t.m) * cdiv64(dw.n, t.n) * dw.parts, sw);
         if (us < best) {
             best = us;
             tile = c.tile;
