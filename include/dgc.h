@@ -595,7 +595,10 @@ typedef struct dgc_linear_args {
  * are of grad_type: `type`, or DGC_FP32 (a learner's flat gradient).  pre is
  * not read for DGC_ACT_NONE; for other activations dz is rounded to `type`
  * before the products (up to 32 rows: to the sum of two numbers of `type`),
- * not before the column sums. */
+ * not before the column sums.  DGC_FP16: times a power of two that brings the
+ * call's largest finite |dz| into [2^14, 2^15), undone afterwards, so that dz
+ * may leave the range of `type` and a small one loses at most 2^-39 of the
+ * largest. */
 typedef struct dgc_linear_backward_args {
     int64_t type, grad_type, act, m, n, k;
     const void* dy;
@@ -632,8 +635,9 @@ typedef struct dgc_gated_ffn_args {
 } dgc_gated_ffn_args;
 
 /* With da = dh * up * act'(gate) and db = dh * act(gate), both rounded to
- * `type` (up to 32 rows: to the sum of two numbers of `type`): dx[m][d] = da w_gate + db w_up, dw_gate[f][d] = da^T x,
- * dw_up = db^T x.  dx may be NULL, and dw_gate and dw_up together. */
+ * `type` (up to 32 rows: to the sum of two numbers of `type`; DGC_FP16: scaled
+ * as above, by the larger of both): dx[m][d] = da w_gate + db w_up,
+ * dw_gate[f][d] = da^T x, dw_up = db^T x.  dx may be NULL, and dw_gate and dw_up together. */
 typedef struct dgc_gated_ffn_backward_args {
     int64_t type, grad_type, act, m, d, f;
     const void* dh;

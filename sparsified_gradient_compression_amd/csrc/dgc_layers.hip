@@ -250,12 +250,13 @@ size_t row_bytes(int64_t rows, int64_t cols) {
 // their own without, where many rows' have 1.4.
 constexpr int64_t kFineRows = 32;
 
-// Where a call keeps what it lays out: dz (da, db), column sums, operands that
-// are repacked, and splits.  From the sizes alone.
+// Where a call keeps what it lays out: dz (da, db), column sums, dz's partial
+// maxima and the factor that its scale is undone by, operands that are
+// repacked, and splits.  From the sizes alone.
 struct Space {
     bool pack = false;
     int32_t fold = 0;  // rows of dz, where it is kept in two halves
-    size_t dz = 0, sums = 0, x = 0, w = 0, w2 = 0, part = 0, total = 0;
+    size_t dz = 0, sums = 0, most = 0, x = 0, w = 0, w2 = 0, part = 0, total = 0;
 };
 
 Space space(bool gated, bool backward, int64_t m, int64_t n, int64_t k) {
@@ -272,6 +273,7 @@ Space space(bool gated, bool backward, int64_t m, int64_t n, int64_t k) {
         s.fold = m <= kFineRows ? int32_t(m) : 0;
         s.dz = take(two * row_bytes(m + s.fold, n));
         s.sums = take(gated ? 0 : round_up(size_t(cdiv64(m, sum_rows(m, n))) * size_t(n) * 4));
+        s.most = take(m > 0 && n > 0 ? round_up((kMostParts + 1) * sizeof(float)) : 0);
         s.pack = worth_repacking(kDx, m, k, n, two, weights) ||
                  worth_repacking(kDw, n, k, m, two, m * k);
         part = std::max(part_bytes(kDx, m, k, n, two, s.fold),
@@ -306,6 +308,13 @@ int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
     const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p), p.fold);
     return type == DGC_BF16 ? Launch<__bf16>::product(p, c, ws, s)
                             : Launch<_Float16>::product(p, c, ws, s);
+}
+
+// fp16 holds a dz that is a product of fp16 numbers only after a scale.
+void scale_dz(int64_t type, SlopeArgs& a, char* space) {
+    if (type != DGC_FP16 || a.M == 0 || a.N == 0) return;
+    a.most = reinterpret_cast<float*>(space);
+    a.unscale = a.most + kMostParts;
 }
 
 int run_prepare(int64_t type, const SlopeArgs& a, const Repack& r, hipStream_t s) {
@@ -431,7 +440,10 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
         sl.act = int32_t(a->act);
         sl.dz = copied ? ws + sp.dz : nullptr;
         sl.ldz = pad8(n);
-        if (sloped && copied) fold = sp.fold;
+        if (sloped && copied) {
+            fold = sp.fold;
+            scale_dz(a->type, sl, ws + sp.most);
+        }
         sl.low = fold * sl.ldz;
         sl.part = a->dbias ? reinterpret_cast<float*>(ws + sp.sums) : nullptr;
         sums.rows = cdiv64(m, sl.per);
@@ -452,6 +464,7 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     dx.fold = dw.fold = fold;
     dx.fin.out[0] = a->dx;
     dx.fin.ldo = a->lddx;
+    dx.fin.unscale = dw.fin.unscale = sl.unscale;
     dw.form = kDw;
     dw.m = n;
     dw.n = k;
@@ -539,6 +552,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     sl.dz2 = ws + sp.dz + row_bytes(m + sp.fold, f);
     sl.ldz = ld;
     sl.low = sp.fold * ld;
+    scale_dz(a->type, sl, ws + sp.most);
     rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
     Product dx, dw;
@@ -552,6 +566,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     dx.b[1] = wu;
     dx.fin.out[0] = a->dx;
     dx.fin.ldo = a->lddx;
+    dx.fin.unscale = dw.fin.unscale = sl.unscale;
     dw.form = kDw;
     dw.parts = 2;
     dw.m = f;

@@ -39,6 +39,7 @@ struct Finish {
     int64_t ldp[2] = {0, 0};
     int32_t act = 0;
     int32_t wide = 0;  // outputs in binary32
+    const float* unscale = nullptr;  // dx, dw: of dz times a power of two, its reciprocal; or null
 };
 
 // What a product's operands look like.
@@ -92,18 +93,23 @@ bool direct(const Product& p);
 Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct,
                  int fold = 0);
 
+constexpr int kMostParts = 512;
+
 // dz = dy * act'(pre), its rows padded with zeros to ldz, and the sums of its
 // columns over `per` rows each into `part` (either null: not wanted); with
 // `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums, `per` (4
 // or 8) elements per thread.  low (not 0): what rounding dz and dz2 loses, so
-// many elements on.
+// many elements on.  most (fp16; or null): space for kMostParts partial maxima
+// of |dz| and |dz2|; they are then stored times the power of two that brings
+// the largest into [2^14, 2^15), and its reciprocal goes to `unscale`.
 struct SlopeArgs {
     int64_t M = 0, N = 0, per = 0, low = 0;
     const void *dy = nullptr, *pre = nullptr, *up = nullptr;
     int64_t lddy = 0, ldp = 0, ldu = 0, ldz = 0;
     void *dz = nullptr, *dz2 = nullptr;
     float* part = nullptr;
-    int32_t act = 0;
+    float *most = nullptr, *unscale = nullptr;
+    int32_t act = 0, parts = 0;  // parts: how many of `most` there are
 };
 
 // The partial column sums, to be added up into `out` (null: none).
@@ -138,8 +144,9 @@ struct Launch {
     // column sums in one launch
     static int both(const Product& dx, const Product& dw, int tile, const Sums& sums,
                     hipStream_t s);
-    // slopes (none if a.N is 0) and rows laid out anew in one launch
-    static int prepare(const SlopeArgs& a, const Repack& r, hipStream_t s);
+    // slopes (none if a.N is 0) and rows laid out anew in one launch; the largest
+    // |dz| in one before, where it is asked for
+    static int prepare(SlopeArgs a, const Repack& r, hipStream_t s);
     static int sum(const Sums& a, hipStream_t s);
 };
 

@@ -2,6 +2,9 @@
 // element type's source file instantiates it.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "layers_big.hpp"
 #include "layers_guarded.hpp"
 #include "layers_mid.hpp"
@@ -116,7 +119,7 @@ int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& 
 }
 
 template <class T>
-int Launch<T>::prepare(const SlopeArgs& a, const Repack& r, hipStream_t s) {
+int Launch<T>::prepare(SlopeArgs a, const Repack& r, hipStream_t s) {
     int64_t slopes = 0, pieces = 0;
     if (a.M > 0 && a.N > 0)
         slopes = a.up ? cdiv64(a.ldz / a.per * a.M, 256) : cdiv64(a.N, 512) * cdiv64(a.M, a.per);
@@ -124,6 +127,15 @@ int Launch<T>::prepare(const SlopeArgs& a, const Repack& r, hipStream_t s) {
     const int64_t blocks = slopes + cdiv64(pieces, 256);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (blocks == 0) return DGC_OK;
+    if constexpr (std::is_same_v<T, _Float16>) {
+        if (a.most && slopes > 0) {
+            int across = 1;
+            while (across < 256 && across * 8 < a.N) across *= 2;
+            a.parts = int32_t(std::min<int64_t>(kMostParts, cdiv64(a.M, 256 / across)));
+            k_most<T><<<dim3(unsigned(a.parts)), 256, 0, s>>>(a, across);
+            DGC_LAYERS_CHECK();
+        }
+    }
     const auto kernel = a.low ? k_prepare<T, true> : k_prepare<T, false>;
     kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, s>>>(a, slopes, r);
     DGC_LAYERS_CHECK();

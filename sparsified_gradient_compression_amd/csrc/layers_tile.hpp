@@ -211,7 +211,14 @@ __device__ __forceinline__ void finish_row(const Finish& f, int z, int64_t m, in
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = act_value(f.act, v[i]) * v2[i];
         store_row<T, C>(static_cast<T*>(f.out[0]) + m * f.ldo + n, valid, v);
-    } else if (f.wide) {
+        return;
+    }
+    if (f.unscale) {
+        const float u = *f.unscale;
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] *= u;
+    }
+    if (f.wide) {
         store_wide<C>(static_cast<float*>(f.out[z]) + m * (z ? f.ldo2 : f.ldo) + n, valid, v);
     } else {
         if (f.bias) {
