@@ -30,10 +30,31 @@
 namespace dgc {
 namespace layers {
 
-// C values rounded to T, and with HALVES what that loses of each, `low` elements
-// on: nothing of a value that has become infinite.  The rounded value is made
-// once for both: made again from the product before it, it may be another.
-// (A template: the few rows' registers would cost the many 3% of their rate.)
+// v as the sum of two numbers of T, both of v's sign and neither 0 (unless v
+// is): the high one lies below v in magnitude, also where T holds v itself.  So
+// both products with an infinite operand are the infinity that v's is; a second
+// half that is 0 or of the other sign would make it NaN.  The sum is off by half
+// a step of the second half, 2^-16 (bf16) or 2^-22 (fp16) of v, or by two of T's
+// least numbers.  An infinite or NaN v is both halves.
+template <class T>
+__device__ __forceinline__ void split(float v, float& high, float& rest) {
+    asm("" : "+v"(v));  // rounded once: T made from the product before it may be another number
+    high = float(T(v));
+    rest = high;
+    if (!(fabsf(v) < __builtin_inff()) || v == 0.0f) return;
+    const uint16_t least = __builtin_bit_cast(uint32_t, v) >> 31 << 15 | 1;
+    uint16_t h = __builtin_bit_cast(uint16_t, T(v));
+    if (fabsf(high) >= fabsf(v)) --h;  // a step towards 0
+    if ((h & 0x7FFF) == 0) h = least;
+    high = float(__builtin_bit_cast(T, h));
+    uint16_t r = __builtin_bit_cast(uint16_t, T(v - high));
+    if ((r & 0x7FFF) == 0 || r >> 15 != least >> 15) r = least;
+    rest = float(__builtin_bit_cast(T, r));
+}
+
+// C values rounded to T, or with HALVES split, the second halves `low`
+// elements on.  (A template: the few rows' registers would cost the many 3% of
+// their rate.)
 template <class T, int C, bool HALVES>
 __device__ __forceinline__ void store_halves(T* p, int64_t low, const float* v) {
     if constexpr (!HALVES) {
@@ -42,11 +63,7 @@ __device__ __forceinline__ void store_halves(T* p, int64_t low, const float* v) 
     }
     float high[C], rest[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        high[i] = float(T(v[i]));
-        asm("" : "+v"(high[i]));
-        rest[i] = fabsf(high[i]) < __builtin_inff() ? v[i] - high[i] : 0.0f;
-    }
+    for (int i = 0; i < C; ++i) split<T>(v[i], high[i], rest[i]);
     store_row<T, C>(p, C, high);
     store_row<T, C>(p + low, C, rest);
 }
