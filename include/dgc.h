@@ -131,6 +131,13 @@ extern "C" {
 #define DGC_ACT_SILU 2      /* z / (1 + exp(-z)) */
 #define DGC_ACT_GELU 3      /* z (1 + erf(z / sqrt 2)) / 2 */
 #define DGC_ACT_GELU_TANH 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+/* Added to the activation of a *_backward call: dz (da, db) is rounded to the
+ * elements' type before the products, which then take half the time; the
+ * gradients' error is 1.4 times that of rounding them once. */
+#define DGC_DZ_ROUNDED 256
+/* As `backward` of *_workspace_bytes: the workspace of calls with DGC_DZ_ROUNDED,
+ * a third of the others'. */
+#define DGC_BACKWARD_ROUNDED 2
 
 /* Norms of the gradient-set operators. */
 #define DGC_NORM_L2 0  /* sqrt of the sum of squares, added in binary64 */
@@ -593,12 +600,13 @@ typedef struct dgc_linear_args {
 /* With dz = dy * act'(pre): dx[m][k] = dz w, dw[n][k] = dz^T x, dbias[n] =
  * the column sums of dz.  Each of dx, dw, dbias may be NULL.  dw and dbias
  * are of grad_type: `type`, or DGC_FP32 (a learner's flat gradient).  pre is
- * not read for DGC_ACT_NONE; for other activations dz is rounded to `type`
- * before the products (up to 32 rows: to the sum of two numbers of `type`),
- * not before the column sums.  DGC_FP16: times a power of two that brings the
+ * not read for DGC_ACT_NONE; for other activations the products take dz as the
+ * sum of two numbers of `type` (off by 2^-16 of it for DGC_BF16, 2^-22 for
+ * DGC_FP16), dw of DGC_BF16 in binary32 as the sum of three (2^-24), and with
+ * DGC_DZ_ROUNDED as one (up to 32 rows: two); the column sums take dz itself.  DGC_FP16: times a power of two that brings the
  * call's largest finite |dz| into [2^14, 2^15), undone afterwards, so that dz
  * may leave the range of `type` and a small one loses at most 2^-39 of the
- * largest (up to 32 rows: 2^-37). */
+ * largest (in two numbers: 2^-37). */
 typedef struct dgc_linear_backward_args {
     int64_t type, grad_type, act, m, n, k;
     const void* dy;
@@ -634,9 +642,8 @@ typedef struct dgc_gated_ffn_args {
     int64_t ldup;
 } dgc_gated_ffn_args;
 
-/* With da = dh * up * act'(gate) and db = dh * act(gate), both rounded to
- * `type` (up to 32 rows: to the sum of two numbers of `type`; DGC_FP16: scaled
- * as above, by the larger of both): dx[m][d] = da w_gate + db w_up,
+/* With da = dh * up * act'(gate) and db = dh * act(gate), both held as dz is
+ * above (DGC_FP16: scaled by the larger of both): dx[m][d] = da w_gate + db w_up,
  * dw_gate[f][d] = da^T x, dw_up = db^T x.  dx may be NULL, and dw_gate and dw_up together. */
 typedef struct dgc_gated_ffn_backward_args {
     int64_t type, grad_type, act, m, d, f;

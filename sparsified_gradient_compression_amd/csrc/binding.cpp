@@ -177,7 +177,7 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
         a.type = type_code(c.type);
         a.grad_type = type_code(g);
         a.act = integer(o[0]);
-        if (a.act != DGC_ACT_NONE && !pre) refuse("linear_backward: an activation's gradient needs pre");
+        if ((a.act & ~int64_t(DGC_DZ_ROUNDED)) != DGC_ACT_NONE && !pre) refuse("linear_backward: an activation's gradient needs pre");
         c.sizes(x, w, a.m, a.n, a.k);
         c.mat(&needed(o[1], "dy"), "dy", a.m, a.n, c.type, a.dy, a.lddy);
         c.mat(&x, "x", a.m, a.k, c.type, a.x, a.ldx);

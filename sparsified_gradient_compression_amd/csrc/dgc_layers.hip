@@ -74,12 +74,13 @@ bool direct(const Product& p) {
     return !two_b || (direct(p.b[1], cb) && p.b[1].ld == p.b[0].ld);
 }
 
-// The rows that a kernel's tile has have to take both halves of dz.
+// The rows that a kernel's tile has have to take both pieces of a folded dz.
 bool takes(const TileSize& t, int form, int fold) { return form != kDx || t.m >= 2 * fold; }
 
-Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct, int fold) {
+Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct, int fold,
+                 int pieces) {
     const int64_t outs = form == kDw ? parts : 1;
-    const int64_t steps = std::max<int64_t>(cdiv64(k, 64) * (form == kDx ? parts : 1), 1);
+    const int64_t steps = std::max<int64_t>(cdiv64(k, 64) * (form == kDx ? parts : 1) * pieces, 1);
     const int64_t wide = form == kPair ? 2 * n : n;
     Cut best;
     best.us = 1e30;
@@ -166,8 +167,8 @@ double both_us(const Cost& c, int64_t nx, double sx, int64_t nw, double sw) {
 int plan_both(const Product& dx, const Product& dw, bool direct, double& best) {
     int tile = kGuarded;
     best = 1e30;
-    const double sx = double(std::max<int64_t>(cdiv64(dx.k, 64) * dx.parts, 1));
-    const double sw = double(std::max<int64_t>(cdiv64(dw.k, 64), 1));
+    const double sx = double(std::max<int64_t>(cdiv64(dx.k, 64) * dx.parts * dx.pieces, 1));
+    const double sw = double(std::max<int64_t>(cdiv64(dw.k, 64) * dw.pieces, 1));
     for (const Cost& c : kCosts) {
         if ((c.tile == kGuarded) == direct || c.tile == kBig) continue;
         const TileSize t = kTileSize[c.tile];
@@ -217,16 +218,19 @@ int space_ok(const void* ws, size_t have, size_t need) {
 
 int64_t pad8(int64_t x) { return (x + 7) / 8 * 8; }
 
-// A product's splits, in the workspace.
-size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts, int fold = 0) {
+// A product's splits, in the workspace: as many as any of its forms has.
+size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts, int fold = 0,
+                  int most_pieces = 1) {
     const int64_t planes = form == kPair ? 2 : form == kDw ? parts : 1;
     size_t most = 0;
     for (const bool d : {false, true}) {
         for (const int fo : {0, fold}) {  // 0 too: without an activation
-            const Cut c = plan_product(form, m, n, k, parts, d, fo);
-            if (c.splits > 1)
-                most = std::max(most,
-                                size_t(c.splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
+            for (int pieces = 1; pieces <= most_pieces; ++pieces) {
+                const Cut c = plan_product(form, m, n, k, parts, d, fo, pieces);
+                if (c.splits > 1)
+                    most = std::max(most, size_t(c.splits) * size_t(planes) * size_t(m) *
+                                              size_t(n) * 4);
+            }
         }
     }
     return round_up(most);
@@ -245,21 +249,22 @@ size_t row_bytes(int64_t rows, int64_t cols) {
     return round_up(size_t(rows) * size_t(pad8(cols)) * 2);
 }
 
-// Rows up to which dz is kept in two halves: as many as leave half of a tile
-// of 64 empty.  One row's 64 gradients had errors of 1.6 times the rounding of
-// their own without, where many rows' have 1.4.
-constexpr int64_t kFineRows = 32;
+// Rows up to which dz is folded: both pieces of as many lie in a tile of 64.
+constexpr int64_t kFoldRows = 32;
+
+// Pieces of dz where the caller does not ask for one (layers_elem.hpp).
+constexpr int kPieces = 2, kMostPieces = 3;
 
 // Where a call keeps what it lays out: dz (da, db), column sums, dz's partial
 // maxima and the factor that its scale is undone by, operands that are
 // repacked, and splits.  From the sizes alone.
 struct Space {
     bool pack = false;
-    int32_t fold = 0;  // rows of dz, where it is kept in two halves
+    int32_t fold = 0;  // rows of dz, where it is folded
     size_t dz = 0, sums = 0, most = 0, x = 0, w = 0, w2 = 0, part = 0, total = 0;
 };
 
-Space space(bool gated, bool backward, int64_t m, int64_t n, int64_t k) {
+Space space(bool gated, int32_t backward, int64_t m, int64_t n, int64_t k) {
     const int two = gated ? 2 : 1;
     const int64_t weights = two * n * k;
     Space s;
@@ -270,14 +275,15 @@ Space space(bool gated, bool backward, int64_t m, int64_t n, int64_t k) {
         return was;
     };
     if (backward) {
-        s.fold = m <= kFineRows ? int32_t(m) : 0;
-        s.dz = take(two * row_bytes(m + s.fold, n));
+        const int pieces = backward == DGC_BACKWARD_ROUNDED ? 1 : kMostPieces;
+        s.fold = m <= kFoldRows ? int32_t(m) : 0;
+        s.dz = take(two * row_bytes(std::max(m + s.fold, pieces * m), n));
         s.sums = take(gated ? 0 : round_up(size_t(cdiv64(m, sum_rows(m, n))) * size_t(n) * 4));
         s.most = take(m > 0 && n > 0 ? round_up((kMostParts + 1) * sizeof(float)) : 0);
         s.pack = worth_repacking(kDx, m, k, n, two, weights) ||
                  worth_repacking(kDw, n, k, m, two, m * k);
-        part = std::max(part_bytes(kDx, m, k, n, two, s.fold),
-                        part_bytes(kDw, n, k, m + s.fold, two));
+        part = std::max(part_bytes(kDx, m, k, n, two, s.fold, pieces),
+                        part_bytes(kDw, n, k, m + s.fold, two, 0, pieces));
     } else {
         s.pack = worth_repacking(gated ? kPair : kRows, m, n, k, 1, weights + m * k);
         part = part_bytes(gated ? kPair : kRows, m, n, k, 1);
@@ -305,16 +311,31 @@ Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
 }
 
 int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
-    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p), p.fold);
+    const Cut c = plan_product(p.form, p.m, p.n, p.k, p.parts, direct(p), p.fold, p.pieces);
     return type == DGC_BF16 ? Launch<__bf16>::product(p, c, ws, s)
                             : Launch<_Float16>::product(p, c, ws, s);
 }
 
-// fp16 holds a dz that is a product of fp16 numbers only after a scale.
-void scale_dz(int64_t type, SlopeArgs& a, char* space) {
+// How a dz that 16 bits do not hold is stored, and what its products make of it.
+void hold_dz(int64_t type, bool rounded, bool wide, const Space& sp, char* ws, SlopeArgs& a,
+             Product& dx, Product& dw) {
+    a.low = dx.low = dw.low = a.M * a.ldz;
+    const int pieces = rounded ? 1 : kPieces;
+    const int dw_pieces = wide && type == DGC_BF16 && !rounded ? kMostPieces : pieces;
+    a.pieces = std::max(dw_pieces, sp.fold ? kPieces : 1);
+    dx.fold = sp.fold;
+    if (!sp.fold) dx.pieces = pieces;
+    if (sp.fold && dw_pieces < kMostPieces) {
+        dw.fold = sp.fold;
+        dw.k += sp.fold;
+    } else {
+        dw.pieces = dw_pieces;
+    }
+    // fp16 holds a product of fp16 numbers only after a scale
     if (type != DGC_FP16 || a.M == 0 || a.N == 0) return;
-    a.most = reinterpret_cast<float*>(space);
+    a.most = reinterpret_cast<float*>(ws + sp.most);
     a.unscale = a.most + kMostParts;
+    dx.fin.unscale = dw.fin.unscale = a.unscale;
 }
 
 int run_prepare(int64_t type, const SlopeArgs& a, const Repack& r, hipStream_t s) {
@@ -332,8 +353,9 @@ int run_gradients(int64_t type, const Product& dx, const Product& dw, const Sums
     int rc = DGC_OK;
     if (has_dx && has_dw) {
         const bool d = direct(dx) && direct(dw);
-        const Cut cx = plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx), dx.fold);
-        const Cut cw = plan_product(kDw, dw.m, dw.n, dw.k, dw.parts, direct(dw));
+        const Cut cx =
+            plan_product(kDx, dx.m, dx.n, dx.k, dx.parts, direct(dx), dx.fold, dx.pieces);
+        const Cut cw = plan_product(kDw, dw.m, dw.n, dw.k, dw.parts, direct(dw), 0, dw.pieces);
         const double apart = cx.us + cw.us + (sums.out ? 2 : 1) * kLaunchUs;  // without a first one
         double us = 0;
         const int tile = plan_both(dx, dw, d, us);
@@ -356,14 +378,14 @@ extern "C" {
 
 int dgc_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t backward, size_t* bytes) {
     if (!bytes || !sizes_ok(m, n, k)) return DGC_EINVAL;
-    *bytes = space(false, backward != 0, m, n, k).total;
+    *bytes = space(false, backward, m, n, k).total;
     return DGC_OK;
 }
 
 int dgc_gated_ffn_workspace_bytes(int64_t m, int64_t d, int64_t f, int32_t backward,
                                   size_t* bytes) {
     if (!bytes || !sizes_ok(m, d, f)) return DGC_EINVAL;
-    *bytes = space(true, backward != 0, m, f, d).total;
+    *bytes = space(true, backward, m, f, d).total;
     return DGC_OK;
 }
 
@@ -376,7 +398,7 @@ int dgc_linear(const dgc_linear_args* a, void* workspace, size_t workspace_bytes
         !mat_ok(a->y, a->ldy, a->m, a->n, 2) || !optional_ok(a->pre, a->ldpre, a->m, a->n, 2))
         return DGC_EINVAL;
     const int64_t m = a->m, n = a->n, k = a->k;
-    const Space sp = space(false, false, m, n, k);
+    const Space sp = space(false, 0, m, n, k);
     int rc = space_ok(workspace, workspace_bytes, sp.total);
     if (rc != DGC_OK) return rc;
     char* ws = static_cast<char*>(workspace);
@@ -403,19 +425,21 @@ int dgc_linear(const dgc_linear_args* a, void* workspace, size_t workspace_bytes
 
 int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
                         size_t workspace_bytes, hipStream_t stream) {
-    if (!a || !half(a->type) || !act_ok(a->act) || !sizes_ok(a->m, a->n, a->k) ||
+    const bool rounded = a && (a->act & DGC_DZ_ROUNDED);
+    const int64_t act = a ? a->act & ~int64_t(DGC_DZ_ROUNDED) : 0;
+    if (!a || !half(a->type) || !act_ok(act) || !sizes_ok(a->m, a->n, a->k) ||
         (a->grad_type != a->type && a->grad_type != DGC_FP32))
         return DGC_EINVAL;
     const int64_t m = a->m, n = a->n, k = a->k;
     const int wide = a->grad_type == DGC_FP32;
-    const bool sloped = a->act != DGC_ACT_NONE;
+    const bool sloped = act != DGC_ACT_NONE;
     if (!mat_ok(a->dy, a->lddy, m, n, 2) || !mat_ok(a->x, a->ldx, m, k, 2) ||
         !mat_ok(a->w, a->ldw, n, k, 2) || (sloped && !mat_ok(a->pre, a->ldpre, m, n, 2)) ||
         !optional_ok(a->dx, a->lddx, m, k, 2) ||
         !optional_ok(a->dw, a->lddw, n, k, wide ? 4 : 2) ||
         !optional_ok(a->dbias, n, 1, n, wide ? 4 : 2))
         return DGC_EINVAL;
-    const Space sp = space(false, true, m, n, k);
+    const Space sp = space(false, rounded ? DGC_BACKWARD_ROUNDED : 1, m, n, k);
     int rc = space_ok(workspace, workspace_bytes, sp.total);
     if (rc != DGC_OK) return rc;
     char* ws = static_cast<char*>(workspace);
@@ -428,7 +452,8 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     if (copied) dz = {ws + sp.dz, pad8(n), true};
     SlopeArgs sl;
     Sums sums;
-    int32_t fold = 0;  // dz in two halves: where a slope made it
+    Product dx, dw;
+    dw.k = m;
     if (copied || a->dbias) {
         sl.M = m;
         sl.N = n;
@@ -437,14 +462,12 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
         sl.lddy = a->lddy;
         sl.pre = a->pre;
         sl.ldp = a->ldpre;
-        sl.act = int32_t(a->act);
+        sl.act = int32_t(act);
         sl.dz = copied ? ws + sp.dz : nullptr;
         sl.ldz = pad8(n);
-        if (sloped && copied) {
-            fold = sp.fold;
-            scale_dz(a->type, sl, ws + sp.most);
-        }
-        sl.low = fold * sl.ldz;
+        // (relu's slope is 0 or 1: dz is 0 or dy)
+        if (sloped && act != DGC_ACT_RELU && copied)
+            hold_dz(a->type, rounded, wide, sp, ws, sl, dx, dw);
         sl.part = a->dbias ? reinterpret_cast<float*>(ws + sp.sums) : nullptr;
         sums.rows = cdiv64(m, sl.per);
         sums.N = n;
@@ -454,21 +477,17 @@ int dgc_linear_backward(const dgc_linear_backward_args* a, void* workspace,
     }
     rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
-    Product dx, dw;
     dx.form = kDx;
     dx.m = m;
     dx.n = k;
     dx.k = n;
     dx.a[0] = dz;
     dx.b[0] = w;
-    dx.fold = dw.fold = fold;
     dx.fin.out[0] = a->dx;
     dx.fin.ldo = a->lddx;
-    dx.fin.unscale = dw.fin.unscale = sl.unscale;
     dw.form = kDw;
     dw.m = n;
     dw.n = k;
-    dw.k = m + fold;
     dw.a[0] = dz;
     dw.b[0] = x;
     dw.fin.out[0] = a->dw;
@@ -485,7 +504,7 @@ int dgc_gated_ffn(const dgc_gated_ffn_args* a, void* workspace, size_t workspace
         !mat_ok(a->w_up, a->ldw_up, f, d, 2) || !mat_ok(a->h, a->ldh, m, f, 2) ||
         !optional_ok(a->gate, a->ldgate, m, f, 2) || !optional_ok(a->up, a->ldup, m, f, 2))
         return DGC_EINVAL;
-    const Space sp = space(true, false, m, f, d);
+    const Space sp = space(true, 0, m, f, d);
     int rc = space_ok(workspace, workspace_bytes, sp.total);
     if (rc != DGC_OK) return rc;
     char* ws = static_cast<char*>(workspace);
@@ -512,7 +531,9 @@ int dgc_gated_ffn(const dgc_gated_ffn_args* a, void* workspace, size_t workspace
 
 int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace,
                            size_t workspace_bytes, hipStream_t stream) {
-    if (!a || !half(a->type) || !act_ok(a->act) || !sizes_ok(a->m, a->d, a->f) ||
+    const bool rounded = a && (a->act & DGC_DZ_ROUNDED);
+    const int64_t act = a ? a->act & ~int64_t(DGC_DZ_ROUNDED) : 0;
+    if (!a || !half(a->type) || !act_ok(act) || !sizes_ok(a->m, a->d, a->f) ||
         (a->grad_type != a->type && a->grad_type != DGC_FP32))
         return DGC_EINVAL;
     const int64_t m = a->m, d = a->d, f = a->f;
@@ -524,7 +545,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
         !optional_ok(a->dw_gate, a->lddw_gate, f, d, size) ||
         !optional_ok(a->dw_up, a->lddw_up, f, d, size) || !a->dw_gate != !a->dw_up)
         return DGC_EINVAL;
-    const Space sp = space(true, true, m, f, d);
+    const Space sp = space(true, rounded ? DGC_BACKWARD_ROUNDED : 1, m, f, d);
     int rc = space_ok(workspace, workspace_bytes, sp.total);
     if (rc != DGC_OK) return rc;
     if (!a->dx && !a->dw_gate) return DGC_OK;
@@ -547,31 +568,28 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     sl.ldp = a->ldgate;
     sl.up = a->up;
     sl.ldu = a->ldup;
-    sl.act = int32_t(a->act);
-    sl.dz = ws + sp.dz;
-    sl.dz2 = ws + sp.dz + row_bytes(m + sp.fold, f);
+    sl.act = int32_t(act);
     sl.ldz = ld;
-    sl.low = sp.fold * ld;
-    scale_dz(a->type, sl, ws + sp.most);
+    Product dx, dw;
+    dw.k = m;
+    hold_dz(a->type, rounded, wide, sp, ws, sl, dx, dw);
+    sl.dz = ws + sp.dz;
+    sl.dz2 = ws + sp.dz + row_bytes(sl.pieces * m, f);
     rc = run_prepare(a->type, sl, r, stream);
     if (rc != DGC_OK) return rc;
-    Product dx, dw;
     dx.form = kDx;
     dx.parts = 2;
     dx.m = m;
     dx.n = d;
     dx.k = f;
-    dx.fold = dw.fold = sp.fold;
     dx.b[0] = wg;
     dx.b[1] = wu;
     dx.fin.out[0] = a->dx;
     dx.fin.ldo = a->lddx;
-    dx.fin.unscale = dw.fin.unscale = sl.unscale;
     dw.form = kDw;
     dw.parts = 2;
     dw.m = f;
     dw.n = d;
-    dw.k = m + sp.fold;
     dw.b[0] = x;
     dw.fin.out[0] = a->dw_gate;
     dw.fin.ldo = a->lddw_gate;

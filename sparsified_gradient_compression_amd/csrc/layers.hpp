@@ -54,10 +54,13 @@ struct Product {
     int64_t m = 0, n = 0, k = 0;
     int parts = 1;  // terms of kDx, outputs of kDw
     Mat a[2], b[2];
-    // Not 0: so many rows of dz, at most 32, come in two halves, all first halves
+    // kDx, kDw: a comes as the sum of so many matrices, `low` elements apart.
+    int32_t pieces = 1;
+    int64_t low = 0;
+    // Not 0: so many rows of dz, at most 32, come in two pieces, all first pieces
     // before all second ones.  kDx: m = fold, a has 2 fold rows (those of a tile),
     // and sums `fold` rows apart are added.  kDw: k = 2 fold (one step of 64), and
-    // b's fold rows are taken for either half.
+    // b's fold rows are taken for either piece.
     int32_t fold = 0;
     Finish fin;
 };
@@ -91,15 +94,15 @@ bool direct(const Product& p);
 
 // From the sizes, and whether the operands' rows lie on 16 bytes.
 Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool direct,
-                 int fold = 0);
+                 int fold = 0, int pieces = 1);
 
 constexpr int kMostParts = 512;
 
 // dz = dy * act'(pre), its rows padded with zeros to ldz, and the sums of its
 // columns over `per` rows each into `part` (either null: not wanted); with
 // `up`, dz = dy * up * act'(pre) and dz2 = dy * act(pre) and no sums, `per` (4
-// or 8) elements per thread.  low (not 0): what rounding dz and dz2 loses, so
-// many elements on.  most (fp16; or null): space for kMostParts partial maxima
+// or 8) elements per thread.  dz and dz2 are stored as the sum of `pieces`
+// matrices, `low` elements apart.  most (fp16; or null): space for kMostParts partial maxima
 // of |dz| and |dz2|; they are then stored times the power of two that brings
 // the largest into [2^14, 2^15), and its reciprocal goes to `unscale`.
 struct SlopeArgs {
@@ -109,7 +112,8 @@ struct SlopeArgs {
     void *dz = nullptr, *dz2 = nullptr;
     float* part = nullptr;
     float *most = nullptr, *unscale = nullptr;
-    int32_t act = 0, parts = 0;  // parts: how many of `most` there are
+    int32_t act = 0, pieces = 1;
+    int32_t parts = 0;  // how many of `most` there are
 };
 
 // The partial column sums, to be added up into `out` (null: none).

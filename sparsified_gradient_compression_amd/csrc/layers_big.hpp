@@ -38,7 +38,7 @@ __device__ __forceinline__ void half_phase_end() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <class T, int FORM>
+template <class T, int FORM, bool SPLIT>
 __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
     typedef typename Arith<T>::v8 v8;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     const int64_t m0 = at_tile.tm * 256, n0 = at_tile.tn * (PAIR ? 128 : 256);
 
     const int ksteps = int((A.K + kStep - 1) / kStep);
-    const int total = ksteps * (FORM == kDx ? A.parts : 1);
+    const int total = all_steps<FORM, SPLIT>(A, ksteps);
     const int first = split * int(A.per);
     const int last = first + int(A.per) < total ? first + int(A.per) : total;
 
@@ -69,19 +69,17 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     // Half h of tile t.  Beyond the last tile nothing is read, but the loads
     // are counted all the same.
     auto order_a = [&](int t, int h, T* lds) {
-        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
-        const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
-        const int64_t left = t < last ? A.K - k0 : 0;
-        const T* p = static_cast<const T*>(A.a[FORM == kDw ? z : seg]) +
+        const auto step = step_at<FORM, SPLIT>(A, t, ksteps);
+        const int64_t k0 = step.k0, left = t < last ? A.K - k0 : 0;
+        const T* p = static_cast<const T*>(A.a[FORM == kDw ? z : step.term]) + step.piece +
                      (ATR ? k0 * lda + m0 + h * 128 : (m0 + h * 128) * lda + k0);
         sa[h].order(left > 0 ? p : static_cast<const T*>(A.a[0]),
                     left < kStep ? int(left) : kStep, lds, wave);
     };
     auto order_b = [&](int t, int h, T* lds) {
-        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
-        const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
-        const int64_t left = t < last ? A.K - k0 : 0;
-        const T* p = static_cast<const T*>(A.b[PAIR ? h : seg]) +
+        const auto step = step_at<FORM, SPLIT>(A, t, ksteps);
+        const int64_t k0 = step.k0, left = t < last ? A.K - k0 : 0;
+        const T* p = static_cast<const T*>(A.b[PAIR ? h : step.term]) +
                      (BTR ? k0 * ldb + n0 + h * 128 : (n0 + (PAIR ? 0 : h * 128)) * ldb + k0);
         sb[h].order(left > 0 ? p : static_cast<const T*>(A.b[0]),
                     left < kStep ? int(left) : kStep, lds, wave);

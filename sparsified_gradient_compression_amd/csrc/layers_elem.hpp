@@ -2,14 +2,14 @@
 // activation's slope makes of an incoming gradient, column sums, and operands
 // laid out anew.
 //
-// The products that follow take 16-bit operands, so dz (da, db) is rounded
-// once to the elements' own type here, as the incoming gradient was: half a
-// step at most, 2^-8 (bf16) or 2^-11 (fp16) of the element, as much as the
-// rounding of the output that it is summed into; together 1.4 times one of
-// them.  For few rows, where the products are bound by reading the weight and
-// few roundings have to even out, what is lost is kept in a second half of 16
-// bits (`low` elements on) and multiplied too, in places of the same tiles
-// that would be empty.
+// The products that follow take 16-bit operands, so dz (da, db) is stored as a
+// sum of numbers of the elements' own type, and each of them is multiplied.  Two
+// hold it to 2^-16 (bf16) or 2^-22 (fp16) of itself, far less than the rounding
+// of a 16-bit output; three hold a bf16 dz to binary32's own precision, for
+// weight gradients in binary32.  One number, half a step of 2^-8 or 2^-11, is
+// for callers that ask for it: the outputs' error is then 1.4 times their own
+// rounding, and the products take half the time.  Up to 32 rows a second number
+// costs nothing: it takes places of the same tiles that would be empty.
 //
 // fp16 has 5 bits of exponent, and dz is a product of up to three numbers: it
 // may be 2^16 times larger or smaller than any of them.  A pass before finds
@@ -30,42 +30,46 @@
 namespace dgc {
 namespace layers {
 
-// v as the sum of two numbers of T, both of v's sign and neither 0 (unless v
-// is): the high one lies below v in magnitude, also where T holds v itself.  So
-// both products with an infinite operand are the infinity that v's is; a second
-// half that is 0 or of the other sign would make it NaN.  The sum is off by half
-// a step of the second half, 2^-16 (bf16) or 2^-22 (fp16) of v, or by two of T's
-// least numbers.  An infinite or NaN v is both halves.
-template <class T>
-__device__ __forceinline__ void split(float v, float& high, float& rest) {
+// v as the sum of P numbers of T, all of v's sign and none of them 0 (unless v
+// is): each but the last lies below what is left of v in magnitude, also where T
+// holds that itself.  So every product with an infinite operand is the infinity
+// that v's is; a piece that is 0 or of the other sign would make it NaN.  The sum
+// is off by half a step of the last piece, or by two of T's least numbers.  An
+// infinite or NaN v is all pieces.
+template <class T, int P>
+__device__ __forceinline__ void split(float v, float* piece) {
     asm("" : "+v"(v));  // rounded once: T made from the product before it may be another number
-    high = float(T(v));
-    rest = high;
-    if (!(fabsf(v) < __builtin_inff()) || v == 0.0f) return;
+#pragma unroll
+    for (int p = 0; p < P; ++p) piece[p] = float(T(v));
+    if (P == 1 || !(fabsf(v) < __builtin_inff()) || v == 0.0f) return;
     const uint16_t least = __builtin_bit_cast(uint32_t, v) >> 31 << 15 | 1;
-    uint16_t h = __builtin_bit_cast(uint16_t, T(v));
-    if (fabsf(high) >= fabsf(v)) --h;  // a step towards 0
-    if ((h & 0x7FFF) == 0) h = least;
-    high = float(__builtin_bit_cast(T, h));
-    uint16_t r = __builtin_bit_cast(uint16_t, T(v - high));
-    if ((r & 0x7FFF) == 0 || r >> 15 != least >> 15) r = least;
-    rest = float(__builtin_bit_cast(T, r));
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        uint16_t h = __builtin_bit_cast(uint16_t, T(v));
+        if (p < P - 1 && fabsf(float(T(v))) >= fabsf(v)) --h;  // a step towards 0
+        if ((h & 0x7FFF) == 0 || v == 0.0f || h >> 15 != least >> 15) h = least;
+        piece[p] = float(__builtin_bit_cast(T, h));
+        v -= piece[p];
+    }
 }
 
-// C values rounded to T, or with HALVES split, the second halves `low`
-// elements on.  (A template: the few rows' registers would cost the many 3% of
-// their rate.)
-template <class T, int C, bool HALVES>
-__device__ __forceinline__ void store_halves(T* p, int64_t low, const float* v) {
-    if constexpr (!HALVES) {
+// C values as P pieces, `low` elements apart.  (A template: the registers of
+// many pieces would cost one 3% of its rate.)
+template <class T, int C, int P>
+__device__ __forceinline__ void store_pieces(T* p, int64_t low, const float* v) {
+    if constexpr (P == 1) {
         store_row<T, C>(p, C, v);
         return;
     }
-    float high[C], rest[C];
+    float piece[C][P], row[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) split<T>(v[i], high[i], rest[i]);
-    store_row<T, C>(p, C, high);
-    store_row<T, C>(p + low, C, rest);
+    for (int i = 0; i < C; ++i) split<T, P>(v[i], piece[i]);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) row[i] = piece[i][q];
+        store_row<T, C>(p + q * low, C, row);
+    }
 }
 
 template <class T, int C>
@@ -131,7 +135,7 @@ __device__ __forceinline__ float dz_scale(const SlopeArgs& A, float* lds) {
 // dz = dy * act'(pre) and the sums of dz's columns (before it is rounded) over
 // `per` rows each.  A block of 256 threads covers 512 columns (64 threads, 8
 // columns each) by `per` rows (4 rows of threads).
-template <class T, bool HALVES>
+template <class T, int P>
 __device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, float (*sums)[512],
                                             float scale) {
     const int64_t across = (A.N + 511) / 512;
@@ -170,7 +174,7 @@ __device__ __forceinline__ void slope_block(const SlopeArgs& A, int64_t id, floa
                     for (int i = 0; i < 8; ++i) sum[i] += d[r][i];
                     scale_row<T, 8>(d[r], scale);
                     // zeros in the padding
-                    if (dz) store_halves<T, 8, HALVES>(dz + (m + 4 * r) * A.ldz + n, A.low, d[r]);
+                    if (dz) store_pieces<T, 8, P>(dz + (m + 4 * r) * A.ldz + n, A.low, d[r]);
                 }
         }
     }
@@ -215,7 +219,7 @@ __global__ __launch_bounds__(256) void k_sum_columns(Sums A) {
 
 // da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; C (4
 // or 8) elements per thread.
-template <class T, int C, bool HALVES>
+template <class T, int C, int P>
 __device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id, float scale) {
     const int64_t groups = A.ldz / C;
     id = id * 256 + threadIdx.x;
@@ -236,8 +240,8 @@ __device__ __forceinline__ void gate_slope_block(const SlopeArgs& A, int64_t id,
     scale_row<T, C>(oa, scale);
     scale_row<T, C>(ob, scale);
     // zeros in the padding
-    store_halves<T, C, HALVES>(static_cast<T*>(A.dz) + m * A.ldz + n, A.low, oa);
-    store_halves<T, C, HALVES>(static_cast<T*>(A.dz2) + m * A.ldz + n, A.low, ob);
+    store_pieces<T, C, P>(static_cast<T*>(A.dz) + m * A.ldz + n, A.low, oa);
+    store_pieces<T, C, P>(static_cast<T*>(A.dz2) + m * A.ldz + n, A.low, ob);
 }
 
 // Rows at any even address to rows on 16 bytes, zeros up to their ends; 8
@@ -268,7 +272,7 @@ __device__ __forceinline__ void repack_block(const Repack& r, int64_t id) {
 }
 
 // What a call lays out before its products, in one launch.
-template <class T, bool HALVES>
+template <class T, int P>
 __global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_blocks, Repack r) {
     __shared__ float sums[4][512];
     const int64_t id = blockIdx.x;
@@ -282,11 +286,11 @@ __global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_bloc
         if (A.most) scale = dz_scale(A, most);
     }
     if (A.up && A.per == 4)
-        gate_slope_block<T, 4, HALVES>(A, id, scale);
+        gate_slope_block<T, 4, P>(A, id, scale);
     else if (A.up)
-        gate_slope_block<T, 8, HALVES>(A, id, scale);
+        gate_slope_block<T, 8, P>(A, id, scale);
     else
-        slope_block<T, HALVES>(A, id, sums, scale);
+        slope_block<T, P>(A, id, sums, scale);
 }
 
 }  // namespace layers

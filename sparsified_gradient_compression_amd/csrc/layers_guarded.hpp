@@ -76,7 +76,7 @@ struct Guarded {
 constexpr int kGuardedGroups = 4;
 constexpr int kGuardedSide = 64 * kStep;
 
-template <class T, int FORM>
+template <class T, int FORM, bool SPLIT>
 __device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem) {
     constexpr bool PAIR = FORM == kPair, ATR = FORM == kDw, BTR = FORM == kDx || FORM == kDw;
     constexpr int KG = kGuardedGroups, MT = 2, NTW = 2, NT = PAIR ? 1 : 2;
@@ -92,7 +92,7 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem)
     const int64_t m0 = at_tile.tm * 64, n0 = at_tile.tn * (PAIR ? 32 : 64);
 
     const int64_t ksteps = (A.K + kStep - 1) / kStep;
-    const int64_t total = ksteps * (FORM == kDx ? A.parts : 1);
+    const int64_t total = all_steps<FORM, SPLIT>(A, ksteps);
     const int64_t first = split * A.per;
     const int64_t last = first + A.per < total ? first + A.per : total;
     const int64_t rounds = (last - first + KG - 1) / KG;
@@ -127,14 +127,13 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem)
     u32x4 ra[2], rb[2];
     auto fetch = [&](int64_t r) {
         const int64_t t = first + r * KG + group;
-        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
-        const int64_t k0 = (t - seg * ksteps) * kStep;
-        const int64_t left = t < last ? A.K - k0 : 0;
-        if (FORM == kDx && seg) {
-            ga[FORM == kDx].load(k0, left, ra);
+        const auto step = step_at<FORM, SPLIT>(A, t, ksteps);
+        const int64_t k0 = step.k0, left = t < last ? A.K - k0 : 0;
+        if (FORM == kDx && step.term) {
+            ga[FORM == kDx].load(step.piece + k0, left, ra);
             gb[FORM == kDx].load(k0 * A.ldb[1], left, rb);
         } else {
-            ga[0].load(ATR ? k0 * A.lda[FORM == kDw ? z : 0] : k0, left, ra);
+            ga[0].load(step.piece + (ATR ? k0 * A.lda[FORM == kDw ? z : 0] : k0), left, ra);
             gb[0].load(BTR ? k0 * A.ldb[0] : k0, left, rb);
         }
     };
@@ -193,14 +192,14 @@ __device__ __forceinline__ void guarded_tile(const TileArgs& A, int id, T* smem)
 constexpr int kGuardedThreads = 256 * kGuardedGroups;
 constexpr int kGuardedLds = kGuardedGroups * 4 * kGuardedSide;
 
-template <class T, int FORM>
+template <class T, int FORM, bool SPLIT>
 __global__ __launch_bounds__(kGuardedThreads) void k_guarded(TileArgs A) {
     __shared__ __align__(16) T smem[kGuardedLds];
-    guarded_tile<T, FORM>(A, blockIdx.x, smem);
+    guarded_tile<T, FORM, SPLIT>(A, blockIdx.x, smem);
 }
 
 // Both gradients of a layer in one launch, and the column sums' last step.
-template <class T>
+template <class T, bool SPLIT>
 __global__ __launch_bounds__(kGuardedThreads) void k_guarded_both(TileArgs dx, TileArgs dw,
                                                                   int dx_blocks, int dw_blocks,
                                                                   Sums sums) {
@@ -208,9 +207,9 @@ __global__ __launch_bounds__(kGuardedThreads) void k_guarded_both(TileArgs dx, T
     // each kind begins with the first die's workgroup
     const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
-        guarded_tile<T, kDx>(dx, id, smem);
+        guarded_tile<T, kDx, SPLIT>(dx, id, smem);
     else if (id >= dw0 && id < sum0)
-        guarded_tile<T, kDw>(dw, id - dw0, smem);
+        guarded_tile<T, kDw, SPLIT>(dw, id - dw0, smem);
     else if (id >= sum0)
         sum_columns<T, kGuardedThreads>(sums, id - sum0, reinterpret_cast<float*>(smem));
 }

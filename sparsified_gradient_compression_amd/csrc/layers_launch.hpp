@@ -17,19 +17,19 @@ namespace layers {
 #define DGC_LAYERS_CHECK() \
     if (hipGetLastError() != hipSuccess) return DGC_EHIP
 
-template <class T, int FORM>
+template <class T, int FORM, bool SPLIT>
 int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
     const int64_t blocks = a.mt * a.nt * (FORM == kDw ? a.parts : 1) * c.splits;
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (c.tile) {
-        case kGuarded: k_guarded<T, FORM><<<grid, kGuardedThreads, 0, s>>>(a); break;
-        case kMid32: k_mid<T, FORM, Shape32><<<grid, 1024, 0, s>>>(a); break;
-        case kMid64: k_mid<T, FORM, Shape64><<<grid, 512, 0, s>>>(a); break;
-        case kLight: k_mid<T, FORM, ShapeLight><<<grid, 256, 0, s>>>(a); break;
-        case kMid128: k_mid<T, FORM, Shape128><<<grid, 512, 0, s>>>(a); break;
-        case kPair128: k_mid<T, FORM, ShapePair><<<grid, 512, 0, s>>>(a); break;
-        case kBig: k_big<T, FORM><<<grid, 512, 0, s>>>(a); break;
+        case kGuarded: k_guarded<T, FORM, SPLIT><<<grid, kGuardedThreads, 0, s>>>(a); break;
+        case kMid32: k_mid<T, FORM, Shape32, SPLIT><<<grid, 1024, 0, s>>>(a); break;
+        case kMid64: k_mid<T, FORM, Shape64, SPLIT><<<grid, 512, 0, s>>>(a); break;
+        case kLight: k_mid<T, FORM, ShapeLight, SPLIT><<<grid, 256, 0, s>>>(a); break;
+        case kMid128: k_mid<T, FORM, Shape128, SPLIT><<<grid, 512, 0, s>>>(a); break;
+        case kPair128: k_mid<T, FORM, ShapePair, SPLIT><<<grid, 512, 0, s>>>(a); break;
+        case kBig: k_big<T, FORM, SPLIT><<<grid, 512, 0, s>>>(a); break;
         default:
             if constexpr (FORM == kRows || FORM == kPair) {
                 const dim3 rows(static_cast<unsigned>(cdiv64(a.N, 16)));
@@ -61,6 +61,9 @@ inline TileArgs tile_args(const Product& p, const Cut& c, void* ws) {
     a.splits = c.splits;
     a.parts = p.parts;
     a.outs = p.form == kDw ? p.parts : 1;
+    a.pieces = p.pieces;
+    a.inverse = uint32_t((0x80000000u + uint32_t(p.pieces) - 1) / uint32_t(p.pieces));
+    a.low = p.low;
     a.fold = p.fold;
     a.part = c.splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.fin = p.fin;
@@ -73,10 +76,16 @@ int Launch<T>::product(const Product& p, const Cut& c, void* ws, hipStream_t s) 
     const TileArgs a = tile_args(p, c, ws);
     int rc = DGC_EINVAL;
     switch (p.form) {
-        case kRows: rc = launch_tiles<T, kRows>(a, c, s); break;
-        case kPair: rc = launch_tiles<T, kPair>(a, c, s); break;
-        case kDx: rc = launch_tiles<T, kDx>(a, c, s); break;
-        case kDw: rc = launch_tiles<T, kDw>(a, c, s); break;
+        case kRows: rc = launch_tiles<T, kRows, false>(a, c, s); break;
+        case kPair: rc = launch_tiles<T, kPair, false>(a, c, s); break;
+        case kDx:
+            rc = a.pieces > 1 ? launch_tiles<T, kDx, true>(a, c, s)
+                              : launch_tiles<T, kDx, false>(a, c, s);
+            break;
+        case kDw:
+            rc = a.pieces > 1 ? launch_tiles<T, kDw, true>(a, c, s)
+                              : launch_tiles<T, kDw, false>(a, c, s);
+            break;
     }
     if (rc != DGC_OK || c.splits == 1) return rc;
     const int64_t blocks = cdiv64(cdiv64(p.n, 4) * p.m * a.outs, 64);
@@ -89,15 +98,8 @@ int Launch<T>::product(const Product& p, const Cut& c, void* ws, hipStream_t s) 
     return DGC_OK;
 }
 
-template <class T>
-int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& sums,
-                    hipStream_t s) {
-    Cut c;
-    c.tile = tile;
-    c.per = cdiv64(dx.k, kStep) * dx.parts;
-    const TileArgs x = tile_args(dx, c, nullptr);
-    c.per = cdiv64(dw.k, kStep);
-    const TileArgs w = tile_args(dw, c, nullptr);
+template <class T, bool SPLIT>
+int launch_both(const TileArgs& x, const TileArgs& w, int tile, const Sums& sums, hipStream_t s) {
     const int64_t nx = x.mt * x.nt, nw = w.mt * w.nt * w.parts;
     const int64_t blocks = (nx + 7) / 8 * 8 + nw + (sums.out ? cdiv64(sums.N, 32) : 0);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
@@ -105,17 +107,30 @@ int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& 
     const dim3 grid(static_cast<unsigned>(blocks));
     switch (tile) {
         case kGuarded:
-            k_guarded_both<T><<<grid, kGuardedThreads, 0, s>>>(x, w, int(nx), int(nw), sums);
+            k_guarded_both<T, SPLIT><<<grid, kGuardedThreads, 0, s>>>(x, w, int(nx), int(nw), sums);
             break;
-        case kMid32: k_mid_both<T, Shape32><<<grid, 1024, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kMid64: k_mid_both<T, Shape64><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kLight: k_mid_both<T, ShapeLight><<<grid, 256, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kMid128: k_mid_both<T, Shape128><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kPair128: k_mid_both<T, ShapePair><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid32: k_mid_both<T, Shape32, SPLIT><<<grid, 1024, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid64: k_mid_both<T, Shape64, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kLight: k_mid_both<T, ShapeLight, SPLIT><<<grid, 256, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid128: k_mid_both<T, Shape128, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kPair128: k_mid_both<T, ShapePair, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
         default: return DGC_EINVAL;
     }
     DGC_LAYERS_CHECK();
     return DGC_OK;
+}
+
+template <class T>
+int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums& sums,
+                    hipStream_t s) {
+    Cut c;
+    c.tile = tile;
+    c.per = cdiv64(dx.k, kStep) * dx.parts * dx.pieces;
+    const TileArgs x = tile_args(dx, c, nullptr);
+    c.per = cdiv64(dw.k, kStep) * dw.pieces;
+    const TileArgs w = tile_args(dw, c, nullptr);
+    return x.pieces > 1 || w.pieces > 1 ? launch_both<T, true>(x, w, tile, sums, s)
+                                        : launch_both<T, false>(x, w, tile, sums, s);
 }
 
 template <class T>
@@ -136,7 +151,9 @@ int Launch<T>::prepare(SlopeArgs a, const Repack& r, hipStream_t s) {
             DGC_LAYERS_CHECK();
         }
     }
-    const auto kernel = a.low ? k_prepare<T, true> : k_prepare<T, false>;
+    auto kernel = a.pieces == 1 ? k_prepare<T, 1> : k_prepare<T, 2>;
+    if constexpr (!std::is_same_v<T, _Float16>)
+        if (a.pieces == 3) kernel = k_prepare<T, 3>;
     kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, s>>>(a, slopes, r);
     DGC_LAYERS_CHECK();
     return DGC_OK;

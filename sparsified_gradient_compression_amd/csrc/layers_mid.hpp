@@ -48,7 +48,7 @@ typedef Shape<128, 128, 2, 4, 1, 2, true> ShapePair;
     __shared__ __align__(16) T s2[SH::S > 2 ? SH::kRing : 8];                  \
     __shared__ __align__(16) T s3[SH::S > 3 ? SH::kRing : 8]
 
-template <class T, int FORM, class SH>
+template <class T, int FORM, class SH, bool SPLIT>
 __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1, T* s2,
                                          T* s3) {
     constexpr int BM = SH::BM, BN = SH::BN, WM = SH::WM, WN = SH::WN, KG = SH::KG, S = SH::S;
@@ -69,7 +69,7 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1
     const int64_t m0 = at_tile.tm * BM, n0 = at_tile.tn * RB;
 
     const int ksteps = int((A.K + kStep - 1) / kStep);
-    const int total = ksteps * (FORM == kDx ? A.parts : 1);
+    const int total = all_steps<FORM, SPLIT>(A, ksteps);
     const int first = split * int(A.per);
     const int last = first + int(A.per) < total ? first + int(A.per) : total;
     const int rounds = (last - first + KG - 1) / KG;
@@ -84,17 +84,16 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1
     // The group's tile of round r; nothing is read beyond the last one.
     auto order = [&](int r, T* ring) {
         const int t = first + r * KG + group;
-        const int seg = FORM == kDx && t >= ksteps ? 1 : 0;
-        const int64_t k0 = int64_t(t - seg * ksteps) * kStep;
-        const int64_t more = t < last ? A.K - k0 : 0;
+        const auto step = step_at<FORM, SPLIT>(A, t, ksteps);
+        const int64_t more = t < last ? A.K - step.k0 : 0;
         const int left = more < kStep ? int(more) : kStep;
-        const int64_t at = more > 0 ? k0 : 0;
+        const int64_t at = more > 0 ? step.k0 : 0;
         T* lds = ring + group * kTile;
-        sa.order(static_cast<const T*>(A.a[FORM == kDw ? z : seg]) +
+        sa.order(static_cast<const T*>(A.a[FORM == kDw ? z : step.term]) + step.piece +
                      (ATR ? at * lda + m0 : m0 * lda + at), left, lds, wave);
 #pragma unroll
         for (int w = 0; w < (PAIR ? 2 : 1); ++w)
-            sb.order(static_cast<const T*>(A.b[PAIR ? w : seg]) +
+            sb.order(static_cast<const T*>(A.b[PAIR ? w : step.term]) +
                          (BTR ? at * ldb + n0 : n0 * ldb + at), left,
                      lds + BM * kStep + w * RB * kStep, wave);
     };
@@ -177,23 +176,23 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1
     put_rows<T, FORM, BM, BN, SH::kThreads>(A, split, z, m0, n0, KG, kGroupStride, at);
 }
 
-template <class T, int FORM, class SH>
+template <class T, int FORM, class SH, bool SPLIT>
 __global__ __launch_bounds__(SH::kThreads) void k_mid(TileArgs A) {
     DGC_RING(T, SH);
-    mid_tile<T, FORM, SH>(A, blockIdx.x, s0, s1, s2, s3);
+    mid_tile<T, FORM, SH, SPLIT>(A, blockIdx.x, s0, s1, s2, s3);
 }
 
 // Both gradients of a layer in one launch, and the column sums' last step.
-template <class T, class SH>
+template <class T, class SH, bool SPLIT>
 __global__ __launch_bounds__(SH::kThreads) void k_mid_both(TileArgs dx, TileArgs dw,
                                                            int dx_blocks, int dw_blocks, Sums sums) {
     DGC_RING(T, SH);
     // each kind begins with the first die's workgroup
     const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
-        mid_tile<T, kDx, SH>(dx, id, s0, s1, s2, s3);
+        mid_tile<T, kDx, SH, SPLIT>(dx, id, s0, s1, s2, s3);
     else if (id >= dw0 && id < sum0)
-        mid_tile<T, kDw, SH>(dw, id - dw0, s0, s1, s2, s3);
+        mid_tile<T, kDw, SH, SPLIT>(dw, id - dw0, s0, s1, s2, s3);
     else if (id >= sum0)
         sum_columns<T, SH::kThreads>(sums, id - sum0, reinterpret_cast<float*>(s0));
 }

@@ -340,7 +340,10 @@ struct TileArgs {
     int64_t mt, nt;        // tiles over m and n
     int64_t per;           // steps of 64 per workgroup along the long axis
     int32_t splits, parts, outs;  // outs: outputs of kDw, else 1
-    int32_t fold;          // rows of dz in two halves (Product), or 0
+    int32_t pieces;        // of a, `low` elements apart
+    uint32_t inverse;      // 2^31 / pieces, rounded up
+    int32_t fold;          // rows of dz in two pieces (Product), or 0
+    int64_t low;
     float* part;           // the splits' sums, or null
     Finish fin;
 };
@@ -349,6 +352,33 @@ struct TileArgs {
 template <int FORM>
 __device__ __forceinline__ int64_t a_rows(const TileArgs& A) {
     return FORM == kDx && A.fold ? 2 * A.fold : A.M;
+}
+
+// How many steps of 64 a sum takes.  SPLIT: of an `a` in pieces (kDx, kDw).
+template <int FORM, bool SPLIT, class I>
+__device__ __forceinline__ I all_steps(const TileArgs& A, I ksteps) {
+    return ksteps * (SPLIT ? A.pieces : 1) * (FORM == kDx ? A.parts : 1);
+}
+
+// Step t of a sum: which of kDx's terms, which piece of a, and the first k.  The
+// pieces of one step of k follow each other, so that the second finds the other
+// operand in the die's L2.  (A template: the arithmetic costs 5% of 8192 x 8192 x
+// 4096, where a is whole; a branch among the loads cost 25%.)
+struct StepAt {
+    int term;
+    int64_t piece, k0;  // piece: elements into a
+};
+
+template <int FORM, bool SPLIT, class I>
+__device__ __forceinline__ StepAt step_at(const TileArgs& A, I t, I ksteps) {
+    const I all = SPLIT ? ksteps * A.pieces : ksteps;
+    const int term = FORM == kDx && t >= all ? 1 : 0;
+    const I u = t - term * all;
+    if constexpr (!SPLIT) return {term, 0, int64_t(u) * kStep};
+    // u / pieces without a branch: exact below 2^30 steps
+    const I k = I((uint64_t(u) * 2 * A.inverse) >> 32);
+    const int piece = int(u - k * A.pieces);
+    return {term, (piece > 0 ? A.low : 0) + (piece > 1 ? A.low : 0), int64_t(k) * kStep};
 }
 
 // Where workgroup `id` of a product works.  Workgroups go to the 8 dies in

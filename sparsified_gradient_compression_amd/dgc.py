@@ -38,6 +38,8 @@ DGC_ACT_RELU = 1
 DGC_ACT_SILU = 2
 DGC_ACT_GELU = 3
 DGC_ACT_GELU_TANH = 4
+DGC_DZ_ROUNDED = 256
+DGC_BACKWARD_ROUNDED = 2
 DGC_NORM_L2 = 0
 DGC_NORM_MAX = 1
 
@@ -553,11 +555,11 @@ def _type_codes():
     return _types
 
 
-def _act(act: str) -> int:
+def _act(act: str, rounded: bool = False) -> int:
     code = ACTIVATIONS.get(act)
     if code is None:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
-    return code
+    return code | DGC_DZ_ROUNDED if rounded else code
 
 
 _native = None
@@ -616,30 +618,31 @@ def _new(x, shape, dtype, stream):
     return t
 
 
-def _workspace(fn: str, m: int, n: int, k: int, backward: bool) -> int:
+def _workspace(fn: str, m: int, n: int, k: int, backward: bool, rounded: bool) -> int:
     out = ctypes.c_size_t(0)
-    _check(getattr(lib(), fn)(m, n, k, int(backward), ctypes.byref(out)), fn)
+    kind = DGC_BACKWARD_ROUNDED if backward and rounded else int(bool(backward))
+    _check(getattr(lib(), fn)(m, n, k, kind, ctypes.byref(out)), fn)
     return int(out.value)
 
 
-def dgc_linear_workspace_bytes(m: int, n: int, k: int, backward: bool = False) -> int:
-    return _workspace("dgc_linear_workspace_bytes", m, n, k, backward)
+def dgc_linear_workspace_bytes(m: int, n: int, k: int, backward: bool = False, rounded: bool = False) -> int:
+    return _workspace("dgc_linear_workspace_bytes", m, n, k, backward, rounded)
 
 
-def dgc_gated_ffn_workspace_bytes(m: int, d: int, f: int, backward: bool = False) -> int:
-    return _workspace("dgc_gated_ffn_workspace_bytes", m, d, f, backward)
+def dgc_gated_ffn_workspace_bytes(m: int, d: int, f: int, backward: bool = False, rounded: bool = False) -> int:
+    return _workspace("dgc_gated_ffn_workspace_bytes", m, d, f, backward, rounded)
 
 
-def linear_workspace(m: int, n: int, k: int, backward: bool = False, device="cuda"):
-    """A workspace for linear (or linear_backward) of these sizes."""
+def linear_workspace(m: int, n: int, k: int, backward: bool = False, device="cuda", rounded: bool = False):
+    """A workspace for linear (or linear_backward; `rounded`: with rounded=True alone) of these sizes."""
     import torch
-    return torch.empty(dgc_linear_workspace_bytes(m, n, k, backward), dtype=torch.uint8, device=device)
+    return torch.empty(dgc_linear_workspace_bytes(m, n, k, backward, rounded), dtype=torch.uint8, device=device)
 
 
-def gated_ffn_workspace(m: int, d: int, f: int, backward: bool = False, device="cuda"):
-    """A workspace for gated_ffn (or gated_ffn_backward) of these sizes."""
+def gated_ffn_workspace(m: int, d: int, f: int, backward: bool = False, device="cuda", rounded: bool = False):
+    """A workspace for gated_ffn (or gated_ffn_backward; `rounded`: with rounded=True alone) of these sizes."""
     import torch
-    return torch.empty(dgc_gated_ffn_workspace_bytes(m, d, f, backward), dtype=torch.uint8, device=device)
+    return torch.empty(dgc_gated_ffn_workspace_bytes(m, d, f, backward, rounded), dtype=torch.uint8, device=device)
 
 
 def linear(x, w, bias=None, residual=None, act: str = "none", out=None, pre=None, workspace=None, stream=None):
@@ -657,13 +660,18 @@ def linear(x, w, bias=None, residual=None, act: str = "none", out=None, pre=None
 
 
 def linear_backward(dy, x, w, pre=None, act: str = "none", dx=None, dw=None, dbias=None, workspace=None,
-                    stream=None):
+                    stream=None, rounded: bool = False):
     """Gradients of linear for the incoming dy [m, n]: with dz = dy * act'(pre), writes each given one of
     dx [m, k] = dz w, dw [n, k] = dz^T x and dbias [n] = the column sums of dz.  dw and dbias are of x's
-    type or float32 (the same for both): views of a learner's flat gradient.  Returns (dx, dw, dbias)."""
+    type or float32 (the same for both): views of a learner's flat gradient.  Returns (dx, dw, dbias).
+
+    The matrix units take 16-bit operands: behind an activation dz goes to them as the sum of two numbers of
+    x's type (three for a bfloat16 x and a float32 dw), so that the gradients are off by little more than
+    their own rounding.  `rounded`: as one number, in half the time, with 1.4 times that error, also in a
+    float32 dw."""
     if workspace is None:
-        workspace = _fresh(dgc_linear_workspace_bytes(x.shape[0], w.shape[0], x.shape[-1], True), x, stream)
-    _check(_torch_calls().linear_backward(_act(act), dy, x, w, pre, dx, dw, dbias, workspace, _stream_on(x, stream)),
+        workspace = _fresh(dgc_linear_workspace_bytes(x.shape[0], w.shape[0], x.shape[-1], True, rounded), x, stream)
+    _check(_torch_calls().linear_backward(_act(act, rounded), dy, x, w, pre, dx, dw, dbias, workspace, _stream_on(x, stream)),
            "dgc_linear_backward")
     return dx, dw, dbias
 
@@ -681,12 +689,15 @@ def gated_ffn(x, w_gate, w_up, act: str = "silu", out=None, gate=None, up=None, 
 
 
 def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None, dw_gate=None, dw_up=None,
-                       workspace=None, stream=None):
+                       workspace=None, stream=None, rounded: bool = False):
     """Gradients of gated_ffn for the incoming dh [m, f] and the saved gate and up: writes dx [m, d] if
-    given, and dw_gate and dw_up [f, d] (together; x's type or float32).  Returns (dx, dw_gate, dw_up)."""
+    given, and dw_gate and dw_up [f, d] (together; x's type or float32).  Returns (dx, dw_gate, dw_up).
+
+    `rounded`: as for linear_backward, of dh * up * act'(gate) and dh * act(gate)."""
     if workspace is None:
-        workspace = _fresh(dgc_gated_ffn_workspace_bytes(x.shape[0], x.shape[-1], w_gate.shape[0], True), x, stream)
-    _check(_torch_calls().gated_ffn_backward(_act(act), dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
+        workspace = _fresh(dgc_gated_ffn_workspace_bytes(x.shape[0], x.shape[-1], w_gate.shape[0], True, rounded), x,
+                           stream)
+    _check(_torch_calls().gated_ffn_backward(_act(act, rounded), dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
                                              _stream_on(x, stream)), "dgc_gated_ffn_backward")
     return dx, dw_gate, dw_up
 
