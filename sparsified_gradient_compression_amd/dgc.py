@@ -594,27 +594,35 @@ def _stream_on(x, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
+def _torch_stream(stream):
+    """`stream` as torch's object, if it is a handle."""
+    import torch
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for work on `stream` (None: the current one), of that stream's own pool: what the current stream's
+    pool hands out may be a block that work on the current stream still uses."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _fresh(size: int, x, stream):
-    """A workspace of `size` bytes for one call; it stays reserved until the call's stream has passed."""
+    """A workspace of `size` bytes for one call."""
     import torch
-    t = torch.empty(size, dtype=torch.uint8, device=x.device)
-    _hold(t, stream)
-    return t
-
-
-def _hold(t, stream):
-    """A tensor made here for work on `stream` is not reused before that work is done."""
-    import torch
-    if stream is not None and not isinstance(stream, int):
-        t.record_stream(stream)
-    elif stream is not None and stream != torch.cuda.current_stream().cuda_stream:
-        t.record_stream(torch.cuda.ExternalStream(stream))
+    return _empty(size, torch.uint8, x.device, stream if x.is_cuda else None)
 
 
 def _new(x, shape, dtype, stream):
+    """An output for the caller, who will use it on the current stream too."""
     import torch
-    t = torch.empty(shape, dtype=dtype, device=x.device)
-    _hold(t, stream)
+    if stream is None or not x.is_cuda:
+        return _empty(shape, dtype, x.device, None)
+    t = _empty(shape, dtype, x.device, stream)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -726,10 +734,11 @@ class GradSet:
         if None in codes:
             raise ValueError("gradients must be bfloat16, float16 or float32")
         self.n = sum(self.sizes)
-        self.workspace = torch.empty(dgc_gradset_bytes(self.sizes, codes), dtype=torch.uint8, device=device)
+        self.workspace = _empty(dgc_gradset_bytes(self.sizes, codes), torch.uint8, device, stream)
         self.device = self.workspace.get_device()
-        self.total = torch.empty(1, dtype=torch.float64, device=device)
-        self.scale = torch.empty(1, dtype=torch.float32, device=device)
+        self.total = _empty(1, torch.float64, device, stream)
+        self.scale = _empty(1, torch.float32, device, stream)
+        self._own_stream = _stream(stream) if self.workspace.is_cuda else None  # whose pool these come from
         handle, s = ctypes.c_void_p(), _i64(self.sizes)
         t = np.ascontiguousarray(np.asarray(codes, np.int32))
         self._layout = s.tobytes(), t.tobytes(), self.device
@@ -738,10 +747,11 @@ class GradSet:
         self.set = handle
 
     def _on(self, stream) -> int:
-        """The handle of `stream`, which the set's own tensors are held for."""
+        """The handle of `stream`.  The set's own tensors are not reused before work on it is done."""
         handle = _stream_on(self.total, stream)
-        for t in (self.workspace, self.total, self.scale):
-            _hold(t, stream)
+        if handle != self._own_stream:
+            for t in (self.workspace, self.total, self.scale):
+                t.record_stream(_torch_stream(handle))
         return handle
 
     @staticmethod
