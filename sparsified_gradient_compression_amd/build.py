@@ -24,7 +24,7 @@ BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("dgc_api.hip", "dgc_gradset.hip", "dgc_layers.hip", "layers_bf16.hip", "layers_fp16.hip")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
-                     ("layers.hpp", "layers_big.hpp", "layers_direct.hpp", "layers_elem.hpp", "layers_guarded.hpp", "layers_mid.hpp", "layers_thin.hpp", "layers_launch.hpp", "layers_tile.hpp",
+                     ("launch_grid.hpp", "layers.hpp", "layers_big.hpp", "layers_direct.hpp", "layers_elem.hpp", "layers_guarded.hpp", "layers_mid.hpp", "layers_thin.hpp", "layers_launch.hpp", "layers_tile.hpp",
                       "dgc_device.hpp", "kernel_fused.hpp", "kernels_binlocal.hpp", "kernels_sampled.hpp",
                       "kernels_compress.hpp", "kernels_codec.hpp", "kernels_shared.hpp", "kernels_tensor.hpp")] + [os.path.join(ROOT, "include", "dgc.h")]
 

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "dgc.h"
+#include "launch_grid.hpp"
 
 namespace {
 
@@ -240,7 +241,7 @@ __device__ __forceinline__ float factor(double norm, double clip, double unscale
 
 // What the second pass needs beside the tensors.
 struct Scaling {
-    int parts, most;
+    int parts, most, pieces;  // pieces: a workgroup each
     double clip, unscale;
     double* out_norm;
     float* out_scale;
@@ -306,7 +307,8 @@ __device__ __forceinline__ void scale_piece(const T* p, O* o, int64_t at, int64_
 template <bool FLAT, bool STREAM, bool FEW>
 __global__ __launch_bounds__(kScaleThreads) void k_set_scale(Tables tb, Scaling k) {
     __shared__ double lds[kThreads / 64];
-    const int64_t pair = blockIdx.x / 2;
+    const int64_t piece = dgc::block_number(), pair = piece / 2;
+    if (piece >= k.pieces) return;
     Tensor x = tb.owner[pair / kOwner];
     if (pair >= x.pair1) {
         // a later tensor, one of the at most 64 that start behind the entry's
@@ -316,13 +318,13 @@ __global__ __launch_bounds__(kScaleThreads) void k_set_scale(Tables tb, Scaling 
         const int later = __builtin_popcountll(__ballot(mine < tb.count && start <= pair));
         x = tb.tensors[__builtin_amdgcn_readfirstlane(x.index + later)];
     }
-    const int64_t at = (pair - x.pair0) * kPair + blockIdx.x % 2 * kPiece;
+    const int64_t at = (pair - x.pair0) * kPair + piece % 2 * kPiece;
     const float known = FEW ? 0.0f : *tb.scale;
     const auto f = [&]() -> float {
         if constexpr (!FEW) return known;
         const double norm = whole_norm<kScaleThreads>(tb.part, k.parts, k.most, k.unscale, lds);
         const float s = factor(norm, k.clip, k.unscale);
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (piece == 0 && threadIdx.x == 0) {
             if (k.out_norm) *k.out_norm = norm;
             if (k.out_scale) *k.out_scale = s;
         }
@@ -441,13 +443,14 @@ int scale_pass(const dgc_gradset* s, const void* const* grads, void* const* outs
     l.parts = s->parts;
     // one round of workgroups and a few partials each: no launch in between
     const int64_t blocks = 2 * s->pairs;
+    l.pieces = int(blocks);
     const bool few = blocks > 0 && blocks <= 2 * kMostBlocks && s->parts <= 2 * kThreads;
     if (!few) k_set_total<<<1, kThreads, 0, stream>>>(s->tables, l);
     const bool large = s->bytes + (FLAT ? 4 * s->elements : s->bytes) > kLarge;
     if (blocks > 0) {
         const auto kernel = few ? k_set_scale<FLAT, false, true>
                                 : large ? k_set_scale<FLAT, true, false> : k_set_scale<FLAT, false, false>;
-        kernel<<<dim3(unsigned(blocks)), kScaleThreads, 0, stream>>>(s->tables, l);
+        kernel<<<dgc::grid_of(blocks, kScaleThreads), kScaleThreads, 0, stream>>>(s->tables, l);
     }
     return hipGetLastError() == hipSuccess ? DGC_OK : DGC_EHIP;
 }
@@ -530,7 +533,7 @@ int dgc_gradset_norm(const dgc_gradset* s, const void* const* grads, int32_t nor
     const int rc = norm_pass(s, grads, nullptr, norm, stream);
     if (rc != DGC_OK) return rc;
     k_set_total<<<1, kThreads, 0, stream>>>(
-        s->tables, Scaling{s->parts, norm, 0.0, unscale, out_norm, nullptr, nullptr});
+        s->tables, Scaling{s->parts, norm, 0, 0.0, unscale, out_norm, nullptr, nullptr});
     return hipGetLastError() == hipSuccess ? DGC_OK : DGC_EHIP;
 }
 
@@ -538,14 +541,14 @@ int dgc_gradset_clip(const dgc_gradset* s, const void* const* grads, void* const
                      double clip, int32_t norm, double unscale, double* out_norm,
                      float* out_scale, hipStream_t stream) {
     return scale_pass<false>(s, grads, outs,
-                             Scaling{0, norm, clip, unscale, out_norm, out_scale, nullptr}, stream);
+                             Scaling{0, norm, 0, clip, unscale, out_norm, out_scale, nullptr}, stream);
 }
 
 int dgc_gradset_pack(const dgc_gradset* s, const void* const* grads, float* flat, double clip,
                      int32_t norm, double unscale, double* out_norm, float* out_scale,
                      hipStream_t stream) {
     return scale_pass<true>(s, grads, nullptr,
-                            Scaling{0, norm, clip, unscale, out_norm, out_scale, flat}, stream);
+                            Scaling{0, norm, 0, clip, unscale, out_norm, out_scale, flat}, stream);
 }
 
 void dgc_gradset_destroy(dgc_gradset* s) { delete s; }

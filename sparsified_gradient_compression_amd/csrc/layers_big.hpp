@@ -48,7 +48,9 @@ __global__ __launch_bounds__(512, 2) void k_big(TileArgs A) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int wm = wave >> 2, wn = wave & 3;
 
-    const Spot at_tile = spot<FORM>(A, int(blockIdx.x));
+    const int64_t id = block_number();
+    if (id >= all_blocks<FORM>(A)) return;
+    const Spot at_tile = spot<FORM>(A, int(id));
     const int split = at_tile.split, z = at_tile.z;
     const int64_t m0 = at_tile.tm * 256, n0 = at_tile.tn * (PAIR ? 128 : 256);
 

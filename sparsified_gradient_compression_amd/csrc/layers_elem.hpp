@@ -127,7 +127,7 @@ __device__ __forceinline__ float dz_scale(const SlopeArgs& A, float* lds) {
     // its exponent, where it is 2^-86 or more; 0 and less: as 2^-86
     const int e = int(__builtin_bit_cast(uint32_t, most) >> 23) - 127;
     const int up = most > 0.0f ? 14 - (e > -86 ? e : -86) : 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
+    if (block_number() == 0 && threadIdx.x == 0)
         *A.unscale = __builtin_bit_cast(float, uint32_t(127 - up) << 23);
     return __builtin_bit_cast(float, uint32_t(127 + up) << 23);
 }
@@ -214,7 +214,7 @@ __device__ __forceinline__ void sum_columns(const Sums& A, int64_t id, float* ld
 template <class T>
 __global__ __launch_bounds__(256) void k_sum_columns(Sums A) {
     __shared__ float lds[256];
-    sum_columns<T, 256>(A, blockIdx.x, lds);
+    sum_columns<T, 256>(A, block_number(), lds);
 }
 
 // da = dh * up * act'(gate), db = dh * act(gate), rows of `ld` elements; C (4
@@ -275,7 +275,7 @@ __device__ __forceinline__ void repack_block(const Repack& r, int64_t id) {
 template <class T, int P>
 __global__ __launch_bounds__(256) void k_prepare(SlopeArgs A, int64_t slope_blocks, Repack r) {
     __shared__ float sums[4][512];
-    const int64_t id = blockIdx.x;
+    const int64_t id = block_number();
     if (id >= slope_blocks) {
         repack_block(r, id - slope_blocks);
         return;

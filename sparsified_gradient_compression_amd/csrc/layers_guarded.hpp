@@ -195,7 +195,8 @@ constexpr int kGuardedLds = kGuardedGroups * 4 * kGuardedSide;
 template <class T, int FORM, bool SPLIT>
 __global__ __launch_bounds__(kGuardedThreads) void k_guarded(TileArgs A) {
     __shared__ __align__(16) T smem[kGuardedLds];
-    guarded_tile<T, FORM, SPLIT>(A, blockIdx.x, smem);
+    const int64_t id = block_number();
+    if (id < all_blocks<FORM>(A)) guarded_tile<T, FORM, SPLIT>(A, int(id), smem);
 }
 
 // Both gradients of a layer in one launch, and the column sums' last step.
@@ -205,12 +206,12 @@ __global__ __launch_bounds__(kGuardedThreads) void k_guarded_both(TileArgs dx, T
                                                                   Sums sums) {
     __shared__ __align__(16) T smem[kGuardedLds];
     // each kind begins with the first die's workgroup
-    const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
+    const int64_t id = block_number(), dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
-        guarded_tile<T, kDx, SPLIT>(dx, id, smem);
+        guarded_tile<T, kDx, SPLIT>(dx, int(id), smem);
     else if (id >= dw0 && id < sum0)
-        guarded_tile<T, kDw, SPLIT>(dw, id - dw0, smem);
-    else if (id >= sum0)
+        guarded_tile<T, kDw, SPLIT>(dw, int(id - dw0), smem);
+    else if (id >= sum0 && sums.out)
         sum_columns<T, kGuardedThreads>(sums, id - sum0, reinterpret_cast<float*>(smem));
 }
 

@@ -21,18 +21,18 @@ template <class T, int FORM, bool SPLIT>
 int launch_tiles(const TileArgs& a, const Cut& c, hipStream_t s) {
     const int64_t blocks = a.mt * a.nt * (FORM == kDw ? a.parts : 1) * c.splits;
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const auto grid = [=](int threads) { return grid_of(blocks, threads); };
     switch (c.tile) {
-        case kGuarded: k_guarded<T, FORM, SPLIT><<<grid, kGuardedThreads, 0, s>>>(a); break;
-        case kMid32: k_mid<T, FORM, Shape32, SPLIT><<<grid, 1024, 0, s>>>(a); break;
-        case kMid64: k_mid<T, FORM, Shape64, SPLIT><<<grid, 512, 0, s>>>(a); break;
-        case kLight: k_mid<T, FORM, ShapeLight, SPLIT><<<grid, 256, 0, s>>>(a); break;
-        case kMid128: k_mid<T, FORM, Shape128, SPLIT><<<grid, 512, 0, s>>>(a); break;
-        case kPair128: k_mid<T, FORM, ShapePair, SPLIT><<<grid, 512, 0, s>>>(a); break;
-        case kBig: k_big<T, FORM, SPLIT><<<grid, 512, 0, s>>>(a); break;
+        case kGuarded: k_guarded<T, FORM, SPLIT><<<grid(kGuardedThreads), kGuardedThreads, 0, s>>>(a); break;
+        case kMid32: k_mid<T, FORM, Shape32, SPLIT><<<grid(1024), 1024, 0, s>>>(a); break;
+        case kMid64: k_mid<T, FORM, Shape64, SPLIT><<<grid(512), 512, 0, s>>>(a); break;
+        case kLight: k_mid<T, FORM, ShapeLight, SPLIT><<<grid(256), 256, 0, s>>>(a); break;
+        case kMid128: k_mid<T, FORM, Shape128, SPLIT><<<grid(512), 512, 0, s>>>(a); break;
+        case kPair128: k_mid<T, FORM, ShapePair, SPLIT><<<grid(512), 512, 0, s>>>(a); break;
+        case kBig: k_big<T, FORM, SPLIT><<<grid(512), 512, 0, s>>>(a); break;
         default:
             if constexpr (FORM == kRows || FORM == kPair) {
-                const dim3 rows(static_cast<unsigned>(cdiv64(a.N, 16)));
+                const dim3 rows = grid_of(cdiv64(a.N, 16), 512);
                 if (a.M <= 16)
                     k_thin<T, FORM == kPair, 1><<<rows, 512, 0, s>>>(a);
                 else
@@ -91,9 +91,9 @@ int Launch<T>::product(const Product& p, const Cut& c, void* ws, hipStream_t s) 
     const int64_t blocks = cdiv64(cdiv64(p.n, 4) * p.m * a.outs, 64);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (p.form == kPair)
-        k_join<T, true><<<dim3(unsigned(blocks)), 64, 0, s>>>(a);
+        k_join<T, true><<<grid_of(blocks, 64), 64, 0, s>>>(a);
     else
-        k_join<T, false><<<dim3(unsigned(blocks)), 64, 0, s>>>(a);
+        k_join<T, false><<<grid_of(blocks, 64), 64, 0, s>>>(a);
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }
@@ -104,16 +104,16 @@ int launch_both(const TileArgs& x, const TileArgs& w, int tile, const Sums& sums
     const int64_t blocks = (nx + 7) / 8 * 8 + nw + (sums.out ? cdiv64(sums.N, 32) : 0);
     if (blocks > 0x7FFFFFFF) return DGC_EINVAL;
     if (blocks == 0) return DGC_OK;
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const auto grid = [=](int threads) { return grid_of(blocks, threads); };
     switch (tile) {
         case kGuarded:
-            k_guarded_both<T, SPLIT><<<grid, kGuardedThreads, 0, s>>>(x, w, int(nx), int(nw), sums);
+            k_guarded_both<T, SPLIT><<<grid(kGuardedThreads), kGuardedThreads, 0, s>>>(x, w, int(nx), int(nw), sums);
             break;
-        case kMid32: k_mid_both<T, Shape32, SPLIT><<<grid, 1024, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kMid64: k_mid_both<T, Shape64, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kLight: k_mid_both<T, ShapeLight, SPLIT><<<grid, 256, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kMid128: k_mid_both<T, Shape128, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
-        case kPair128: k_mid_both<T, ShapePair, SPLIT><<<grid, 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid32: k_mid_both<T, Shape32, SPLIT><<<grid(1024), 1024, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid64: k_mid_both<T, Shape64, SPLIT><<<grid(512), 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kLight: k_mid_both<T, ShapeLight, SPLIT><<<grid(256), 256, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kMid128: k_mid_both<T, Shape128, SPLIT><<<grid(512), 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
+        case kPair128: k_mid_both<T, ShapePair, SPLIT><<<grid(512), 512, 0, s>>>(x, w, int(nx), int(nw), sums); break;
         default: return DGC_EINVAL;
     }
     DGC_LAYERS_CHECK();
@@ -154,7 +154,7 @@ int Launch<T>::prepare(SlopeArgs a, const Repack& r, hipStream_t s) {
     auto kernel = a.pieces == 1 ? k_prepare<T, 1> : k_prepare<T, 2>;
     if constexpr (!std::is_same_v<T, _Float16>)
         if (a.pieces == 3) kernel = k_prepare<T, 3>;
-    kernel<<<dim3(static_cast<unsigned>(blocks)), 256, 0, s>>>(a, slopes, r);
+    kernel<<<grid_of(blocks, 256), 256, 0, s>>>(a, slopes, r);
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }
@@ -162,7 +162,7 @@ int Launch<T>::prepare(SlopeArgs a, const Repack& r, hipStream_t s) {
 template <class T>
 int Launch<T>::sum(const Sums& a, hipStream_t s) {
     if (!a.out || a.N == 0) return DGC_OK;
-    k_sum_columns<T><<<dim3(static_cast<unsigned>(cdiv64(a.N, 32))), 256, 0, s>>>(a);
+    k_sum_columns<T><<<grid_of(cdiv64(a.N, 32), 256), 256, 0, s>>>(a);
     DGC_LAYERS_CHECK();
     return DGC_OK;
 }

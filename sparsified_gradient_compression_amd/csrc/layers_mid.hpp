@@ -179,7 +179,8 @@ __device__ __forceinline__ void mid_tile(const TileArgs& A, int id, T* s0, T* s1
 template <class T, int FORM, class SH, bool SPLIT>
 __global__ __launch_bounds__(SH::kThreads) void k_mid(TileArgs A) {
     DGC_RING(T, SH);
-    mid_tile<T, FORM, SH, SPLIT>(A, blockIdx.x, s0, s1, s2, s3);
+    const int64_t id = block_number();
+    if (id < all_blocks<FORM>(A)) mid_tile<T, FORM, SH, SPLIT>(A, int(id), s0, s1, s2, s3);
 }
 
 // Both gradients of a layer in one launch, and the column sums' last step.
@@ -188,12 +189,12 @@ __global__ __launch_bounds__(SH::kThreads) void k_mid_both(TileArgs dx, TileArgs
                                                            int dx_blocks, int dw_blocks, Sums sums) {
     DGC_RING(T, SH);
     // each kind begins with the first die's workgroup
-    const int id = blockIdx.x, dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
+    const int64_t id = block_number(), dw0 = (dx_blocks + 7) & ~7, sum0 = dw0 + dw_blocks;
     if (id < dx_blocks)
-        mid_tile<T, kDx, SH, SPLIT>(dx, id, s0, s1, s2, s3);
+        mid_tile<T, kDx, SH, SPLIT>(dx, int(id), s0, s1, s2, s3);
     else if (id >= dw0 && id < sum0)
-        mid_tile<T, kDw, SH, SPLIT>(dw, id - dw0, s0, s1, s2, s3);
-    else if (id >= sum0)
+        mid_tile<T, kDw, SH, SPLIT>(dw, int(id - dw0), s0, s1, s2, s3);
+    else if (id >= sum0 && sums.out)
         sum_columns<T, SH::kThreads>(sums, id - sum0, reinterpret_cast<float*>(s0));
 }
 

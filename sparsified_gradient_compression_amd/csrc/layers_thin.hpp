@@ -24,7 +24,7 @@ __global__ __launch_bounds__(512) void k_thin(TileArgs A) {
     __shared__ __align__(16) float sums[kWaves][P][MT * 16][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i = lane & 15, g = lane >> 4;
-    const int64_t n0 = int64_t(blockIdx.x) * 16;
+    const int64_t n0 = block_number() * 16;
     // rows that do not exist repeat the last one; their sums are not stored
     const int64_t n = n0 + i < A.N ? n0 + i : A.N - 1;
     const T* w[P];

@@ -12,6 +12,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "launch_grid.hpp"
 #include "layers.hpp"
 
 namespace dgc {
@@ -390,6 +391,12 @@ struct Spot {
     int64_t tm, tn;
 };
 
+// A product's workgroups.
+template <int FORM>
+__device__ __forceinline__ int64_t all_blocks(const TileArgs& A) {
+    return A.mt * A.nt * (FORM == kDw ? A.outs : 1) * A.splits;
+}
+
 template <int FORM>
 __device__ __forceinline__ Spot spot(const TileArgs& A, int id) {
     const int mt = int(A.mt), nt = int(A.nt), tiles = mt * nt;
@@ -493,7 +500,7 @@ __device__ __forceinline__ void put_tile(float* row, int r, int col, int j, int 
 template <class T, bool PAIR>
 __global__ __launch_bounds__(64) void k_join(TileArgs A) {
     const int64_t groups = (A.N + 3) / 4, z_count = A.outs;
-    int64_t id = int64_t(blockIdx.x) * 64 + threadIdx.x;
+    int64_t id = block_number() * 64 + threadIdx.x;
     if (id >= groups * A.M * z_count) return;
     const int z = int(id / (groups * A.M));
     id -= z * groups * A.M;
