@@ -299,8 +299,7 @@ Space space(bool gated, int32_t backward, int64_t m, int64_t n, int64_t k) {
 }
 
 // Notes a matrix that is to be laid out anew at `to`, and returns what to use.
-Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
-    if (!pack || rows == 0 || cols == 0 || direct(a, cols)) return a;
+Mat anew(Repack& r, Mat a, int64_t rows, int64_t cols, void* to) {
     r.from[r.count] = a.p;
     r.to[r.count] = to;
     r.ld[r.count] = a.ld;
@@ -308,6 +307,23 @@ Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
     r.cols[r.count] = cols;
     ++r.count;
     return {to, pad8(cols), true};
+}
+
+// The same for one that does not lie on 16 bytes, if laying out pays.
+Mat packed(Repack& r, bool pack, Mat a, int64_t rows, int64_t cols, void* to) {
+    const bool as_is = !pack || rows == 0 || cols == 0 || direct(a, cols);
+    return as_is ? a : anew(r, a, rows, cols, to);
+}
+
+// Both weights of a gated block: the kernels that take rows on 16 bytes take
+// them of one length too.  One whose rows are as long as a copy's stays.
+void packed_pair(Repack& r, bool pack, Mat& a, Mat& b, int64_t rows, int64_t cols, void* to_a,
+                 void* to_b) {
+    if (!pack || rows == 0 || cols == 0) return;
+    const bool da = direct(a, cols), db = direct(b, cols);
+    if (da && db && a.ld == b.ld) return;
+    if (!da || a.ld != pad8(cols)) a = anew(r, a, rows, cols, to_a);
+    if (!db || b.ld != pad8(cols)) b = anew(r, b, rows, cols, to_b);
 }
 
 int run_product(int64_t type, const Product& p, void* ws, hipStream_t s) {
@@ -515,8 +531,9 @@ int dgc_gated_ffn(const dgc_gated_ffn_args* a, void* workspace, size_t workspace
     p.n = f;
     p.k = d;
     p.a[0] = packed(r, sp.pack, {a->x, a->ldx}, m, d, ws + sp.x);
-    p.b[0] = packed(r, sp.pack, {a->w_gate, a->ldw_gate}, f, d, ws + sp.w);
-    p.b[1] = packed(r, sp.pack, {a->w_up, a->ldw_up}, f, d, ws + sp.w2);
+    p.b[0] = {a->w_gate, a->ldw_gate};
+    p.b[1] = {a->w_up, a->ldw_up};
+    packed_pair(r, sp.pack, p.b[0], p.b[1], f, d, ws + sp.w, ws + sp.w2);
     rc = run_prepare(a->type, SlopeArgs{}, r, stream);
     if (rc != DGC_OK) return rc;
     p.fin.out[0] = a->h;
@@ -554,10 +571,7 @@ int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* a, void* workspace
     Repack r;
     Mat x{a->x, a->ldx}, wg{a->w_gate, a->ldw_gate}, wu{a->w_up, a->ldw_up};
     if (a->dw_gate) x = packed(r, sp.pack, x, m, d, ws + sp.x);
-    if (a->dx) {
-        wg = packed(r, sp.pack, wg, f, d, ws + sp.w);
-        wu = packed(r, sp.pack, wu, f, d, ws + sp.w2);
-    }
+    if (a->dx) packed_pair(r, sp.pack, wg, wu, f, d, ws + sp.w, ws + sp.w2);
     SlopeArgs sl;
     sl.M = m;
     sl.N = f;

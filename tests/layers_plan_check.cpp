@@ -1,0 +1,119 @@
+// layers_plan_check.cpp -- what the layer operators' host code hands to its
+// launchers, which are replaced here: nothing runs on a GPU, and the addresses
+// are never followed.  Built with dgc_layers.hip and run by
+// tests/test_layers_plan.py.
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+
+#include "layers.hpp"
+
+#define CHECK(c)                                                             \
+    do {                                                                     \
+        if (!(c)) {                                                          \
+            std::fprintf(stderr, "check failed: %s (line %d)\n", #c, __LINE__); \
+            std::abort();                                                    \
+        }                                                                    \
+    } while (0)
+
+namespace dgc {
+namespace layers {
+
+std::vector<Product> products;
+std::vector<int> tiles;
+std::vector<Repack> repacks;
+
+template <class T>
+int Launch<T>::product(const Product& p, const Cut& c, void*, hipStream_t) {
+    products.push_back(p);
+    tiles.push_back(c.tile);
+    return DGC_OK;
+}
+
+template <class T>
+int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums&, hipStream_t) {
+    products.push_back(dx);
+    products.push_back(dw);
+    tiles.push_back(tile);
+    return DGC_OK;
+}
+
+template <class T>
+int Launch<T>::prepare(SlopeArgs, const Repack& r, hipStream_t) {
+    repacks.push_back(r);
+    return DGC_OK;
+}
+
+template <class T>
+int Launch<T>::sum(const Sums&, hipStream_t) {
+    return DGC_OK;
+}
+
+template struct Launch<__bf16>;
+template struct Launch<_Float16>;
+
+}  // namespace layers
+}  // namespace dgc
+
+using namespace dgc::layers;
+
+namespace {
+
+void* const kSpace = reinterpret_cast<void*>(uintptr_t(1) << 40);
+
+const void* at(int i, int off = 0) {
+    return reinterpret_cast<const void*>((uintptr_t(i) << 34) + uintptr_t(off));
+}
+
+void* out(int i) { return const_cast<void*>(at(i)); }
+
+void reset() {
+    products.clear();
+    tiles.clear();
+    repacks.clear();
+}
+
+// Every product takes rows on 16 bytes, and `copies` matrices were laid out anew for it.
+void check_direct(int copies) {
+    CHECK(!products.empty() && repacks.size() == 1);
+    for (const Product& p : products) CHECK(direct(p));
+    for (int t : tiles) CHECK(t != kGuarded);
+    CHECK(repacks[0].count == copies);
+}
+
+// A gated block of m x d and f x d, its weights' rows ld_g and ld_u elements
+// apart and starting off_g and off_u bytes off 16.
+void gated(int64_t m, int64_t d, int64_t f, int64_t ld_g, int64_t ld_u, int off_g, int off_u,
+           int copies) {
+    size_t bytes = 0;
+    reset();
+    CHECK(dgc_gated_ffn_workspace_bytes(m, d, f, 0, &bytes) == DGC_OK);
+    dgc_gated_ffn_args a{DGC_BF16, DGC_ACT_SILU, m, d, f, at(1), d, at(2, off_g), ld_g,
+                         at(3, off_u), ld_u, out(4), f, out(5), f, out(6), f};
+    CHECK(dgc_gated_ffn(&a, kSpace, bytes, nullptr) == DGC_OK);
+    check_direct(copies);
+    reset();
+    CHECK(dgc_gated_ffn_workspace_bytes(m, d, f, 1, &bytes) == DGC_OK);
+    dgc_gated_ffn_backward_args b{DGC_BF16, DGC_BF16, DGC_ACT_SILU, m, d, f, at(7), f, at(1), d,
+                                  at(2, off_g), ld_g, at(3, off_u), ld_u, at(5), f, at(6), f,
+                                  out(8), d, out(9), d, out(10), d};
+    CHECK(dgc_gated_ffn_backward(&b, kSpace, bytes, nullptr) == DGC_OK);
+    check_direct(copies);
+}
+
+}  // namespace
+
+int main() {
+    const int64_t m = 2048, d = 1024, f = 4096;
+    gated(m, d, f, d, d, 0, 0, 0);
+    gated(m, d, f, d + 64, d + 64, 0, 0, 0);
+    gated(m, d, f, d + 8, d, 0, 0, 1);    // the one in rows of their own width stays
+    gated(m, d, f, d, d + 8, 0, 0, 1);
+    gated(m, d, f, d + 8, d + 16, 0, 0, 2);
+    gated(m, d, f, d, d, 2, 0, 1);        // one of them off 16 bytes
+    gated(m, d, f, d, d + 1, 0, 0, 1);
+    gated(m, d, f, d + 64, d + 64, 0, 6, 2);
+    gated(m, d, f, d + 3, d + 5, 4, 2, 2);
+    std::printf("plan check: ok\n");
+    return 0;
+}
