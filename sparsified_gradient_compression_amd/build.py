@@ -1,5 +1,5 @@
-"""Build libdgc.so for gfx950 with hipcc, and the torch module over it with
-g++, in-tree.
+"""Build libdgc.so for gfx950 with hipcc, and, where torch and g++ are there,
+the torch module over it, in-tree.
 
     python -m sparsified_gradient_compression_amd.build
 
@@ -9,6 +9,7 @@ method's arithmetic is defined.
 """
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -65,6 +66,11 @@ def hipcc():
     return exe
 
 
+def has_binding():
+    """Whether the torch module can be built here.  The library itself needs hipcc alone."""
+    return importlib.util.find_spec("torch") is not None and shutil.which("g++") is not None
+
+
 def build(verbose=True):
     """Compile libdgc.so and the torch module over it (always recompiles)."""
     os.makedirs(LIBDIR, exist_ok=True)
@@ -82,18 +88,25 @@ def build(verbose=True):
                       zip(SOURCES, objects)))
     run([hipcc(), f"--offload-arch={ARCH}", "-shared"] + objects + ["-o", tmp])
     os.replace(tmp, LIB)
-    run(binding_command(BINDING + ".tmp"))
-    os.replace(BINDING + ".tmp", BINDING)
     for o in objects:
         os.remove(o)
+    if has_binding():
+        run(binding_command(BINDING + ".tmp"))
+        os.replace(BINDING + ".tmp", BINDING)
+    elif os.path.exists(BINDING):
+        os.remove(BINDING)  # of another library
     return LIB
 
 
 def is_stale():
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    built, sources = [LIB], list(DEPENDS)
+    if has_binding():
+        built.append(BINDING)
+        sources.append(BINDING_SOURCE)
+    if not all(map(os.path.exists, built)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in DEPENDS + [BINDING_SOURCE])
+    t = min(map(os.path.getmtime, built))
+    return any(os.path.getmtime(f) > t for f in sources)
 
 
 if __name__ == "__main__":
