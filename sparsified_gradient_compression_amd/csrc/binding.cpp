@@ -5,8 +5,10 @@
 // gradient set has hundreds of tensors: read through Python's attributes,
 // their types, shapes and addresses would take longer than the kernels
 // (161 gradients and outputs: 70 us there, 4 us here).
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -21,10 +23,29 @@ struct Refusal {
 
 [[noreturn]] void refuse(const std::string& what) { throw Refusal{what}; }
 
+const at::Tensor& unpacked(PyObject* o, const char* name) {
+    if (!THPVariable_Check(o)) refuse(std::string(name) + ": expected a tensor");
+    return THPVariable_Unpack(o);
+}
+
 const at::Tensor* tensor(PyObject* o, const char* name) {
     if (o == Py_None) return nullptr;
-    if (!THPVariable_Check(o)) refuse(std::string(name) + ": expected a tensor");
-    return &THPVariable_Unpack(o);
+    const at::Tensor& t = unpacked(o, name);
+    // what these calls write has no history, as of torch's own calls with out=
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse(std::string(name) + ": requires a gradient, and these calls record none: call them under torch.no_grad()");
+    return &t;
+}
+
+// Tensors that a call has written: what saved one of them for a backward pass finds out.
+void wrote(std::initializer_list<const at::Tensor*> outs) {
+    for (const at::Tensor* t : outs)
+        if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
+int done(int rc, std::initializer_list<const at::Tensor*> outs) {
+    if (rc == DGC_OK) wrote(outs);
+    return rc;
 }
 
 const at::Tensor& needed(PyObject* o, const char* name) {
@@ -157,12 +178,13 @@ PyObject* py_linear(PyObject*, PyObject* const* o, Py_ssize_t count) {
         c.mat(&w, "w", a.n, a.k, c.type, a.w, a.ldw);
         c.vec(tensor(o[3], "bias"), "bias", a.n, c.type, a.bias);
         c.mat(tensor(o[4], "residual"), "residual", a.m, a.n, c.type, a.residual, a.ldr);
-        c.mat(&needed(o[5], "out"), "out", a.m, a.n, c.type, a.y, a.ldy);
-        c.mat(tensor(o[6], "pre"), "pre", a.m, a.n, c.type, a.pre, a.ldpre);
+        const at::Tensor *y = &needed(o[5], "out"), *pre = tensor(o[6], "pre");
+        c.mat(y, "out", a.m, a.n, c.type, a.y, a.ldy);
+        c.mat(pre, "pre", a.m, a.n, c.type, a.pre, a.ldpre);
         void* ws;
         size_t bytes;
         c.space(tensor(o[7], "workspace"), ws, bytes);
-        return dgc_linear(&a, ws, bytes, stream_of(o[8]));
+        return done(dgc_linear(&a, ws, bytes, stream_of(o[8])), {y, pre});
     });
 }
 
@@ -170,7 +192,8 @@ PyObject* py_linear(PyObject*, PyObject* const* o, Py_ssize_t count) {
 PyObject* py_linear_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
     return guarded(count, 10, [&] {
         const at::Tensor &x = needed(o[2], "x"), &w = needed(o[3], "w");
-        const at::Tensor *pre = tensor(o[4], "pre"), *dw = tensor(o[6], "dw"), *db = tensor(o[7], "dbias");
+        const at::Tensor *pre = tensor(o[4], "pre"), *dx = tensor(o[5], "dx"), *dw = tensor(o[6], "dw");
+        const at::Tensor* db = tensor(o[7], "dbias");
         const Call c("linear_backward", x);
         const at::ScalarType g = c.gradients(dw, db);
         dgc_linear_backward_args a{};
@@ -183,13 +206,13 @@ PyObject* py_linear_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
         c.mat(&x, "x", a.m, a.k, c.type, a.x, a.ldx);
         c.mat(&w, "w", a.n, a.k, c.type, a.w, a.ldw);
         c.mat(pre, "pre", a.m, a.n, c.type, a.pre, a.ldpre);
-        c.mat(tensor(o[5], "dx"), "dx", a.m, a.k, c.type, a.dx, a.lddx);
+        c.mat(dx, "dx", a.m, a.k, c.type, a.dx, a.lddx);
         c.mat(dw, "dw", a.n, a.k, g, a.dw, a.lddw);
         c.vec(db, "dbias", a.n, g, a.dbias);
         void* ws;
         size_t bytes;
         c.space(tensor(o[8], "workspace"), ws, bytes);
-        return dgc_linear_backward(&a, ws, bytes, stream_of(o[9]));
+        return done(dgc_linear_backward(&a, ws, bytes, stream_of(o[9])), {dx, dw, db});
     });
 }
 
@@ -205,13 +228,14 @@ PyObject* py_gated_ffn(PyObject*, PyObject* const* o, Py_ssize_t count) {
         c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
         c.mat(&w, "w_gate", a.f, a.d, c.type, a.w_gate, a.ldw_gate);
         c.mat(&needed(o[3], "w_up"), "w_up", a.f, a.d, c.type, a.w_up, a.ldw_up);
-        c.mat(&needed(o[4], "out"), "out", a.m, a.f, c.type, a.h, a.ldh);
-        c.mat(tensor(o[5], "gate"), "gate", a.m, a.f, c.type, a.gate, a.ldgate);
-        c.mat(tensor(o[6], "up"), "up", a.m, a.f, c.type, a.up, a.ldup);
+        const at::Tensor *h = &needed(o[4], "out"), *gate = tensor(o[5], "gate"), *up = tensor(o[6], "up");
+        c.mat(h, "out", a.m, a.f, c.type, a.h, a.ldh);
+        c.mat(gate, "gate", a.m, a.f, c.type, a.gate, a.ldgate);
+        c.mat(up, "up", a.m, a.f, c.type, a.up, a.ldup);
         void* ws;
         size_t bytes;
         c.space(tensor(o[7], "workspace"), ws, bytes);
-        return dgc_gated_ffn(&a, ws, bytes, stream_of(o[8]));
+        return done(dgc_gated_ffn(&a, ws, bytes, stream_of(o[8])), {h, gate, up});
     });
 }
 
@@ -219,7 +243,7 @@ PyObject* py_gated_ffn(PyObject*, PyObject* const* o, Py_ssize_t count) {
 PyObject* py_gated_ffn_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
     return guarded(count, 12, [&] {
         const at::Tensor &x = needed(o[2], "x"), &w = needed(o[3], "w_gate");
-        const at::Tensor *dg = tensor(o[8], "dw_gate"), *du = tensor(o[9], "dw_up");
+        const at::Tensor *dx = tensor(o[7], "dx"), *dg = tensor(o[8], "dw_gate"), *du = tensor(o[9], "dw_up");
         const Call c("gated_ffn_backward", x);
         if (!dg != !du) refuse("gated_ffn_backward: dw_gate and dw_up come together");
         const at::ScalarType g = c.gradients(dg, nullptr);
@@ -234,15 +258,30 @@ PyObject* py_gated_ffn_backward(PyObject*, PyObject* const* o, Py_ssize_t count)
         c.mat(&needed(o[4], "w_up"), "w_up", a.f, a.d, c.type, a.w_up, a.ldw_up);
         c.mat(&needed(o[5], "gate"), "gate", a.m, a.f, c.type, a.gate, a.ldgate);
         c.mat(&needed(o[6], "up"), "up", a.m, a.f, c.type, a.up, a.ldup);
-        c.mat(tensor(o[7], "dx"), "dx", a.m, a.d, c.type, a.dx, a.lddx);
+        c.mat(dx, "dx", a.m, a.d, c.type, a.dx, a.lddx);
         c.mat(dg, "dw_gate", a.f, a.d, g, a.dw_gate, a.lddw_gate);
         c.mat(du, "dw_up", a.f, a.d, g, a.dw_up, a.lddw_up);
         void* ws;
         size_t bytes;
         c.space(tensor(o[10], "workspace"), ws, bytes);
-        return dgc_gated_ffn_backward(&a, ws, bytes, stream_of(o[11]));
+        return done(dgc_gated_ffn_backward(&a, ws, bytes, stream_of(o[11])), {dx, dg, du});
     });
 }
+
+// A sequence of tensors, kept until the call that takes their addresses has returned.
+struct Tensors {
+    PyObject* fast = nullptr;
+    std::vector<void*> data;
+
+    Tensors() = default;
+    Tensors(const Tensors&) = delete;
+    ~Tensors() { Py_XDECREF(fast); }
+
+    void wrote_all() const {
+        for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(fast); ++i)
+            wrote({&THPVariable_Unpack(PySequence_Fast_GET_ITEM(fast, i))});
+    }
+};
 
 // A set's layout as the binding holds it: element counts and types, in bytes
 // objects of int64 and int32.
@@ -260,32 +299,27 @@ struct Layout {
         types = reinterpret_cast<const int32_t*>(PyBytes_AS_STRING(t));
     }
 
-    std::vector<void*> pointers(PyObject* seq, const char* what) const {
-        PyObject* fast = PySequence_Fast(seq, "expected a sequence of tensors");
-        if (!fast) {
+    // out: what the call writes and does not read.  (Whether it requires a gradient is not looked up: of 161 views
+    // that takes 6 us before the first launch, and that they were written is noted behind the last one.)
+    void read(PyObject* seq, const char* what, Tensors& to, bool out = false) const {
+        to.fast = PySequence_Fast(seq, "expected a sequence of tensors");
+        if (!to.fast) {
             PyErr_Clear();
             refuse(std::string(what) + ": expected a sequence of tensors");
         }
-        std::vector<void*> p;
-        try {
-            if (PySequence_Fast_GET_SIZE(fast) != count)
-                refuse(std::string(what) + ": expected " + std::to_string(count) + " tensors");
-            p.reserve(size_t(count));
-            for (Py_ssize_t i = 0; i < count; ++i) {
-                const at::Tensor& t = needed(PySequence_Fast_GET_ITEM(fast, i), what);
-                if (t.numel() != sizes[i] || type_code(t.scalar_type()) != types[i])
-                    refuse(std::string(what) + ": tensor " + std::to_string(i) +
-                           " differs from the set's shapes or dtypes");
-                if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous())
-                    refuse(std::string(what) + ": expected contiguous tensors on the set's device");
-                p.push_back(t.data_ptr());
-            }
-        } catch (...) {
-            Py_DECREF(fast);
-            throw;
+        if (PySequence_Fast_GET_SIZE(to.fast) != count)
+            refuse(std::string(what) + ": expected " + std::to_string(count) + " tensors");
+        to.data.reserve(size_t(count));
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            PyObject* const item = PySequence_Fast_GET_ITEM(to.fast, i);
+            const at::Tensor& t = out ? unpacked(item, what) : needed(item, what);
+            if (t.numel() != sizes[i] || type_code(t.scalar_type()) != types[i])
+                refuse(std::string(what) + ": tensor " + std::to_string(i) +
+                       " differs from the set's shapes or dtypes");
+            if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous())
+                refuse(std::string(what) + ": expected contiguous tensors on the set's device");
+            to.data.push_back(t.data_ptr());
         }
-        Py_DECREF(fast);
-        return p;
     }
 };
 
@@ -302,10 +336,13 @@ double number(PyObject* o, const char* name) {
 PyObject* py_set_norm(PyObject*, PyObject* const* o, Py_ssize_t count) {
     return guarded(count, 9, [&] {
         const Layout l(o[1], o[2], o[3]);
-        const std::vector<void*> g = l.pointers(o[4], "grads");
-        return dgc_gradset_norm(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data(),
-                                int32_t(integer(o[5])), number(o[6], "unscale"),
-                                static_cast<double*>(needed(o[7], "total").data_ptr()), stream_of(o[8]));
+        Tensors g;
+        l.read(o[4], "grads", g);
+        const at::Tensor& total = needed(o[7], "total");
+        return done(dgc_gradset_norm(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data.data(),
+                                     int32_t(integer(o[5])), number(o[6], "unscale"),
+                                     static_cast<double*>(total.data_ptr()), stream_of(o[8])),
+                    {&total});
     });
 }
 
@@ -313,14 +350,18 @@ PyObject* py_set_norm(PyObject*, PyObject* const* o, Py_ssize_t count) {
 PyObject* py_set_clip(PyObject*, PyObject* const* o, Py_ssize_t count) {
     return guarded(count, 12, [&] {
         const Layout l(o[1], o[2], o[3]);
-        const std::vector<void*> g = l.pointers(o[4], "grads");
-        std::vector<void*> out;
-        if (o[5] != Py_None) out = l.pointers(o[5], "out");
-        return dgc_gradset_clip(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data(),
-                                o[5] == Py_None ? g.data() : out.data(), number(o[6], "clip"),
-                                int32_t(integer(o[7])), number(o[8], "unscale"),
-                                static_cast<double*>(needed(o[9], "total").data_ptr()),
-                                static_cast<float*>(needed(o[10], "scale").data_ptr()), stream_of(o[11]));
+        Tensors g, other;
+        l.read(o[4], "grads", g);
+        if (o[5] != Py_None) l.read(o[5], "out", other, true);
+        const Tensors& out = o[5] == Py_None ? g : other;
+        const at::Tensor &total = needed(o[9], "total"), &scale = needed(o[10], "scale");
+        const int rc = dgc_gradset_clip(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data.data(),
+                                        out.data.data(), number(o[6], "clip"),
+                                        int32_t(integer(o[7])), number(o[8], "unscale"),
+                                        static_cast<double*>(total.data_ptr()),
+                                        static_cast<float*>(scale.data_ptr()), stream_of(o[11]));
+        if (rc == DGC_OK) out.wrote_all();
+        return done(rc, {&total, &scale});
     });
 }
 
@@ -328,7 +369,8 @@ PyObject* py_set_clip(PyObject*, PyObject* const* o, Py_ssize_t count) {
 PyObject* py_set_pack(PyObject*, PyObject* const* o, Py_ssize_t count) {
     return guarded(count, 12, [&] {
         const Layout l(o[1], o[2], o[3]);
-        const std::vector<void*> g = l.pointers(o[4], "grads");
+        Tensors g;
+        l.read(o[4], "grads", g);
         const at::Tensor& flat = needed(o[5], "flat");
         int64_t n = 0;
         for (Py_ssize_t i = 0; i < l.count; ++i) n += l.sizes[i];
@@ -336,10 +378,13 @@ PyObject* py_set_pack(PyObject*, PyObject* const* o, Py_ssize_t count) {
             flat.get_device() != l.device || !flat.is_contiguous())
             refuse("flat: expected at least " + std::to_string(n) +
                    " contiguous float32 elements on the set's device");
-        return dgc_gradset_pack(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data(),
-                                static_cast<float*>(flat.data_ptr()), number(o[6], "clip"), int32_t(integer(o[7])),
-                                number(o[8], "unscale"), static_cast<double*>(needed(o[9], "total").data_ptr()),
-                                static_cast<float*>(needed(o[10], "scale").data_ptr()), stream_of(o[11]));
+        const at::Tensor &total = needed(o[9], "total"), &scale = needed(o[10], "scale");
+        return done(dgc_gradset_pack(reinterpret_cast<dgc_gradset*>(uintptr_t(integer(o[0]))), g.data.data(),
+                                     static_cast<float*>(flat.data_ptr()), number(o[6], "clip"),
+                                     int32_t(integer(o[7])), number(o[8], "unscale"),
+                                     static_cast<double*>(total.data_ptr()), static_cast<float*>(scale.data_ptr()),
+                                     stream_of(o[11])),
+                    {&flat, &total, &scale});
     });
 }
 

@@ -656,6 +656,7 @@ def gated_ffn_workspace(m: int, d: int, f: int, backward: bool = False, device="
 def linear(x, w, bias=None, residual=None, act: str = "none", out=None, pre=None, workspace=None, stream=None):
     """act(x w^T + bias) + residual for x [m, k] and w [n, k] (bfloat16 or float16, contiguous columns).
 
+    No call here records a gradient: tensors that require one are refused outside of torch.no_grad().
     `out` and `pre` are written if given; `pre` receives x w^T + bias for linear_backward.  `out` may be
     `residual`.  `workspace` is what linear_workspace(m, n, k) gives; without one the call allocates it."""
     if out is None:
