@@ -212,14 +212,7 @@ __device__ __forceinline__ void finish_row(const Finish& f, int z, int64_t m, in
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = act_value(f.act, v[i]) * v2[i];
         store_row<T, C>(static_cast<T*>(f.out[0]) + m * f.ldo + n, valid, v);
-        return;
-    }
-    if (f.unscale) {
-        const float u = *f.unscale;
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] *= u;
-    }
-    if (f.wide) {
+    } else if (f.wide) {
         store_wide<C>(static_cast<float*>(f.out[z]) + m * (z ? f.ldo2 : f.ldo) + n, valid, v);
     } else {
         if (f.bias) {
@@ -443,6 +436,8 @@ __device__ __forceinline__ void put_rows(const TileArgs& A, int split, int z, in
     if (!PAIR && f.bias) load_row<T, 8>(static_cast<const T*>(f.bias) + n, valid, bias);
     const int rows = A.M - m0 < ROWS ? int(A.M - m0) : ROWS;
     const int fold = FORM == kDx ? A.fold : 0;
+    constexpr bool BACK = FORM == kDx || FORM == kDw;
+    const float unscale = BACK && f.unscale ? *f.unscale : 1.0f;
     const auto sum = [&](int r, int col4) {
         const float* p = at(r) + out_at(r, col4);
         f32x4 t = *reinterpret_cast<const f32x4*>(p);
@@ -480,6 +475,10 @@ __device__ __forceinline__ void put_rows(const TileArgs& A, int split, int z, in
                 store_wide<8>(o, valid, v);
                 if (PAIR) store_wide<8>(o + A.M * A.N, valid, v2);
             } else {
+                if (BACK) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] *= unscale;
+                }
                 finish_row<T, PAIR, 8>(f, z, m, n, valid, v, v2, bias, residual[u]);
             }
         }
@@ -534,6 +533,10 @@ __global__ __launch_bounds__(64) void k_join(TileArgs A) {
                 v2[e] += t[s][P - 1][e];
             }
         }
+    }
+    if (!PAIR && A.fin.unscale) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= *A.fin.unscale;
     }
     finish_one<T, PAIR, 4>(A.fin, z, m, n, A.N, v, v2);
 }
