@@ -63,6 +63,29 @@ double rounds_us(const Cost& c, int64_t blocks, double steps) {
 // A second launch that adds the splits' sums, and its traffic.
 double join_us(double bytes) { return kLaunchUs + bytes / 5e6; }
 
+// Up to 32 rows, kThin and the tiles.  kThin's waves read every row of x for
+// their 16 columns; a tile of 32 or 64 rows reads x once for 64 columns, and
+// the weight no faster than the memory gives it.  Microseconds per call, in a
+// row of calls on six sets of inputs:
+//                            kThin  kMid32  kMid32 in 4
+//   4 x 4096, k 4096          10.0    11.6    12.1
+//   32 x 704, k 704            5.0     6.0     8.6
+//   16 x 1024, k 4096         10.4    11.6    10.1
+//   32 x 4096, k 4096         14.0    12.6    12.6
+//   32 x 512, k 8192          24.1    19.1    11.8
+//   16 x 8192, k 2048         11.3     9.4    15.0
+//   32 x 16384, k 4096        54.7    32.3    40.2
+// The tiles are taken where they are expected to need 15% less, which of 90
+// products measured so is never the slower choice.
+constexpr int64_t kFewRows = 32;
+constexpr double kTilesGain = 0.85, kWeightRate = 5e6;  // bytes per microsecond
+
+double thin_us(int64_t m, int64_t n, int64_t k, int products) {
+    const double rounds = double(cdiv64(cdiv64(n, 16), 256)), steps = double(k) / 512;
+    const double us = rounds * (3.3 + steps * (0.52 * products + 0.0245 * double(m)));
+    return std::max(us, 3.3 + 2.0 * double(n) * double(k) * products / kWeightRate);
+}
+
 }  // namespace
 
 bool direct(const Product& p) {
@@ -84,14 +107,13 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
     const int64_t wide = form == kPair ? 2 * n : n;
     Cut best;
     best.us = 1e30;
-    // few rows: reading the weight is all there is to it (1 x 4096, k 4096:
-    // kThin 7.2, kMid32 10.7 us; 30 x 704, k 704: 4.2 and 5.7; 30 x 4096, k 4096:
-    // 13.0 and 12.2; 60 x 4096, k 4096: 20.8 and 12.2)
-    if ((form == kRows || form == kPair) && m <= 32) {
+    const bool few = (form == kRows || form == kPair) && m <= kFewRows;
+    const double weight_us = few ? 2.0 * double(wide) * double(k) / kWeightRate : 0.0;
+    if (few) {
         best.tile = kThin;
         best.per = steps;
-        best.us = 0;
-        return best;
+        best.us = kTilesGain * thin_us(m, n, k, form == kPair ? 2 : 1);
+        if (!direct) return best;  // no tile reads rows off 16 bytes as fast
     }
     for (const Cost& c : kCosts) {
         if ((c.tile == kGuarded) == direct) continue;
@@ -103,8 +125,10 @@ Cut plan_product(int form, int64_t m, int64_t n, int64_t k, int parts, bool dire
             if (splits > 1 && (steps < 8 * splits || tiles * splits > c.round)) break;
             const int64_t per = cdiv64(steps, splits), work = tiles * splits;
             double us = rounds_us(c, work, double(per));
+            if (few) us = std::max(us, c.start + weight_us);
             if (splits > 1)
-                us += join_us(8.0 * double(splits) * double(m) * double(wide) * double(outs));
+                us += join_us(8.0 * double(splits) * double(m) * double(wide) * double(outs)) +
+                      (few ? 1.0 : 0.0);  // measured where nothing hides it
             if (us < best.us) {
                 best.tile = c.tile;
                 best.per = per;

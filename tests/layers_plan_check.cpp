@@ -103,7 +103,28 @@ void gated(int64_t m, int64_t d, int64_t f, int64_t ld_g, int64_t ld_u, int off_
 
 }  // namespace
 
+// Few rows: kThin where it is measured to be faster, tiles where they are.
+void few_rows() {
+    struct Case {
+        int form;
+        int64_t m, n, k;
+        bool thin;
+    };
+    for (const Case& c : {Case{kRows, 1, 4096, 4096, true}, Case{kPair, 3, 8192, 2048, true},
+                          Case{kRows, 32, 704, 704, true}, Case{kRows, 16, 4096, 1024, true},
+                          Case{kRows, 32, 4096, 1024, true}, Case{kRows, 16, 1000, 2048, true},
+                          Case{kPair, 4, 16384, 4096, true}, Case{kRows, 4, 4096, 8192, true},
+                          Case{kRows, 32, 512, 8192, false}, Case{kPair, 4, 512, 8192, false},
+                          Case{kRows, 32, 16384, 4096, false}, Case{kRows, 17, 8192, 2048, false},
+                          Case{kPair, 32, 1024, 4096, false}, Case{kRows, 24, 1024, 4096, false}}) {
+        const Cut cut = plan_product(c.form, c.m, c.n, c.k, 1, true);
+        CHECK((cut.tile == kThin) == c.thin && cut.us > 0);
+        CHECK(plan_product(c.form, c.m, c.n, c.k, 1, false).tile == kThin);
+    }
+}
+
 int main() {
+    few_rows();
     const int64_t m = 2048, d = 1024, f = 4096;
     gated(m, d, f, d, d, 0, 0, 0);
     gated(m, d, f, d + 64, d + 64, 0, 0, 0);
