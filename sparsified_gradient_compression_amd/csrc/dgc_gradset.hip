@@ -436,7 +436,8 @@ int scale_pass(const dgc_gradset* s, const void* const* grads, void* const* outs
         k.unscale <= 0.0 || std::isnan(k.clip) || !pointers_ok(s, grads) ||
         !aligned(k.out_norm, 8) || !aligned(k.out_scale, 4))
         return DGC_EINVAL;
-    if (FLAT ? !k.flat || !aligned(k.flat, 4) : !pointers_ok(s, outs)) return DGC_EINVAL;
+    if (FLAT ? (!k.flat && s->elements > 0) || !aligned(k.flat, 4) : !pointers_ok(s, outs))
+        return DGC_EINVAL;
     const int rc = norm_pass(s, grads, outs, k.most, stream);
     if (rc != DGC_OK) return rc;
     Scaling l = k;
