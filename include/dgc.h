@@ -602,8 +602,8 @@ typedef struct dgc_linear_args {
  * are of grad_type: `type`, or DGC_FP32 (a learner's flat gradient).  pre is
  * not read for DGC_ACT_NONE; for other activations the products take dz as the
  * sum of two numbers of `type` (off by 2^-16 of it for DGC_BF16, 2^-22 for
- * DGC_FP16), dw of DGC_BF16 in binary32 as the sum of three (2^-24), and with
- * DGC_DZ_ROUNDED as one (up to 32 rows: two); the column sums take dz itself.  DGC_FP16: times a power of two that brings the
+ * DGC_FP16), dw of DGC_BF16 in binary32 as the sum of three (2^-24; dx then of
+ * the first two of them, 2^-15), and with DGC_DZ_ROUNDED as one (up to 32 rows: two); the column sums take dz itself.  DGC_FP16: times a power of two that brings the
  * call's largest finite |dz| into [2^14, 2^15), undone afterwards, so that dz
  * may leave the range of `type` and a small one loses at most 2^-39 of the
  * largest (in two numbers: 2^-37). */

@@ -27,9 +27,9 @@ def gpu():
 def held(dz, e, dtype, pieces, most):
     """The error of dz, e before, as a sum of `pieces` numbers of dtype.  Each but the last leaves at most a step
     (2^-7, 2^-10 of the number), the last at most half a step of what is left: 2^-8 and 2^-16 and 2^-24 (bf16), 2^-11
-    and 2^-22 (fp16).  fp16 is scaled: its least number is 2^-24 / 2^14 of the largest |dz|, and two of them may be
+    and 2^-22 (fp16); the first two of three leave a whole step, 2^-15.  fp16 is scaled: its least number is 2^-24 / 2^14 of the largest |dz|, and two of them may be
     lost (one number: half of one)."""
-    bits = {BF16: {1: 8, 2: 16, 3: 24}, FP16: {1: 11, 2: 22}}[dtype][pieces]
+    bits = {BF16: {1: 8, 2: 16, 3: 24, "2 of 3": 15}, FP16: {1: 11, 2: 22}}[dtype][pieces]
     low = 0.0 if dtype == BF16 else most * (2.0 ** -39 if pieces == 1 else 2.0 ** -37)
     return e + 2.0 ** -bits * (dz.abs() + e) + low
 
@@ -38,7 +38,7 @@ def pieces_of(dtype, wide, rounded, m):
     """(in dx, in dw)"""
     if rounded:
         return (2, 2) if m <= 32 else (1, 1)
-    return 2, 3 if wide and dtype == BF16 else 2
+    return ("2 of 3", 3) if wide and dtype == BF16 else (2, 2)
 
 
 def linear(m, n, k, dtype, act, wide, rounded=False, pad=0, shift=0):
@@ -53,7 +53,7 @@ def linear(m, n, k, dtype, act, wide, rounded=False, pad=0, shift=0):
     dz, e, _ = R.slope(dy.double(), pre.double(), act, dtype)
     most = float(dz.abs().max())
     px, pw = pieces_of(dtype, wide, rounded, m)
-    R.check("dx", dx, *R.product(dz, w.double(), held(dz, e, dtype, px, most), px * n), dtype)
+    R.check("dx", dx, *R.product(dz, w.double(), held(dz, e, dtype, px, most), 2 * n), dtype)
     R.check("dw", dw, *R.product(dz.t(), x.double(), held(dz, e, dtype, pw, most).t(), pw * m), g)
     mk.untouched()
 
@@ -76,8 +76,8 @@ def gated(m, d, f, dtype, act, wide, rounded=False, pad=0, shift=0):
     eb = h.abs() * R.act_error(a, 0.0) + 2.0 ** -23 * db.abs()
     most = max(float(da.abs().max()), float(db.abs().max()))
     px, pw = pieces_of(dtype, wide, rounded, m)
-    pa, qa = R.product(da, wg.double(), held(da, ea, dtype, px, most), 2 * px * f)
-    pb, qb = R.product(db, wu.double(), held(db, eb, dtype, px, most), 2 * px * f)
+    pa, qa = R.product(da, wg.double(), held(da, ea, dtype, px, most), 4 * f)
+    pb, qb = R.product(db, wu.double(), held(db, eb, dtype, px, most), 4 * f)
     R.check("dx", dx, pa + pb, qa + qb, dtype)
     R.check("dw_gate", dwg, *R.product(da.t(), x.double(), held(da, ea, dtype, pw, most).t(), pw * m), g)
     R.check("dw_up", dwu, *R.product(db.t(), x.double(), held(db, eb, dtype, pw, most).t(), pw * m), g)

@@ -91,6 +91,32 @@ def test_an_infinite_gradient_does_not_set_the_scale():
     assert torch.equal(dx[rows], dx1[rows]) and bool(torch.isnan(dx1[9]).all()) and not bool(torch.isfinite(dx1[7]).any())
 
 
+def test_the_scale_is_found_anew_in_every_replay():
+    """A captured call on gradients 2^20 times larger and smaller than those it was captured with."""
+    m, d, f = 130, 72, 136
+    x, dh, gate, up = (normal(i, *s).to(FP16) for i, s in enumerate(((m, d), (m, f), (m, f), (m, f))))
+    wg, wu = ((normal(i, f, d) * 2.0 ** -10).to(FP16) for i in (5, 6))
+    outs = torch.empty_like(x), torch.empty(f, d, device="cuda"), torch.empty(f, d, device="cuda")
+    ws = dgc.gated_ffn_workspace(m, d, f, backward=True)
+
+    def step():
+        dgc.gated_ffn_backward(dh, x, wg, wu, gate, up, dx=outs[0], dw_gate=outs[1], dw_up=outs[2], workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i, scale in enumerate((20000.0, 2.0 ** -18, 1.0, 20000.0)):
+        dh.copy_((normal(10 + i, m, f) * scale).clamp(-65504, 65504))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and bool(torch.isfinite(a).all()) for a, b in zip(got, outs)), i
+
+
 def test_gradients_of_zero_stay_zero():
     m, n, k = 40, 64, 40
     dy, x, pre, w = torch.zeros(m, n, dtype=FP16, device="cuda"), *(normal(i, *s).to(FP16) for i, s in enumerate(((m, k), (m, n), (n, k))))
