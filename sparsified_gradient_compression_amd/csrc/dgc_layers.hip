@@ -172,8 +172,9 @@ double queue_us(int64_t slots, int64_t nx, double ux, int64_t nw, double uw) {
 }
 
 // Both gradients in one launch, dx's workgroups first: sx and sw steps each.
-// Gates' gradients (1531 x 3840 x 1280, 120 and 300 tiles of 128; expected and
-// measured): kMid128 48.6 and 48.2, kPair128 46.5 and 46.7.
+// Gates' gradients (1531 x 3840 x 1280, 120 and 300 tiles of 128, dz in one piece;
+// expected, and measured as what the call takes more than its slopes): kMid128
+// 48.6 and 48.2, kPair128 46.5 and 46.7 (traced: 51).
 double both_us(const Cost& c, int64_t nx, double sx, int64_t nw, double sw) {
     if (nx + nw <= c.light) return c.light_start + c.light_step * std::max(sx, sw);
     if (nx + nw <= c.round) {  // all at once, and then the longer ones alone

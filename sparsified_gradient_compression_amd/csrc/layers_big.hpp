@@ -19,10 +19,12 @@
 // the waiting there is.  Half phases of 16 matrix instructions leave the reads
 // less time than they take (8192 x 8192 x 4096: 394 us, not 380).
 //
-// 8192^3 with bias and residual: 783 us, 1403 TFLOP/s; a gated block's forward
-// pass, 8192 x 4096 x 12288: 1210 us, 1363; its dx 1177 us, 1401, and dw (both
-// operands turned on the way) 1318 us, 1252.  Bound by the matrix units but
-// for 11 us per round of workgroups, while the outputs leave.
+// 8192^3 with bias and residual: 766-824 us from card to card, 1334-1435
+// TFLOP/s; a gated block's forward pass, 8192 x 4096 x 12288: 1226-1249 us,
+// 1320-1345; its dx, da and db in one piece, 1177 us, 1401, and dw (both operands
+// turned on the way) 1318 us, 1252, in two pieces 2600-2700 and 2560-2670.  Bound
+// by the matrix units but for 11 us per round of workgroups, while the outputs
+// leave.
 #pragma once
 
 #include "layers_direct.hpp"

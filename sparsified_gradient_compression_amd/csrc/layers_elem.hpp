@@ -21,8 +21,9 @@
 // of 333 rows, 1152 x 3456.
 //
 // All passes are bound by memory.  A gated block's slopes of 8192 x 12288: 155
-// us, 6.5 TB/s; a layer's of 1531 x 3840 with its column sums: 14 us, one round
-// of workgroups, most of it the way to memory and back.
+// us, 6.5 TB/s, and 259, 5.4 TB/s, in two pieces; a layer's of 1531 x 3840 with
+// its column sums: 13 and 20 us, one round of workgroups, most of it the way to
+// memory and back.
 #pragma once
 
 #include "layers_tile.hpp"

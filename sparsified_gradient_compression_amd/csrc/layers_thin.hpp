@@ -7,8 +7,8 @@
 // matrix instruction takes them from, four steps of 64 ahead, and x from the
 // caches.  The waves' sums meet in LDS and are finished there, so nothing
 // passes through memory and there is one launch.  Any strides and alignment.
-// 1 x 4096, k 4096: 8.2 us of the kernel, 4.1 TB/s; 3 x 8192, k 2048, both
-// weights of a gated block: 12.6 us, 5.3 TB/s.
+// 1 x 4096, k 4096: 8.2 us of the kernel (traced: 7.9 to 8.8), 4.1 TB/s; 3 x
+// 8192, k 2048, both weights of a gated block: 12.6 us, 5.3 TB/s.
 #pragma once
 
 #include "layers_tile.hpp"
