@@ -251,15 +251,16 @@ size_t part_bytes(int form, int64_t m, int64_t n, int64_t k, int parts, int fold
                   int most_pieces = 1) {
     const int64_t planes = form == kPair ? 2 : form == kDw ? parts : 1;
     size_t most = 0;
+    const auto form_of = [&](bool d, int fo, int pieces) {
+        const Cut c = plan_product(form, m, n, k, parts, d, fo, pieces);
+        if (c.splits > 1)
+            most = std::max(most,
+                            size_t(c.splits) * size_t(planes) * size_t(m) * size_t(n) * 4);
+    };
     for (const bool d : {false, true}) {
-        for (const int fo : {0, fold}) {  // 0 too: without an activation
-            for (int pieces = 1; pieces <= most_pieces; ++pieces) {
-                const Cut c = plan_product(form, m, n, k, parts, d, fo, pieces);
-                if (c.splits > 1)
-                    most = std::max(most, size_t(c.splits) * size_t(planes) * size_t(m) *
-                                              size_t(n) * 4);
-            }
-        }
+        // folded dz is one piece as far as its steps go; none is folded without an activation
+        if (fold) form_of(d, fold, 1);
+        for (int pieces = 1; pieces <= most_pieces; ++pieces) form_of(d, 0, pieces);
     }
     return round_up(most);
 }

@@ -2,8 +2,10 @@
 // launchers, which are replaced here: nothing runs on a GPU, and the addresses
 // are never followed.  Built with dgc_layers.hip and run by
 // tests/test_layers_plan.py.
+#include <algorithm>
 #include <cstdio>
 #include <cstdlib>
+#include <random>
 #include <vector>
 
 #include "layers.hpp"
@@ -22,9 +24,27 @@ namespace layers {
 std::vector<Product> products;
 std::vector<int> tiles;
 std::vector<Repack> repacks;
+uintptr_t space_begin = 0, space_end = 0;  // the call's workspace, where it is checked
+std::vector<std::pair<uintptr_t, uintptr_t>> used;
+
+// A range of the workspace that a launch uses; none overlap.
+void uses(const void* p, int64_t bytes) {
+    if (space_end == 0 || bytes == 0) return;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = a + uintptr_t(bytes);
+    CHECK(a >= space_begin && b <= space_end);
+    for (const auto& r : used) CHECK(b <= r.first || a >= r.second);
+    used.push_back({a, b});
+}
 
 template <class T>
-int Launch<T>::product(const Product& p, const Cut& c, void*, hipStream_t) {
+int Launch<T>::product(const Product& p, const Cut& c, void* ws, hipStream_t) {
+    if (c.splits > 1) {
+        const int64_t planes = p.form == kPair ? 2 : p.form == kDw ? p.parts : 1;
+        const auto before = used;  // the next product's sums may lie there again
+        uses(ws, 4 * c.splits * planes * p.m * p.n);
+        used = before;
+    }
+    CHECK(c.splits * c.per * 64 >= p.k * p.pieces * (p.form == kDx ? p.parts : 1));
     products.push_back(p);
     tiles.push_back(c.tile);
     return DGC_OK;
@@ -39,7 +59,20 @@ int Launch<T>::both(const Product& dx, const Product& dw, int tile, const Sums&,
 }
 
 template <class T>
-int Launch<T>::prepare(SlopeArgs, const Repack& r, hipStream_t) {
+int Launch<T>::prepare(SlopeArgs a, const Repack& r, hipStream_t) {
+    if (a.M > 0 && a.N > 0) {
+        const int64_t piece = a.M * a.ldz;
+        CHECK(a.pieces >= 1 && a.pieces <= 3 && (a.pieces == 1 || a.low == piece));
+        if (a.dz) uses(a.dz, 2 * a.pieces * piece);
+        if (a.dz2) uses(a.dz2, 2 * a.pieces * piece);
+        if (a.part) uses(a.part, 4 * cdiv64(a.M, a.per) * a.N);
+        if (a.most) {
+            CHECK(sizeof(T) == 2 && (__is_same(T, _Float16)));
+            uses(a.most, 4 * kMostParts);
+            uses(a.unscale, 4);
+        }
+    }
+    for (int i = 0; i < r.count; ++i) uses(r.to[i], 2 * r.rows[i] * ((r.cols[i] + 7) / 8 * 8));
     repacks.push_back(r);
     return DGC_OK;
 }
@@ -123,8 +156,65 @@ void few_rows() {
     }
 }
 
+// Calls of any sizes, types and strides: whatever they launch stays in the
+// workspace that their sizes gave.
+void workspaces() {
+    std::mt19937 rng(5);
+    const auto pick = [&](int n) { return int(rng() % unsigned(n)); };
+    const auto size = [&] {
+        const int64_t v = int64_t(1) << pick(14);
+        return v + pick(int(v));
+    };
+    for (int round = 0; round < 20000; ++round) {
+        const int64_t m = pick(3) ? size() : 1 + pick(40), n = size(), k = size();
+        const int64_t type = pick(2) ? DGC_BF16 : DGC_FP16, act = pick(5);
+        const int64_t grad = pick(2) ? type : int64_t(DGC_FP32);
+        const int64_t flag = pick(3) ? 0 : DGC_DZ_ROUNDED;
+        const int back = flag ? DGC_BACKWARD_ROUNDED : 1;
+        const int64_t pad = pick(2) ? 0 : 1 + pick(16), pad2 = pick(2) ? pad : 8 * pick(3);
+        const int off = pick(2) ? 0 : 2 * pick(8);
+        const auto call = [&](size_t bytes, auto f) {
+            reset();
+            used.clear();
+            space_begin = reinterpret_cast<uintptr_t>(kSpace);
+            space_end = space_begin + bytes;
+            CHECK(f(bytes) == DGC_OK);
+            space_end = 0;
+        };
+        size_t bytes = 0;
+        CHECK(dgc_linear_workspace_bytes(m, n, k, 0, &bytes) == DGC_OK);
+        call(bytes, [&](size_t b) {
+            dgc_linear_args a{type, act, m, n, k, at(1, off), k + pad, at(2), k + pad2, at(3),
+                              at(4), n, out(5), n, out(6), n};
+            return dgc_linear(&a, kSpace, b, nullptr);
+        });
+        CHECK(dgc_linear_workspace_bytes(m, n, k, back, &bytes) == DGC_OK);
+        call(bytes, [&](size_t b) {
+            dgc_linear_backward_args a{type, grad, act | flag, m, n, k, at(7, off), n + pad, at(1), k + pad2,
+                                       at(2), k + pad, at(6), n, pick(4) ? out(8) : nullptr, k,
+                                       pick(4) ? out(9) : nullptr, k, pick(2) ? out(10) : nullptr};
+            return dgc_linear_backward(&a, kSpace, b, nullptr);
+        });
+        CHECK(dgc_gated_ffn_workspace_bytes(m, k, n, 0, &bytes) == DGC_OK);
+        call(bytes, [&](size_t b) {
+            dgc_gated_ffn_args a{type, act, m, k, n, at(1), k + pad2, at(2, off), k + pad, at(3), k + pad2,
+                                 out(4), n, out(5), n, out(6), n};
+            return dgc_gated_ffn(&a, kSpace, b, nullptr);
+        });
+        CHECK(dgc_gated_ffn_workspace_bytes(m, k, n, back, &bytes) == DGC_OK);
+        const bool dw = pick(4);
+        call(bytes, [&](size_t b) {
+            dgc_gated_ffn_backward_args a{type, grad, act | flag, m, k, n, at(7), n, at(1, off), k + pad, at(2),
+                                          k + pad2, at(3), k + pad, at(5), n + pad, at(6), n, pick(4) ? out(8) : nullptr,
+                                          k, dw ? out(9) : nullptr, k, dw ? out(10) : nullptr, k};
+            return dgc_gated_ffn_backward(&a, kSpace, b, nullptr);
+        });
+    }
+}
+
 int main() {
     few_rows();
+    workspaces();
     const int64_t m = 2048, d = 1024, f = 4096;
     gated(m, d, f, d, d, 0, 0, 0);
     gated(m, d, f, d + 64, d + 64, 0, 0, 0);
