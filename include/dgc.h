@@ -120,10 +120,13 @@ extern "C" {
 #define DGC_TIMER_DECODE 3    /* all of dgc_decode_accumulate, dgc_decode_sum
                                  or dgc_shared_sum */
 
-/* Element types of the layer and gradient-set operators. */
+/* Element types of the layer, token and gradient-set operators. */
 #define DGC_BF16 1
 #define DGC_FP16 2
 #define DGC_FP32 3
+/* Index types of the token operators. */
+#define DGC_INT32 4
+#define DGC_INT64 5
 
 /* Activations of the layer operators. */
 #define DGC_ACT_NONE 0
@@ -678,6 +681,63 @@ int dgc_gated_ffn(const dgc_gated_ffn_args* args, void* workspace, size_t worksp
                   hipStream_t stream);
 int dgc_gated_ffn_backward(const dgc_gated_ffn_backward_args* args, void* workspace,
                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Token operators: what stands around the layers
+ * ----------------------------------------------
+ * Matrices and vectors as above, of DGC_BF16, DGC_FP16 or DGC_FP32 (`type`);
+ * sums, statistics and states are held in binary32 or more, and outputs are
+ * rounded once.  Sizes may be 0 and go up to 2^31 - 1.  Outputs must not
+ * overlap inputs, except where an output is said to be one of them, with the
+ * same ld.  Workspaces and return codes as above; no call waits for the stream
+ * or allocates, so each can be captured.
+ */
+
+/* y = (x - mean) * rstd * weight + bias for each row of x[m][d], mean and
+ * variance over the row, rstd = 1 / sqrt(variance + eps).  weight and bias
+ * (vectors of weight_type: `type` or DGC_FP32), mean and rstd (binary32[m], for
+ * the backward pass) may be NULL; without columns they are not written.  y may be x.  Squares of differences are held in
+ * binary32: a row that deviates by 2^63 and more overflows. */
+typedef struct dgc_layer_norm_args {
+    int64_t type, weight_type, m, d;
+    double eps;
+    const void* x;
+    int64_t ldx;
+    const void* weight;
+    const void* bias;
+    void* y;
+    int64_t ldy;
+    float* mean;
+    float* rstd;
+} dgc_layer_norm_args;
+
+/* With n = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - mean over the row of g - n * mean over the row of g n) + residual
+ *   dweight = the column sums of dy n, dbias = the column sums of dy
+ * weight may be NULL (ones), residual (the gradient that goes past the norm) too,
+ * and each of dx, dweight, dbias.  dweight and dbias are of grad_type: `type`
+ * or DGC_FP32.  dx may be dy or residual. */
+typedef struct dgc_layer_norm_backward_args {
+    int64_t type, weight_type, grad_type, m, d;
+    const void* dy;
+    int64_t lddy;
+    const void* x;
+    int64_t ldx;
+    const float* mean;
+    const float* rstd;
+    const void* weight;
+    const void* residual;
+    int64_t ldr;
+    void* dx;
+    int64_t lddx;
+    void* dweight;
+    void* dbias;
+} dgc_layer_norm_backward_args;
+
+int dgc_layer_norm_workspace_bytes(int64_t m, int64_t d, int32_t backward, size_t* bytes);
+int dgc_layer_norm(const dgc_layer_norm_args* args, hipStream_t stream);
+int dgc_layer_norm_backward(const dgc_layer_norm_backward_args* args, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Gradient sets: from a model's tensors to a learner

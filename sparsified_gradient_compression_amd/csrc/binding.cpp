@@ -1,4 +1,4 @@
-// binding.cpp -- the checks and argument blocks of the layer and gradient-set
+// binding.cpp -- the checks and argument blocks of the layer, token and gradient-set
 // operators for torch tensors, as a CPython module over the C ABI.
 //
 // A call of the smallest sizes takes a few microseconds on the GPU, and a
@@ -70,9 +70,12 @@ struct Call {
     at::ScalarType type;
     int device;
 
-    Call(const char* name, const at::Tensor& x) : fn(name), type(x.scalar_type()), device(x.get_device()) {
-        if (type != at::kBFloat16 && type != at::kHalf)
-            refuse(std::string(fn) + ": expected bfloat16 or float16, got " + c10::toString(type));
+    // wide: binary32 too
+    Call(const char* name, const at::Tensor& x, bool wide = false)
+        : fn(name), type(x.scalar_type()), device(x.get_device()) {
+        if (type != at::kBFloat16 && type != at::kHalf && !(wide && type == at::kFloat))
+            refuse(std::string(fn) + ": expected bfloat16" + (wide ? ", float16 or float32" : " or float16") + ", got " +
+                   c10::toString(type));
     }
 
     void place(const at::Tensor& t, const char* name, at::ScalarType want) const {
@@ -95,7 +98,7 @@ struct Call {
         ld = rows > 1 ? t->stride(0) : cols;
         if ((t->stride(1) != 1 && cols > 1) || ld < cols)
             refuse(std::string(name) + ": columns must be contiguous and rows must not overlap");
-        p = t->data_ptr();
+        p = static_cast<P>(t->data_ptr());
     }
 
     template <class P>
@@ -105,7 +108,7 @@ struct Call {
         place(*t, name, want);
         if (t->dim() != 1 || t->size(0) != n || !t->is_contiguous())
             refuse(std::string(name) + ": expected " + std::to_string(n) + " contiguous elements");
-        p = t->data_ptr();
+        p = static_cast<P>(t->data_ptr());
     }
 
     // m, n, k of x [m, k] and w [n, k]
@@ -128,6 +131,21 @@ struct Call {
         p = bytes ? w->data_ptr() : nullptr;
     }
 
+    // The type of a gain and a bias: x's, or binary32.
+    at::ScalarType weights(const at::Tensor* a, const at::Tensor* b) const {
+        const at::ScalarType w = a ? a->scalar_type() : b ? b->scalar_type() : type;
+        if (w != type && w != at::kFloat)
+            refuse(std::string(fn) + ": weights are of x's type or float32, not " + c10::toString(w));
+        return w;
+    }
+
+    // The rows and columns of a matrix.
+    void sides(const at::Tensor& x, const char* name, int64_t& m, int64_t& d) const {
+        if (x.dim() != 2) refuse(std::string(name) + ": expected a matrix, got " + shape(x));
+        m = x.size(0);
+        d = x.size(1);
+    }
+
     // The type of weight gradients: x's, or binary32.
     at::ScalarType gradients(const at::Tensor* a, const at::Tensor* b) const {
         const at::ScalarType g = a ? a->scalar_type() : b ? b->scalar_type() : type;
@@ -142,6 +160,15 @@ int64_t integer(PyObject* o) {
     if (v == -1 && PyErr_Occurred()) {
         PyErr_Clear();
         refuse("expected an integer");
+    }
+    return v;
+}
+
+double number(PyObject* o, const char* name) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse(std::string(name) + ": expected a number");
     }
     return v;
 }
@@ -268,6 +295,58 @@ PyObject* py_gated_ffn_backward(PyObject*, PyObject* const* o, Py_ssize_t count)
     });
 }
 
+// layer_norm(x, weight, bias, eps, out, mean, rstd, stream)
+PyObject* py_layer_norm(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 8, [&] {
+        const at::Tensor& x = needed(o[0], "x");
+        const at::Tensor *w = tensor(o[1], "weight"), *b = tensor(o[2], "bias");
+        const Call c("layer_norm", x, true);
+        const at::ScalarType g = c.weights(w, b);
+        dgc_layer_norm_args a{};
+        a.type = type_code(c.type);
+        a.weight_type = type_code(g);
+        a.eps = number(o[3], "eps");
+        c.sides(x, "x", a.m, a.d);
+        c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
+        c.vec(w, "weight", a.d, g, a.weight);
+        c.vec(b, "bias", a.d, g, a.bias);
+        const at::Tensor *y = &needed(o[4], "out"), *mean = tensor(o[5], "mean"), *rstd = tensor(o[6], "rstd");
+        c.mat(y, "out", a.m, a.d, c.type, a.y, a.ldy);
+        c.vec(mean, "mean", a.m, at::kFloat, a.mean);
+        c.vec(rstd, "rstd", a.m, at::kFloat, a.rstd);
+        return done(dgc_layer_norm(&a, stream_of(o[7])), {y, mean, rstd});
+    });
+}
+
+// layer_norm_backward(dy, x, mean, rstd, weight, residual, dx, dweight, dbias, workspace, stream)
+PyObject* py_layer_norm_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 11, [&] {
+        const at::Tensor& x = needed(o[1], "x");
+        const at::Tensor *w = tensor(o[4], "weight"), *dx = tensor(o[6], "dx");
+        const at::Tensor *dw = tensor(o[7], "dweight"), *db = tensor(o[8], "dbias");
+        const Call c("layer_norm_backward", x, true);
+        const at::ScalarType wt = c.weights(w, nullptr), g = c.gradients(dw, db);
+        dgc_layer_norm_backward_args a{};
+        a.type = type_code(c.type);
+        a.weight_type = type_code(wt);
+        a.grad_type = type_code(g);
+        c.sides(x, "x", a.m, a.d);
+        c.mat(&needed(o[0], "dy"), "dy", a.m, a.d, c.type, a.dy, a.lddy);
+        c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
+        c.vec(&needed(o[2], "mean"), "mean", a.m, at::kFloat, a.mean);
+        c.vec(&needed(o[3], "rstd"), "rstd", a.m, at::kFloat, a.rstd);
+        c.vec(w, "weight", a.d, wt, a.weight);
+        c.mat(tensor(o[5], "residual"), "residual", a.m, a.d, c.type, a.residual, a.ldr);
+        c.mat(dx, "dx", a.m, a.d, c.type, a.dx, a.lddx);
+        c.vec(dw, "dweight", a.d, g, a.dweight);
+        c.vec(db, "dbias", a.d, g, a.dbias);
+        void* ws;
+        size_t bytes;
+        c.space(tensor(o[9], "workspace"), ws, bytes);
+        return done(dgc_layer_norm_backward(&a, ws, bytes, stream_of(o[10])), {dx, dw, db});
+    });
+}
+
 // A sequence of tensors, kept until the call that takes their addresses has returned.
 struct Tensors {
     PyObject* fast = nullptr;
@@ -322,15 +401,6 @@ struct Layout {
         }
     }
 };
-
-double number(PyObject* o, const char* name) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) {
-        PyErr_Clear();
-        refuse(std::string(name) + ": expected a number");
-    }
-    return v;
-}
 
 // set_norm(set, sizes, types, device, grads, norm, unscale, out_norm, stream)
 PyObject* py_set_norm(PyObject*, PyObject* const* o, Py_ssize_t count) {
@@ -397,12 +467,14 @@ PyMethodDef methods[] = {method<py_linear>("linear"),
                          method<py_linear_backward>("linear_backward"),
                          method<py_gated_ffn>("gated_ffn"),
                          method<py_gated_ffn_backward>("gated_ffn_backward"),
+                         method<py_layer_norm>("layer_norm"),
+                         method<py_layer_norm_backward>("layer_norm_backward"),
                          method<py_set_norm>("set_norm"),
                          method<py_set_clip>("set_clip"),
                          method<py_set_pack>("set_pack"),
                          {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dgc_torch", "libdgc's layer and gradient-set calls for torch tensors.",
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dgc_torch", "libdgc's layer, token and gradient-set calls for torch tensors.",
                       -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,197 @@
+// tokens.hpp -- what the token operators (layer norm, embedding, dropout,
+// recurrence) share: rows of eights in any of the three element types, sums
+// over a workgroup, and the host's checks.
+//
+// All of them are bound by memory, so a lane takes 8 elements of a row at a
+// time (16 or 32 bytes) at whatever address they have: the hardware splits
+// what does not lie on 16 bytes, and a row's last few elements go one by one.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "dgc.h"
+
+namespace dgc {
+namespace tokens {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------ device
+
+constexpr int kRow = 8;  // elements of a row per lane and step
+
+// 16 bytes at any address that an element of so many bytes can have.
+template <int BYTES>
+struct At;
+template <>
+struct At<2> {
+    typedef u32x4 V __attribute__((aligned(2), may_alias));
+};
+template <>
+struct At<4> {
+    typedef u32x4 V __attribute__((aligned(4), may_alias));
+};
+
+// 8 consecutive elements, as they are in memory.
+template <class T>
+struct Eight {
+    T t[kRow];
+};
+
+// ONCE: past the caches, for what is not read again soon.
+template <bool ONCE = false, class T>
+__device__ __forceinline__ Eight<T> read8(const T* p) {
+    typedef typename At<sizeof(T)>::V V;
+    Eight<T> e;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+        const V* q = reinterpret_cast<const V*>(p) + i;
+        const u32x4 w = ONCE ? __builtin_nontemporal_load(q) : *q;
+        __builtin_memcpy(e.t + i * (16 / sizeof(T)), &w, 16);
+    }
+    return e;
+}
+
+// The first `valid` of 8; the others are 0.
+template <bool ONCE = false, class T>
+__device__ __forceinline__ Eight<T> read8(const T* p, int valid) {
+    if (valid >= kRow) return read8<ONCE>(p);
+    Eight<T> e;
+#pragma unroll
+    for (int i = 0; i < kRow; ++i) e.t[i] = i < valid ? p[i] : T(0.0f);
+    return e;
+}
+
+template <class T>
+__device__ __forceinline__ void widen(const Eight<T>& e, float* v) {
+#pragma unroll
+    for (int i = 0; i < kRow; ++i) v[i] = float(e.t[i]);
+}
+
+template <bool ONCE = false, class T>
+__device__ __forceinline__ void load8(const T* p, int valid, float* v) {
+    widen(read8<ONCE>(p, valid), v);
+}
+
+// Rounds to nearest, ties to even: the one rounding of an output.
+template <bool ONCE = false, class T>
+__device__ __forceinline__ void store8(T* p, int valid, const float* v) {
+    typedef typename At<sizeof(T)>::V V;
+    if (valid >= kRow) {
+        Eight<T> e;
+#pragma unroll
+        for (int i = 0; i < kRow; ++i) e.t[i] = T(v[i]);
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
+            u32x4 w;
+            __builtin_memcpy(&w, e.t + i * (16 / sizeof(T)), 16);
+            V* q = reinterpret_cast<V*>(p) + i;
+            if constexpr (ONCE)
+                __builtin_nontemporal_store(w, q);
+            else
+                *q = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRow; ++i)
+            if (i < valid) p[i] = T(v[i]);
+    }
+}
+
+// 8 of a vector that is of type T or, if `wide`, binary32 (the same for the
+// whole launch).
+template <class T>
+__device__ __forceinline__ void load8_either(const void* p, int64_t at, int wide, int valid, float* v) {
+    if (wide)
+        load8(static_cast<const float*>(p) + at, valid, v);
+    else
+        load8(static_cast<const T*>(p) + at, valid, v);
+}
+
+template <class T>
+__device__ __forceinline__ void store8_either(void* p, int64_t at, int wide, int valid, const float* v) {
+    if (wide)
+        store8(static_cast<float*>(p) + at, valid, v);
+    else
+        store8(static_cast<T*>(p) + at, valid, v);
+}
+
+__device__ __forceinline__ int valid_of(int64_t end, int64_t at) {
+    return end - at >= kRow ? kRow : end > at ? int(end - at) : 0;
+}
+
+// Over 2^k lanes that lie side by side; every one of them gets the sum.
+template <int LANES, class F>
+__device__ __forceinline__ F sum_lanes(F s) {
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    return s;
+}
+
+// Over the workgroup, in a fixed order; every thread gets the sum.  Two sums in
+// a row need two places in LDS.
+template <int THREADS, class F>
+__device__ __forceinline__ F sum_block(F s, F* lds) {
+    s = sum_lanes<64>(s);
+    if constexpr (THREADS == 64) return s;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = lds[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) s += lds[w];
+    return s;
+}
+
+// -------------------------------------------------------------------- host
+
+constexpr size_t kPad = 256;
+constexpr int64_t kMostSide = (int64_t(1) << 31) - 1;  // of rows, columns, ids and sequences
+constexpr int64_t kMostArea = int64_t(1) << 48;        // elements between a matrix's ends
+
+inline size_t round_up(size_t x) { return (x + kPad - 1) / kPad * kPad; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline bool side_ok(int64_t v) { return v >= 0 && v <= kMostSide; }
+
+inline bool type_ok(int64_t t) { return t == DGC_BF16 || t == DGC_FP16 || t == DGC_FP32; }
+inline int size_of(int64_t t) { return t == DGC_FP32 || t == DGC_INT32 ? 4 : t == DGC_INT64 ? 8 : 2; }
+inline bool index_ok(int64_t t) { return t == DGC_INT32 || t == DGC_INT64; }
+
+// A matrix of rows x cols: present where it has elements, aligned to its
+// elements, its rows not overlapping.
+inline bool mat_ok(const void* p, int64_t ld, int64_t rows, int64_t cols, int size) {
+    if (rows == 0 || cols == 0) return true;
+    return p && reinterpret_cast<uintptr_t>(p) % uintptr_t(size) == 0 && ld >= cols && ld <= kMostArea / rows;
+}
+
+inline bool optional_ok(const void* p, int64_t ld, int64_t rows, int64_t cols, int size) {
+    return !p || mat_ok(p, ld, rows, cols, size);
+}
+
+inline bool vec_ok(const void* p, int64_t n, int size) { return mat_ok(p, n, 1, n, size); }
+inline bool optional_vec_ok(const void* p, int64_t n, int size) { return !p || vec_ok(p, n, size); }
+
+inline int space_ok(const void* ws, size_t have, size_t need) {
+    if (need == 0) return DGC_OK;
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % kPad != 0) return DGC_EINVAL;
+    return have < need ? DGC_ECAPACITY : DGC_OK;
+}
+
+inline int launched() { return hipGetLastError() == hipSuccess ? DGC_OK : DGC_EHIP; }
+
+// f(an element of the type), as f(__bf16()): for launches of a template.
+template <class F>
+int with_type(int64_t type, F f) {
+    switch (type) {
+        case DGC_BF16: return f(__bf16());
+        case DGC_FP16: return f(_Float16());
+        default: return f(float());
+    }
+}
+
+}  // namespace tokens
+}  // namespace dgc

@@ -33,6 +33,8 @@ DGC_MAX_BIN = 1024
 DGC_BF16 = 1
 DGC_FP16 = 2
 DGC_FP32 = 3
+DGC_INT32 = 4
+DGC_INT64 = 5
 DGC_ACT_NONE = 0
 DGC_ACT_RELU = 1
 DGC_ACT_SILU = 2
@@ -124,6 +126,11 @@ def lib() -> ctypes.CDLL:
         for call in (name, name + "_backward"):  # an argument block, workspace, its bytes, stream
             getattr(L, call).argtypes = [P, P, size, P]
             getattr(L, call).restype = ctypes.c_int
+    L.dgc_layer_norm_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(size)]
+    L.dgc_layer_norm.argtypes = [P, P]  # an argument block, stream
+    L.dgc_layer_norm_backward.argtypes = [P, P, size, P]
+    for name in ("dgc_layer_norm_workspace_bytes", "dgc_layer_norm", "dgc_layer_norm_backward"):
+        getattr(L, name).restype = ctypes.c_int
     L.dgc_gradset_bytes.argtypes = [i32, P, P, ctypes.POINTER(size)]
     L.dgc_gradset_bytes.restype = ctypes.c_int
     L.dgc_gradset_init.argtypes = [ctypes.POINTER(P), i32, P, P, P, size, P]
@@ -709,6 +716,47 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, act: str = "silu", dx=None
     _check(_torch_calls().gated_ffn_backward(_act(act, rounded), dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up, workspace,
                                              _stream_on(x, stream)), "dgc_gated_ffn_backward")
     return dx, dw_gate, dw_up
+
+
+# ------------------------------------------------------------ token operators
+
+def dgc_layer_norm_workspace_bytes(m: int, d: int, backward: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_layer_norm_workspace_bytes(m, d, int(bool(backward)), ctypes.byref(out)),
+           "dgc_layer_norm_workspace_bytes")
+    return int(out.value)
+
+
+def layer_norm_workspace(m: int, d: int, backward: bool = False, device="cuda"):
+    """A workspace for layer_norm_backward of these sizes (layer_norm needs none)."""
+    import torch
+    return torch.empty(dgc_layer_norm_workspace_bytes(m, d, backward), dtype=torch.uint8, device=device)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
+    """(x - mean) * rstd * weight + bias for the rows of x [m, d] (bfloat16, float16 or float32, contiguous
+    columns), rstd = 1 / sqrt(variance + eps).  weight and bias [d] are of x's type or float32, the same for both.
+
+    `out`, `mean` and `rstd` are written if given; mean and rstd (float32 [m]) are what layer_norm_backward
+    takes.  `out` may be x."""
+    if out is None:
+        out = _new(x, tuple(x.shape), x.dtype, stream)
+    _check(_torch_calls().layer_norm(x, weight, bias, eps, out, mean, rstd, _stream_on(x, stream)), "dgc_layer_norm")
+    return out
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, residual=None, dx=None, dweight=None, dbias=None,
+                        workspace=None, stream=None):
+    """Gradients of layer_norm for the incoming dy [m, d] and the saved mean and rstd: writes each given one of
+    dx [m, d], dweight [d] and dbias [d] (x's type or float32, the same for both: views of a learner's flat
+    gradient).  `residual` [m, d], the gradient that goes past the norm, is added to dx.  dx may be dy or
+    residual.  Returns (dx, dweight, dbias)."""
+    if workspace is None:
+        need = dgc_layer_norm_workspace_bytes(x.shape[0], x.shape[-1], True) if x.dim() == 2 else 0
+        workspace = _fresh(need, x, stream)
+    _check(_torch_calls().layer_norm_backward(dy, x, mean, rstd, weight, residual, dx, dweight, dbias, workspace,
+                                              _stream_on(x, stream)), "dgc_layer_norm_backward")
+    return dx, dweight, dbias
 
 
 def dgc_gradset_bytes(sizes: Sequence[int], types: Sequence[int]) -> int:
