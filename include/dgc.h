@@ -739,6 +739,33 @@ int dgc_layer_norm(const dgc_layer_norm_args* args, hipStream_t stream);
 int dgc_layer_norm_backward(const dgc_layer_norm_backward_args* args, void* workspace,
                             size_t workspace_bytes, hipStream_t stream);
 
+/* y = x * keep / P(keep) + residual for x[m][d].  keep is drawn anew from a
+ * counter wherever it is needed and stored nowhere: element (i, j) takes 16 bits
+ * of Philox4x32-10 (Salmon, Moraes, Dror, Shaw: Parallel random numbers: as easy
+ * as 1, 2, 3, 2011) with the key `seed` (its low word first) and the counter
+ * (j / 8, i, offset's low word, offset's high word): of the four words the one
+ * numbered j % 8 / 2, of that the low half for an even j.  It is kept where these
+ * bits, as a number, are below K = floor((1 - p) * 65536 + 0.5), and P(keep) =
+ * K / 65536 (K = 0: all zeros).  What is not kept counts as 0, whatever it holds.
+ * step (device, one int64, or NULL) is added to offset when the call runs, so
+ * that a captured call draws anew in each replay.  p lies in [0, 1]; residual
+ * may be NULL; y may be x or residual.  The gradient for x is the same call on the
+ * incoming gradient, without a residual. */
+typedef struct dgc_dropout_args {
+    int64_t type, m, d;
+    double p;
+    uint64_t seed, offset;
+    const int64_t* step;
+    const void* x;
+    int64_t ldx;
+    const void* residual;
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+} dgc_dropout_args;
+
+int dgc_dropout(const dgc_dropout_args* args, hipStream_t stream);
+
 /*
  * Gradient sets: from a model's tensors to a learner
  * --------------------------------------------------

@@ -173,6 +173,15 @@ double number(PyObject* o, const char* name) {
     return v;
 }
 
+uint64_t unsigned_integer(PyObject* o, const char* name) {
+    const uint64_t v = PyLong_Check(o) ? PyLong_AsUnsignedLongLong(o) : uint64_t(-1);
+    if (!PyLong_Check(o) || (v == uint64_t(-1) && PyErr_Occurred())) {
+        PyErr_Clear();
+        refuse(std::string(name) + ": expected an integer of 0 to 2^64 - 1");
+    }
+    return v;
+}
+
 hipStream_t stream_of(PyObject* o) { return reinterpret_cast<hipStream_t>(uintptr_t(integer(o))); }
 
 // Runs f, which returns a DGC_* code; refusals become ValueError.
@@ -347,6 +356,26 @@ PyObject* py_layer_norm_backward(PyObject*, PyObject* const* o, Py_ssize_t count
     });
 }
 
+// dropout(x, p, seed, offset, step, residual, out, stream)
+PyObject* py_dropout(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 8, [&] {
+        const at::Tensor& x = needed(o[0], "x");
+        const Call c("dropout", x, true);
+        dgc_dropout_args a{};
+        a.type = type_code(c.type);
+        a.p = number(o[1], "p");
+        a.seed = unsigned_integer(o[2], "seed");
+        a.offset = unsigned_integer(o[3], "offset");
+        c.vec(tensor(o[4], "step"), "step", 1, at::kLong, a.step);
+        c.sides(x, "x", a.m, a.d);
+        c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
+        c.mat(tensor(o[5], "residual"), "residual", a.m, a.d, c.type, a.residual, a.ldr);
+        const at::Tensor* y = &needed(o[6], "out");
+        c.mat(y, "out", a.m, a.d, c.type, a.y, a.ldy);
+        return done(dgc_dropout(&a, stream_of(o[7])), {y});
+    });
+}
+
 // A sequence of tensors, kept until the call that takes their addresses has returned.
 struct Tensors {
     PyObject* fast = nullptr;
@@ -469,6 +498,7 @@ PyMethodDef methods[] = {method<py_linear>("linear"),
                          method<py_gated_ffn_backward>("gated_ffn_backward"),
                          method<py_layer_norm>("layer_norm"),
                          method<py_layer_norm_backward>("layer_norm_backward"),
+                         method<py_dropout>("dropout"),
                          method<py_set_norm>("set_norm"),
                          method<py_set_clip>("set_clip"),
                          method<py_set_pack>("set_pack"),

@@ -127,9 +127,9 @@ def lib() -> ctypes.CDLL:
             getattr(L, call).argtypes = [P, P, size, P]
             getattr(L, call).restype = ctypes.c_int
     L.dgc_layer_norm_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(size)]
-    L.dgc_layer_norm.argtypes = [P, P]  # an argument block, stream
+    L.dgc_dropout.argtypes = L.dgc_layer_norm.argtypes = [P, P]  # an argument block, stream
     L.dgc_layer_norm_backward.argtypes = [P, P, size, P]
-    for name in ("dgc_layer_norm_workspace_bytes", "dgc_layer_norm", "dgc_layer_norm_backward"):
+    for name in ("dgc_layer_norm_workspace_bytes", "dgc_layer_norm", "dgc_layer_norm_backward", "dgc_dropout"):
         getattr(L, name).restype = ctypes.c_int
     L.dgc_gradset_bytes.argtypes = [i32, P, P, ctypes.POINTER(size)]
     L.dgc_gradset_bytes.restype = ctypes.c_int
@@ -757,6 +757,26 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, residual=None, dx=None, 
     _check(_torch_calls().layer_norm_backward(dy, x, mean, rstd, weight, residual, dx, dweight, dbias, workspace,
                                               _stream_on(x, stream)), "dgc_layer_norm_backward")
     return dx, dweight, dbias
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, out=None, stream=None):
+    """x * keep / P(keep) + residual for x [m, d] (bfloat16, float16 or float32, contiguous columns): each element
+    is kept with the probability 1 - p, held to 16 bits.
+
+    Which ones follows from (seed, offset, row, column) alone and is stored nowhere: dropout_backward with the same
+    numbers keeps the same ones.  Every use takes another `offset` (0 to 2^64 - 1).  `step`, an int64 tensor of one
+    element on the device, is added to it when the call runs: a captured call draws anew in each replay, once the
+    program has changed it.  `out` may be x or residual."""
+    if out is None:
+        out = _new(x, tuple(x.shape), x.dtype, stream)
+    _check(_torch_calls().dropout(x, p, seed, offset, step, residual, out, _stream_on(x, stream)), "dgc_dropout")
+    return out
+
+
+def dropout_backward(dy, p: float, seed: int, offset: int = 0, step=None, dx=None, stream=None):
+    """The gradient of dropout's x for the incoming dy, of the same p, seed, offset and step.  (Its residual's is dy
+    itself.)  `dx` may be dy."""
+    return dropout(dy, p, seed, offset, step, None, dx, stream)
 
 
 def dgc_gradset_bytes(sizes: Sequence[int], types: Sequence[int]) -> int:

@@ -7,6 +7,7 @@ threads, and what makes the terms; so it is off by DEPTH * U of the sum of the
 magnitudes.  Outputs are rounded by half a step of their type
 (layer_reference.rounding)."""
 
+import numpy as np
 import torch
 
 from layer_reference import check, rounding  # noqa: F401
@@ -59,3 +60,28 @@ def layer_norm_backward(dy, x, mean, rstd, weight, residual):
         e = e + 2 * U * (dx.abs() + residual.abs())
     return {"dx": (dx, e), "dweight": ((dy * n).sum(0), (m + 8) * U * (dy * n).abs().sum(0)),
             "dbias": (dy.sum(0), (m + 4) * U * dy.abs().sum(0))}
+
+
+def philox(counter, key):
+    """Philox4x32-10 of four arrays of 32-bit words in numpy's uint64."""
+    mask, half = np.uint64(0xFFFFFFFF), np.uint64(32)
+    c, (k0, k1) = list(counter), key
+    for _ in range(10):
+        p, q = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(q >> half) ^ c[1] ^ np.uint64(k0), q & mask, (p >> half) ^ c[3] ^ np.uint64(k1), p & mask]
+        k0, k1 = (k0 + 0x9E3779B9) & 0xFFFFFFFF, (k1 + 0xBB67AE85) & 0xFFFFFFFF
+    return c
+
+
+def draws(m, d, seed, offset):
+    """The 16 bits of each element, as numbers [m, d]."""
+    groups, low = (d + 7) // 8, 0xFFFFFFFF
+    counter = [np.broadcast_to(np.arange(groups, dtype=np.uint64), (m, groups)),
+               np.broadcast_to(np.arange(m, dtype=np.uint64)[:, None], (m, groups)),
+               np.full((m, groups), offset & low, np.uint64), np.full((m, groups), offset >> 32, np.uint64)]
+    words = np.stack(philox(counter, (seed & low, seed >> 32)), 2).astype(np.int64)
+    return np.stack([words & 0xFFFF, words >> 16], 3).reshape(m, groups * 8)[:, :d]
+
+
+def kept(p):
+    return int(np.floor((1 - p) * 65536 + 0.5))
