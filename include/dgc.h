@@ -766,6 +766,39 @@ typedef struct dgc_dropout_args {
 
 int dgc_dropout(const dgc_dropout_args* args, hipStream_t stream);
 
+/* y[i] = scale * table[ids[i]] for ids[m] (DGC_INT32 or DGC_INT64, device) and
+ * table[vocab][d].  An id outside of [0, vocab) is padding: a row of zeros. */
+typedef struct dgc_embedding_args {
+    int64_t type, index_type, m, vocab, d;
+    const void* ids;
+    const void* table;
+    int64_t ldt;
+    double scale;
+    void* y;
+    int64_t ldy;
+} dgc_embedding_args;
+
+/* dtable[v] = scale * the sum of dy[i] over all i with ids[i] = v, in the order
+ * of i whatever the timing: the same bits every run.  accumulate: that is
+ * added to the rows that some id names, and no other row is touched; else
+ * every row is written, zeros where no id names it.  Padding adds nothing.
+ * dtable is of grad_type: `type` or DGC_FP32. */
+typedef struct dgc_embedding_backward_args {
+    int64_t type, grad_type, index_type, m, vocab, d, accumulate;
+    const void* dy;
+    int64_t lddy;
+    const void* ids;
+    double scale;
+    void* dtable;
+    int64_t lddt;
+} dgc_embedding_backward_args;
+
+int dgc_embedding_workspace_bytes(int64_t m, int64_t vocab, int64_t d, int32_t backward,
+                                  size_t* bytes);
+int dgc_embedding(const dgc_embedding_args* args, hipStream_t stream);
+int dgc_embedding_backward(const dgc_embedding_backward_args* args, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Gradient sets: from a model's tensors to a learner
  * --------------------------------------------------

@@ -58,6 +58,9 @@ int64_t type_code(at::ScalarType t) {
     return t == at::kBFloat16 ? DGC_BF16 : t == at::kHalf ? DGC_FP16 : t == at::kFloat ? DGC_FP32 : 0;
 }
 
+// Of ids and row numbers; 0: none of both.
+int64_t index_code(at::ScalarType t) { return t == at::kInt ? DGC_INT32 : t == at::kLong ? DGC_INT64 : 0; }
+
 std::string shape(const at::Tensor& t) {
     std::string s = "(";
     for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
@@ -144,6 +147,14 @@ struct Call {
         if (x.dim() != 2) refuse(std::string(name) + ": expected a matrix, got " + shape(x));
         m = x.size(0);
         d = x.size(1);
+    }
+
+    // `n` whole numbers of 32 or 64 bits; their type.
+    int64_t indices(const at::Tensor& t, const char* name, int64_t n, const void*& p) const {
+        const int64_t code = index_code(t.scalar_type());
+        if (!code) refuse(std::string(name) + ": expected int32 or int64, got " + c10::toString(t.scalar_type()));
+        vec(&t, name, n, t.scalar_type(), p);
+        return code;
     }
 
     // The type of weight gradients: x's, or binary32.
@@ -376,6 +387,48 @@ PyObject* py_dropout(PyObject*, PyObject* const* o, Py_ssize_t count) {
     });
 }
 
+// embedding(ids, table, scale, out, stream)
+PyObject* py_embedding(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 5, [&] {
+        const at::Tensor &ids = needed(o[0], "ids"), &table = needed(o[1], "table");
+        const Call c("embedding", table, true);
+        dgc_embedding_args a{};
+        a.type = type_code(c.type);
+        a.scale = number(o[2], "scale");
+        c.sides(table, "table", a.vocab, a.d);
+        c.mat(&table, "table", a.vocab, a.d, c.type, a.table, a.ldt);
+        a.m = ids.numel();
+        a.index_type = c.indices(ids, "ids", a.m, a.ids);
+        const at::Tensor* y = &needed(o[3], "out");
+        c.mat(y, "out", a.m, a.d, c.type, a.y, a.ldy);
+        return done(dgc_embedding(&a, stream_of(o[4])), {y});
+    });
+}
+
+// embedding_backward(dy, ids, dtable, scale, accumulate, workspace, stream)
+PyObject* py_embedding_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 7, [&] {
+        const at::Tensor &dy = needed(o[0], "dy"), &ids = needed(o[1], "ids"), &dt = needed(o[2], "dtable");
+        const Call c("embedding_backward", dy, true);
+        dgc_embedding_backward_args a{};
+        a.type = type_code(c.type);
+        const at::ScalarType g = c.gradients(&dt, nullptr);
+        a.grad_type = type_code(g);
+        a.scale = number(o[3], "scale");
+        a.accumulate = integer(o[4]);
+        c.sides(dy, "dy", a.m, a.d);
+        c.mat(&dy, "dy", a.m, a.d, c.type, a.dy, a.lddy);
+        a.index_type = c.indices(ids, "ids", a.m, a.ids);
+        int64_t d;
+        c.sides(dt, "dtable", a.vocab, d);
+        c.mat(&dt, "dtable", a.vocab, a.d, g, a.dtable, a.lddt);
+        void* ws;
+        size_t bytes;
+        c.space(tensor(o[5], "workspace"), ws, bytes);
+        return done(dgc_embedding_backward(&a, ws, bytes, stream_of(o[6])), {&dt});
+    });
+}
+
 // A sequence of tensors, kept until the call that takes their addresses has returned.
 struct Tensors {
     PyObject* fast = nullptr;
@@ -499,6 +552,8 @@ PyMethodDef methods[] = {method<py_linear>("linear"),
                          method<py_layer_norm>("layer_norm"),
                          method<py_layer_norm_backward>("layer_norm_backward"),
                          method<py_dropout>("dropout"),
+                         method<py_embedding>("embedding"),
+                         method<py_embedding_backward>("embedding_backward"),
                          method<py_set_norm>("set_norm"),
                          method<py_set_clip>("set_clip"),
                          method<py_set_pack>("set_pack"),

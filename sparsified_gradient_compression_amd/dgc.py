@@ -127,9 +127,13 @@ def lib() -> ctypes.CDLL:
             getattr(L, call).argtypes = [P, P, size, P]
             getattr(L, call).restype = ctypes.c_int
     L.dgc_layer_norm_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(size)]
-    L.dgc_dropout.argtypes = L.dgc_layer_norm.argtypes = [P, P]  # an argument block, stream
-    L.dgc_layer_norm_backward.argtypes = [P, P, size, P]
-    for name in ("dgc_layer_norm_workspace_bytes", "dgc_layer_norm", "dgc_layer_norm_backward", "dgc_dropout"):
+    L.dgc_embedding_workspace_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(size)]
+    for name in ("dgc_layer_norm", "dgc_dropout", "dgc_embedding"):  # an argument block, stream
+        getattr(L, name).argtypes = [P, P]
+    for name in ("dgc_layer_norm_backward", "dgc_embedding_backward"):  # ... and a workspace and its bytes before it
+        getattr(L, name).argtypes = [P, P, size, P]
+    for name in ("dgc_layer_norm", "dgc_layer_norm_backward", "dgc_layer_norm_workspace_bytes", "dgc_dropout",
+                 "dgc_embedding", "dgc_embedding_backward", "dgc_embedding_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_int
     L.dgc_gradset_bytes.argtypes = [i32, P, P, ctypes.POINTER(size)]
     L.dgc_gradset_bytes.restype = ctypes.c_int
@@ -777,6 +781,42 @@ def dropout_backward(dy, p: float, seed: int, offset: int = 0, step=None, dx=Non
     """The gradient of dropout's x for the incoming dy, of the same p, seed, offset and step.  (Its residual's is dy
     itself.)  `dx` may be dy."""
     return dropout(dy, p, seed, offset, step, None, dx, stream)
+
+
+def dgc_embedding_workspace_bytes(m: int, vocab: int, d: int, backward: bool = True) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_embedding_workspace_bytes(m, vocab, d, int(bool(backward)), ctypes.byref(out)),
+           "dgc_embedding_workspace_bytes")
+    return int(out.value)
+
+
+def embedding_workspace(m: int, vocab: int, d: int, device="cuda"):
+    """A workspace for embedding_backward of m tokens (embedding needs none)."""
+    import torch
+    return torch.empty(dgc_embedding_workspace_bytes(m, vocab, d), dtype=torch.uint8, device=device)
+
+
+def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
+    """scale * table[ids] for ids [m] (int32 or int64) and table [vocab, d] (bfloat16, float16 or float32,
+    contiguous columns).  An id outside of [0, vocab), -1 for instance, is padding: a row of zeros."""
+    if out is None:
+        out = _new(table, (ids.numel(), table.shape[-1]), table.dtype, stream)
+    _check(_torch_calls().embedding(ids, table, scale, out, _stream_on(table, stream)), "dgc_embedding")
+    return out
+
+
+def embedding_backward(dy, ids, dtable, scale: float = 1.0, accumulate: bool = False, workspace=None, stream=None):
+    """The gradient of embedding's table for the incoming dy [m, d]: dtable[v] = scale * the sum of dy[i] over the
+    ids that are v, in binary32, in the order of i: the same bits every run.  dtable [vocab, d] is of dy's type
+    or float32: a view of a learner's flat gradient.  All of it is written; with `accumulate` the sums are added
+    to the rows that some id names, and no other row is touched (a table that is an output layer's weight too).
+    `workspace`: embedding_workspace(m, vocab, d).  Returns dtable."""
+    if workspace is None:
+        need = dgc_embedding_workspace_bytes(dy.shape[0], dtable.shape[0], dy.shape[-1]) if dy.dim() == dtable.dim() == 2 else 0
+        workspace = _fresh(need, dy, stream)
+    _check(_torch_calls().embedding_backward(dy, ids, dtable, scale, int(bool(accumulate)), workspace,
+                                             _stream_on(dy, stream)), "dgc_embedding_backward")
+    return dtable
 
 
 def dgc_gradset_bytes(sizes: Sequence[int], types: Sequence[int]) -> int:
