@@ -799,6 +799,66 @@ int dgc_embedding(const dgc_embedding_args* args, hipStream_t stream);
 int dgc_embedding_backward(const dgc_embedding_backward_args* args, void* workspace,
                            size_t workspace_bytes, hipStream_t stream);
 
+/* A gated linear recurrence along `batch` sequences of rows: with f = 1 / (1 +
+ * exp(-gate)), h[t] = f[t] h[t-1] + (1 - f[t]) x[t] for each column.  gate, x and
+ * h are m x d; the sequences lie end to end in their rows.  offsets (batch + 1
+ * row numbers of index_type, device, not decreasing): sequence b has the rows
+ * from offsets[b] up to offsets[b + 1]; rows outside of all sequences are neither
+ * read nor written.  NULL: all are equally long, m / batch rows.  Numbers
+ * outside of [0, m] are taken as 0 or m, so that no bad one leads out of the
+ * matrices.  Before its first row a sequence has h0[b] (binary32[batch][d], NULL:
+ * zeros), and its last h, in binary32, goes to state[b] (NULL: nowhere; h0[b] for
+ * an empty sequence).  state may be h0.  h itself is binary32 on its way along
+ * the rows; what is stored is rounded. */
+typedef struct dgc_recurrence_args {
+    int64_t type, index_type, m, d, batch;
+    const void* offsets;
+    const void* gate;
+    int64_t ldg;
+    const void* x;
+    int64_t ldx;
+    const float* h0;
+    int64_t ldh0;
+    void* h;
+    int64_t ldh;
+    float* state;
+    int64_t lds;
+} dgc_recurrence_args;
+
+/* With g[t] = dh[t] + f[t+1] g[t+1] (behind the last row: dstate, binary32, NULL:
+ * zeros), and h as it was written: dx = (1 - f) g, dgate = g (h[t-1] - x) f (1 -
+ * f), dh0[b] = f[first] g[first] (dstate[b] for an empty sequence).  Each of
+ * dgate, dx and dh0 may be NULL, and dh0 may be dstate. */
+typedef struct dgc_recurrence_backward_args {
+    int64_t type, index_type, m, d, batch;
+    const void* offsets;
+    const void* dh;
+    int64_t lddh;
+    const void* gate;
+    int64_t ldg;
+    const void* x;
+    int64_t ldx;
+    const void* h;
+    int64_t ldh;
+    const float* h0;
+    int64_t ldh0;
+    const float* dstate;
+    int64_t ldds;
+    void* dgate;
+    int64_t lddg;
+    void* dx;
+    int64_t lddx;
+    float* dh0;
+    int64_t lddh0;
+} dgc_recurrence_backward_args;
+
+int dgc_recurrence_workspace_bytes(int64_t m, int64_t d, int64_t batch, int32_t backward,
+                                   size_t* bytes);
+int dgc_recurrence(const dgc_recurrence_args* args, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+int dgc_recurrence_backward(const dgc_recurrence_backward_args* args, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Gradient sets: from a model's tensors to a learner
  * --------------------------------------------------

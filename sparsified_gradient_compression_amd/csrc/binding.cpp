@@ -429,6 +429,69 @@ PyObject* py_embedding_backward(PyObject*, PyObject* const* o, Py_ssize_t count)
     });
 }
 
+// The rows of a recurrence's sequences: `batch` of equal length, or offsets.
+void sequences(const Call& c, PyObject* batch, const at::Tensor* offsets, int64_t& count, int64_t& type, const void*& p) {
+    p = nullptr;
+    type = DGC_INT32;
+    if (batch != Py_None) count = integer(batch);
+    if (!offsets) {
+        if (batch == Py_None) refuse(std::string(c.fn) + ": expected a batch or offsets");
+        return;
+    }
+    if (batch != Py_None) refuse(std::string(c.fn) + ": a batch of equally long sequences, or offsets, not both");
+    if (offsets->dim() != 1 || offsets->size(0) < 1) refuse("offsets: expected batch + 1 row numbers, got " + shape(*offsets));
+    count = offsets->size(0) - 1;
+    type = c.indices(*offsets, "offsets", count + 1, p);
+}
+
+// recurrence(gate, x, h0, batch, offsets, out, state, workspace, stream)
+PyObject* py_recurrence(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 9, [&] {
+        const at::Tensor& x = needed(o[1], "x");
+        const Call c("recurrence", x, true);
+        dgc_recurrence_args a{};
+        a.type = type_code(c.type);
+        c.sides(x, "x", a.m, a.d);
+        sequences(c, o[3], tensor(o[4], "offsets"), a.batch, a.index_type, a.offsets);
+        c.mat(&needed(o[0], "gate"), "gate", a.m, a.d, c.type, a.gate, a.ldg);
+        c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
+        c.mat(tensor(o[2], "h0"), "h0", a.batch, a.d, at::kFloat, a.h0, a.ldh0);
+        const at::Tensor *h = &needed(o[5], "out"), *state = tensor(o[6], "state");
+        c.mat(h, "out", a.m, a.d, c.type, a.h, a.ldh);
+        c.mat(state, "state", a.batch, a.d, at::kFloat, a.state, a.lds);
+        void* ws;
+        size_t bytes;
+        c.space(tensor(o[7], "workspace"), ws, bytes);
+        return done(dgc_recurrence(&a, ws, bytes, stream_of(o[8])), {h, state});
+    });
+}
+
+// recurrence_backward(dh, gate, x, h, h0, dstate, batch, offsets, dgate, dx, dh0, workspace, stream)
+PyObject* py_recurrence_backward(PyObject*, PyObject* const* o, Py_ssize_t count) {
+    return guarded(count, 13, [&] {
+        const at::Tensor& x = needed(o[2], "x");
+        const Call c("recurrence_backward", x, true);
+        dgc_recurrence_backward_args a{};
+        a.type = type_code(c.type);
+        c.sides(x, "x", a.m, a.d);
+        sequences(c, o[6], tensor(o[7], "offsets"), a.batch, a.index_type, a.offsets);
+        c.mat(&needed(o[0], "dh"), "dh", a.m, a.d, c.type, a.dh, a.lddh);
+        c.mat(&needed(o[1], "gate"), "gate", a.m, a.d, c.type, a.gate, a.ldg);
+        c.mat(&x, "x", a.m, a.d, c.type, a.x, a.ldx);
+        c.mat(&needed(o[3], "h"), "h", a.m, a.d, c.type, a.h, a.ldh);
+        c.mat(tensor(o[4], "h0"), "h0", a.batch, a.d, at::kFloat, a.h0, a.ldh0);
+        c.mat(tensor(o[5], "dstate"), "dstate", a.batch, a.d, at::kFloat, a.dstate, a.ldds);
+        const at::Tensor *dg = tensor(o[8], "dgate"), *dx = tensor(o[9], "dx"), *d0 = tensor(o[10], "dh0");
+        c.mat(dg, "dgate", a.m, a.d, c.type, a.dgate, a.lddg);
+        c.mat(dx, "dx", a.m, a.d, c.type, a.dx, a.lddx);
+        c.mat(d0, "dh0", a.batch, a.d, at::kFloat, a.dh0, a.lddh0);
+        void* ws;
+        size_t bytes;
+        c.space(tensor(o[11], "workspace"), ws, bytes);
+        return done(dgc_recurrence_backward(&a, ws, bytes, stream_of(o[12])), {dg, dx, d0});
+    });
+}
+
 // A sequence of tensors, kept until the call that takes their addresses has returned.
 struct Tensors {
     PyObject* fast = nullptr;
@@ -554,6 +617,8 @@ PyMethodDef methods[] = {method<py_linear>("linear"),
                          method<py_dropout>("dropout"),
                          method<py_embedding>("embedding"),
                          method<py_embedding_backward>("embedding_backward"),
+                         method<py_recurrence>("recurrence"),
+                         method<py_recurrence_backward>("recurrence_backward"),
                          method<py_set_norm>("set_norm"),
                          method<py_set_clip>("set_clip"),
                          method<py_set_pack>("set_pack"),

@@ -127,13 +127,16 @@ def lib() -> ctypes.CDLL:
             getattr(L, call).argtypes = [P, P, size, P]
             getattr(L, call).restype = ctypes.c_int
     L.dgc_layer_norm_workspace_bytes.argtypes = [i64, i64, i32, ctypes.POINTER(size)]
-    L.dgc_embedding_workspace_bytes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(size)]
+    for name in ("dgc_embedding_workspace_bytes", "dgc_recurrence_workspace_bytes"):
+        getattr(L, name).argtypes = [i64, i64, i64, i32, ctypes.POINTER(size)]
     for name in ("dgc_layer_norm", "dgc_dropout", "dgc_embedding"):  # an argument block, stream
         getattr(L, name).argtypes = [P, P]
-    for name in ("dgc_layer_norm_backward", "dgc_embedding_backward"):  # ... and a workspace and its bytes before it
+    # ... and a workspace and its bytes before it
+    for name in ("dgc_layer_norm_backward", "dgc_embedding_backward", "dgc_recurrence", "dgc_recurrence_backward"):
         getattr(L, name).argtypes = [P, P, size, P]
     for name in ("dgc_layer_norm", "dgc_layer_norm_backward", "dgc_layer_norm_workspace_bytes", "dgc_dropout",
-                 "dgc_embedding", "dgc_embedding_backward", "dgc_embedding_workspace_bytes"):
+                 "dgc_embedding", "dgc_embedding_backward", "dgc_embedding_workspace_bytes", "dgc_recurrence",
+                 "dgc_recurrence_backward", "dgc_recurrence_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_int
     L.dgc_gradset_bytes.argtypes = [i32, P, P, ctypes.POINTER(size)]
     L.dgc_gradset_bytes.restype = ctypes.c_int
@@ -817,6 +820,61 @@ def embedding_backward(dy, ids, dtable, scale: float = 1.0, accumulate: bool = F
     _check(_torch_calls().embedding_backward(dy, ids, dtable, scale, int(bool(accumulate)), workspace,
                                              _stream_on(dy, stream)), "dgc_embedding_backward")
     return dtable
+
+
+def dgc_recurrence_workspace_bytes(m: int, d: int, batch: int = 1, backward: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_recurrence_workspace_bytes(m, d, batch, int(bool(backward)), ctypes.byref(out)),
+           "dgc_recurrence_workspace_bytes")
+    return int(out.value)
+
+
+def recurrence_workspace(m: int, d: int, batch: int = 1, backward: bool = False, device="cuda"):
+    """A workspace for recurrence (or recurrence_backward) of `batch` sequences of m rows in all."""
+    import torch
+    return torch.empty(dgc_recurrence_workspace_bytes(m, d, batch, backward), dtype=torch.uint8, device=device)
+
+
+def _sequences(batch, offsets, h0):
+    """(batch or None, the number of sequences)."""
+    if offsets is not None:
+        return batch, max(int(offsets.numel()) - 1, 0)
+    if batch is None:
+        batch = 1 if h0 is None else int(h0.shape[0])
+    return batch, batch
+
+
+def recurrence(gate, x, h0=None, batch: Optional[int] = None, offsets=None, out=None, state=None, workspace=None,
+               stream=None):
+    """h[t] = f[t] h[t-1] + (1 - f[t]) x[t] with f = sigmoid(gate), column by column along sequences, for gate and
+    x [m, d] (bfloat16, float16 or float32, contiguous columns; halves of one wider matrix for instance).
+
+    The sequences lie end to end in the rows: `batch` of them, equally long (as many as h0 has, else one), or
+    from each of the row numbers in `offsets` (int32 or int64, batch + 1 of them, on the device) up to the next; rows
+    outside of them are left as they are.  h0 [batch, d] (float32; without it zeros) comes before the first rows,
+    `state` [batch, d] (float32) receives the last ones unrounded; it may be h0: one step for each of m answers is
+    recurrence(gate, x, state, batch=m, state=state).  `workspace`: recurrence_workspace(m, d, batch)."""
+    batch, count = _sequences(batch, offsets, h0)
+    if out is None:
+        out = _new(x, tuple(x.shape), x.dtype, stream)
+    if workspace is None:
+        workspace = _fresh(dgc_recurrence_workspace_bytes(x.shape[0], x.shape[-1], count), x, stream)
+    _check(_torch_calls().recurrence(gate, x, h0, batch, offsets, out, state, workspace, _stream_on(x, stream)),
+           "dgc_recurrence")
+    return out
+
+
+def recurrence_backward(dh, gate, x, h, h0=None, dstate=None, batch: Optional[int] = None, offsets=None, dgate=None,
+                        dx=None, dh0=None, workspace=None, stream=None):
+    """Gradients of recurrence for the incoming dh [m, d], of h as it was written, and dstate [batch, d] (float32),
+    of the last rows' states: writes each given one of dgate and dx [m, d] and dh0 [batch, d] (float32; may be
+    dstate).  `workspace`: recurrence_workspace(m, d, batch, backward=True).  Returns (dgate, dx, dh0)."""
+    batch, count = _sequences(batch, offsets, h0 if h0 is not None else dstate)
+    if workspace is None:
+        workspace = _fresh(dgc_recurrence_workspace_bytes(x.shape[0], x.shape[-1], count, True), x, stream)
+    _check(_torch_calls().recurrence_backward(dh, gate, x, h, h0, dstate, batch, offsets, dgate, dx, dh0, workspace,
+                                              _stream_on(x, stream)), "dgc_recurrence_backward")
+    return dgate, dx, dh0
 
 
 def dgc_gradset_bytes(sizes: Sequence[int], types: Sequence[int]) -> int:

@@ -85,3 +85,79 @@ def draws(m, d, seed, offset):
 
 def kept(p):
     return int(np.floor((1 - p) * 65536 + 0.5))
+
+
+# Of f and 1 - f: an exponential within 2 steps, a sum, a quotient and a product.
+GATE = 8 * U
+# Additions between parts of a sequence, on the way of any term.
+PARTS = 40 * U
+
+
+def places(offsets, m):
+    """Row numbers of the sequences [batch, longest] and which of these places hold one, from the host's offsets."""
+    begin = torch.tensor(offsets[:-1], dtype=torch.int64, device="cuda")
+    length = torch.tensor(offsets[1:], dtype=torch.int64, device="cuda") - begin
+    step = torch.arange(int(length.max()) if len(length) else 0, device="cuda")
+    valid = step < length[:, None]
+    return torch.where(valid, begin[:, None] + step, 0), valid
+
+
+def lay(v, row, valid, other):
+    return torch.where(valid[:, :, None], v.double()[row], other) if row.numel() else v.new_zeros((*row.shape, v.shape[1]), dtype=torch.float64)
+
+
+def back(v, row, valid, m):
+    out = torch.zeros((m, v.shape[2]), dtype=torch.float64, device="cuda")
+    out[row[valid]] = v[valid]
+    return out
+
+
+def recurrence(gate, x, h0, offsets):
+    """(h, its error, state, its error), row by row.
+
+    A term that is t steps old has gone through t products with an f: each adds GATE and a rounding of its share.
+    The magnitudes' own recurrence carries that along."""
+    m, d = x.shape
+    row, valid = places(offsets, m)
+    f, r = lay(torch.sigmoid(gate.double()), row, valid, 1.0), lay(torch.sigmoid(-gate.double()), row, valid, 0.0)
+    xs = lay(x, row, valid, 0.0)
+    now = torch.zeros(len(offsets) - 1, d, dtype=torch.float64, device="cuda")
+    now = now if h0 is None else now + h0
+    size, e = now.abs(), torch.zeros_like(now)
+    h, eh = torch.zeros_like(f), torch.zeros_like(f)
+    for t in range(row.shape[1]):
+        on = valid[:, t, None]
+        e = torch.where(on, f[:, t] * (e + (GATE + 2 * U) * size) + (GATE + 2 * U) * r[:, t] * xs[:, t].abs(), e)
+        now = f[:, t] * now + r[:, t] * xs[:, t]
+        size = f[:, t] * size + r[:, t] * xs[:, t].abs()
+        h[:, t], eh[:, t] = now, e + PARTS * size
+    return back(h, row, valid, m), back(eh, row, valid, m), now, e + PARTS * size
+
+
+def recurrence_backward(dh, gate, x, h, h0, dstate, offsets):
+    """{name: (value, its error)} of dgate, dx and dh0."""
+    m, d = x.shape
+    row, valid = places(offsets, m)
+    f, r = lay(torch.sigmoid(gate.double()), row, valid, 1.0), lay(torch.sigmoid(-gate.double()), row, valid, 0.0)
+    xs, dhs, hs = (lay(v, row, valid, 0.0) for v in (x, dh, h))
+    n = len(offsets) - 1
+    start = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    start = start if h0 is None else start + h0
+    before = torch.cat([start[:, None], hs], 1)[:, :row.shape[1]]
+    now = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    now = now if dstate is None else now + dstate
+    size, e = now.abs(), torch.zeros_like(now)
+    g, eg = torch.zeros_like(f), torch.zeros_like(f)
+    for t in reversed(range(row.shape[1])):
+        on = valid[:, t, None]
+        g[:, t] = now + dhs[:, t]
+        size = size + dhs[:, t].abs()
+        eg[:, t] = e + PARTS * size
+        e = torch.where(on, f[:, t] * (e + (GATE + 2 * U) * size), e)
+        now, size = f[:, t] * g[:, t], f[:, t] * size
+    dx, edx = r * g, r * (eg + (GATE + 2 * U) * g.abs())
+    off = before - xs
+    dgate = g * off * f * r
+    edgate = f * r * off.abs() * (eg + (2 * GATE + 6 * U) * g.abs())
+    return {"dgate": (back(dgate, row, valid, m), back(edgate, row, valid, m)),
+            "dx": (back(dx, row, valid, m), back(edx, row, valid, m)), "dh0": (now, e + PARTS * size)}
