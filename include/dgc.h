@@ -803,8 +803,8 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* args, void* worksp
  * exp(-gate)), h[t] = f[t] h[t-1] + (1 - f[t]) x[t] for each column.  gate, x and
  * h are m x d; the sequences lie end to end in their rows.  offsets (batch + 1
  * row numbers of index_type, device, not decreasing): sequence b has the rows
- * from offsets[b] up to offsets[b + 1]; rows outside of all sequences are neither
- * read nor written.  NULL: all are equally long, m / batch rows.  Numbers
+ * from offsets[b] up to offsets[b + 1]; rows outside of all sequences are left as
+ * they are.  NULL: all are equally long, m / batch rows.  Numbers
  * outside of [0, m] are taken as 0 or m, so that no bad one leads out of the
  * matrices.  Before its first row a sequence has h0[b] (binary32[batch][d], NULL:
  * zeros), and its last h, in binary32, goes to state[b] (NULL: nowhere; h0[b] for

@@ -1,7 +1,25 @@
 // dgc_recurrence.hip -- a gated linear recurrence along sequences, and its
 // gradients.  See include/dgc.h for the contract of every function.
+//
+// Along a column both directions are c <- f c + u: forward c is h and u =
+// (1 - f) x; backward, over the rows from the last to the first, c is what a
+// row hands to the one before it, f g, and u = f dh.  Rows [a, b) together are
+// c <- A c + B with A the product of their f, so they can be worked on side by
+// side: the waves of a workgroup take kRows rows each, work out their A and B,
+// and after one exchange through LDS go over their rows (still in registers)
+// again with the c that comes in.  A row where a sequence begins takes its
+// initial value instead of what comes in, and says so beside A and B (a product
+// with 0 would not stop an infinity).
+//
+// A workgroup goes along a part of the rows in chunks of kWaves * kRows, the next
+// chunk's loads under way while it works on this one.  Where sequences of
+// equal length give enough parts, parts begin where sequences do and every
+// input is read once.  Else a first pass leaves A and B of each part, and
+// the second folds those before its part.
 #include <algorithm>
+#include <type_traits>
 
+#include "launch_grid.hpp"
 #include "tokens.hpp"
 
 using namespace dgc::tokens;
@@ -9,107 +27,504 @@ using namespace dgc::tokens;
 namespace {
 
 constexpr int kLanes = 64;
-constexpr int64_t kMostBlocks = 1 << 20;  // of a launch: workgroups take what is left in turn
+constexpr int kWaves = 16;
+constexpr int kThreads = kLanes * kWaves;
+constexpr int kRows = 8;                       // of a wave at a time
+constexpr int64_t kChunk = kWaves * kRows;     // rows of a workgroup at a time
+constexpr int64_t kShort = 4;                  // rows of a sequence, see run()
+constexpr int64_t kFill = 256;                 // workgroups that fill the card
+constexpr int64_t kMostBlocks = 1 << 20;       // of a launch: workgroups take what is left in turn
 
 struct Rows {
     int64_t m, d, batch;
     int wide_index;
-    const void* offsets;  // or null: m / batch rows each
+    const void* offsets;    // or null: m / batch rows each
+    uint32_t length;        // then, m / batch
+    const int32_t* owner;   // with offsets: each row's sequence, -1 for none
 };
 
-struct Forward {
-    Rows s;
-    const void* gate;
-    int64_t ldg;
-    const void* x;
-    int64_t ldx;
-    const float* h0;
-    int64_t ldh0;
-    void* h;
-    int64_t ldh;
-    float* state;
-    int64_t lds;
+// The parts that workgroups go along.
+struct Parts {
+    int64_t rows, count, strips;  // rows of a part, parts, strips of columns
+    int split;                    // whether sequences go from part to part
+    float* sums;                  // then [count][2][d]: A and B of each part
+    float* kept;                  // [count][d]: the initial value of the last sequence that begins in a part
+    int64_t* last;                // [count]: and that sequence's first row, or -1
 };
 
-struct Backward {
+struct Args {
     Rows s;
+    Parts p;
     const void* dh;
     int64_t lddh;
     const void* gate;
     int64_t ldg;
     const void* x;
     int64_t ldx;
-    const void* h;
+    const void* h;  // backward: as it was written
     int64_t ldh;
     const float* h0;
     int64_t ldh0;
-    const float* dstate;
-    int64_t ldds;
-    void* dgate;
-    int64_t lddg;
-    void* dx;
-    int64_t lddx;
-    float* dh0;
-    int64_t lddh0;
+    const float* init;  // forward h0, backward dstate
+    int64_t ldi;
+    float* final;       // forward state, backward dh0
+    int64_t ldf;
+    void* out;   // forward h, backward dx
+    int64_t ldo;
+    void* out2;  // backward dgate
+    int64_t ldo2;
 };
 
 // Where sequence b begins, within [0, m].
 __device__ __forceinline__ int64_t row_of(const Rows& s, int64_t b) {
-    if (!s.offsets) return s.m / s.batch * b;
     const int64_t r = s.wide_index ? static_cast<const int64_t*>(s.offsets)[b]
                                    : static_cast<const int32_t*>(s.offsets)[b];
     return r < 0 ? 0 : r > s.m ? s.m : r;
 }
 
-// f = sigmoid(z) and 1 - f, each accurate relative to itself.
+// f = sigmoid(z) and r = 1 - f, each accurate relative to itself: exp(-|z|) as a
+// power of 2, whose exponent's rounding is made good to first order, and a
+// reciprocal with one step of Newton's.
 __device__ __forceinline__ void gate_pair(float z, float& f, float& r) {
-    const float e = expf(-fabsf(z)), s = 1.0f / (1.0f + e);
-    f = z >= 0.0f ? s : e * s;
-    r = z >= 0.0f ? e * s : s;
-    if (z != z) f = r = z;
+    float a = -fabsf(z);
+    a = a < -150.0f ? -150.0f : a;  // (a NaN stays)
+    const float t = a * 1.44269502f;
+    const float rest = fmaf(a, 1.44269502f, -t) + a * 1.92596303e-8f;
+    float e = __builtin_amdgcn_exp2f(t);
+    e = fmaf(e, rest * 0.693147182f, e);
+    const float one = 1.0f + e;
+    float s = __builtin_amdgcn_rcpf(one);
+    s = fmaf(fmaf(-one, s, 1.0f), s, s);
+    const float small = e * s;
+    f = z >= 0.0f ? s : small;
+    r = z >= 0.0f ? small : s;
 }
 
-// A lane per column and sequence, row by row.
-template <class T>
-__global__ __launch_bounds__(kLanes) void k_forward(Forward a, int64_t strips) {
-    const int64_t tasks = a.s.batch * strips;
-    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const int64_t b = task / strips, c = task % strips * kLanes + threadIdx.x;
-        if (c >= a.s.d) continue;
-        float h = a.h0 ? a.h0[b * a.ldh0 + c] : 0.0f;
-        const int64_t end = row_of(a.s, b + 1);
-        for (int64_t t = row_of(a.s, b); t < end; ++t) {
-            float f, r;
-            gate_pair(float(static_cast<const T*>(a.gate)[t * a.ldg + c]), f, r);
-            h = f * h + r * float(static_cast<const T*>(a.x)[t * a.ldx + c]);
-            static_cast<T*>(a.h)[t * a.ldh + c] = T(h);
+template <class T, int C>
+struct Some {
+    T t[C];
+};
+
+// A workgroup's columns: `base` is the first lane's first one, the same for a
+// whole wave, as rows are, so that an address is a scalar and a lane's small part.
+struct Columns {
+    int64_t base;
+    uint32_t lane;  // a lane's first column behind that
+    bool mine;      // not a copy of another lane's, behind the last column
+};
+
+template <int C>
+__device__ __forceinline__ Columns columns_of(int64_t d, int64_t strip) {
+    Columns c;
+    c.base = strip * kLanes * C;
+    const uint32_t lane = (threadIdx.x & 63) * C;
+    c.mine = c.base + lane < d;
+    c.lane = c.mine ? lane : uint32_t(d - C - c.base);
+    return c;
+}
+
+template <class T, int C>
+struct __attribute__((packed, aligned(sizeof(T) == 2 ? 2 : 4), may_alias)) Packed {
+    T t[C];
+};
+
+// C columns of a row, at any address that an element can have.
+template <class T, int C>
+__device__ __forceinline__ Some<T, C> get(const void* p, int64_t at, const Columns& c) {
+    const T* const base = static_cast<const T*>(p) + (at + c.base);
+    Some<T, C> s;
+    __builtin_memcpy(&s, reinterpret_cast<const Packed<T, C>*>(base + c.lane), sizeof(s));
+    return s;
+}
+
+template <class T, int C>
+__device__ __forceinline__ void put(void* p, int64_t at, const Columns& c, const float* v) {
+    Packed<T, C> s;
+#pragma unroll
+    for (int i = 0; i < C; ++i) s.t[i] = T(v[i]);
+    *reinterpret_cast<Packed<T, C>*>(static_cast<T*>(p) + (at + c.base) + c.lane) = s;
+}
+
+// ... of a matrix in binary32.
+template <int C>
+__device__ __forceinline__ void get_wide(const float* p, int64_t at, const Columns& c, float* v) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = p[at + c.base + c.lane + i];
+}
+
+template <int C>
+__device__ __forceinline__ void put_wide(float* p, int64_t at, const Columns& c, const float* v) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) p[at + c.base + c.lane + i] = v[i];
+}
+
+// Rows in the order of the recurrence: backward from the last to the first.
+template <bool BACK>
+__device__ __forceinline__ int64_t row(const Args& a, int64_t v) {
+    return BACK ? a.s.m - 1 - v : v;
+}
+
+template <bool BACK>
+__device__ __forceinline__ int32_t owner(const Args& a, int64_t v) {
+    if (v < 0 || v >= a.s.m) return -1;
+    const int64_t r = row<BACK>(a, v);
+    return a.s.owner ? a.s.owner[r] : int32_t(uint32_t(r) / a.s.length);
+}
+
+// What a wave's rows v0 .. v0 + kRows - 1, as far as they lie before `end`, are.
+struct Marks {
+    uint32_t inside, first, last;  // of any sequence; in the order of the recurrence its first, its last
+    int32_t own;                   // lane i + 1: row i's sequence
+    __device__ int32_t sequence(int i) const { return __builtin_amdgcn_readlane(own, i + 1); }
+};
+
+template <bool BACK>
+__device__ __forceinline__ Marks marks(const Args& a, int64_t v0, int64_t end) {
+    const int lane = threadIdx.x & 63;
+    Marks k;
+    k.own = lane < kRows + 2 ? owner<BACK>(a, v0 - 1 + lane) : -1;
+    const int32_t before = __shfl(k.own, (lane + 63) & 63), behind = __shfl(k.own, (lane + 1) & 63);
+    const bool mine = lane >= 1 && lane <= kRows && v0 - 1 + lane < end && k.own >= 0;
+    k.inside = uint32_t(__ballot(mine) >> 1);
+    k.first = uint32_t(__ballot(mine && before != k.own) >> 1);
+    k.last = uint32_t(__ballot(mine && behind != k.own) >> 1);
+    return k;
+}
+
+// A wave's rows as they are in memory: what A and B are made of.
+template <class T, int C, bool BACK>
+struct Raw {
+    Some<T, C> gate[kRows], in[kRows];  // in: x, backward dh
+    Marks k;
+};
+
+// What the backward pass needs beside that, once it knows what comes in: x, and
+// h of the row before.
+template <class T, int C, bool BACK>
+struct Late {
+    Some<T, C> x[BACK ? kRows : 1], h[BACK ? kRows : 1];
+};
+
+template <class T, int C, bool BACK>
+__device__ __forceinline__ void fetch_late(const Args& a, int64_t v0, int64_t end, const Columns& c, Late<T, C, BACK>& q) {
+    if constexpr (BACK) {
+        if (v0 >= end) return;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t v = v0 + i < end ? v0 + i : end - 1, r = row<BACK>(a, v);
+            q.x[i] = get<T, C>(a.x, r * a.ldx, c);
+            q.h[i] = get<T, C>(a.h, (r > 0 ? r - 1 : 0) * a.ldh, c);
         }
-        if (a.state) a.state[b * a.lds + c] = h;
     }
 }
 
-template <class T>
-__global__ __launch_bounds__(kLanes) void k_backward(Backward a, int64_t strips) {
-    const int64_t tasks = a.s.batch * strips;
-    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-        const int64_t b = task / strips, c = task % strips * kLanes + threadIdx.x;
-        if (c >= a.s.d) continue;
-        float after = a.dstate ? a.dstate[b * a.ldds + c] : 0.0f;
-        const int64_t begin = row_of(a.s, b);
-        for (int64_t t = row_of(a.s, b + 1) - 1; t >= begin; --t) {
-            float f, r;
-            gate_pair(float(static_cast<const T*>(a.gate)[t * a.ldg + c]), f, r);
-            const float x = float(static_cast<const T*>(a.x)[t * a.ldx + c]);
-            const float h = t > begin ? float(static_cast<const T*>(a.h)[(t - 1) * a.ldh + c])
-                                      : a.h0 ? a.h0[b * a.ldh0 + c] : 0.0f;
-            const float g = float(static_cast<const T*>(a.dh)[t * a.lddh + c]) + after;
-            if (a.dx) static_cast<T*>(a.dx)[t * a.lddx + c] = T(r * g);
-            if (a.dgate) static_cast<T*>(a.dgate)[t * a.lddg + c] = T(g * (h - x) * (f * r));
-            after = f * g;
-        }
-        if (a.dh0) a.dh0[b * a.lddh0 + c] = after;
+template <class T, int C, bool BACK>
+__device__ __forceinline__ void fetch(const Args& a, int64_t v0, int64_t end, const Columns& c, Raw<T, C, BACK>& q) {
+    if (v0 >= end) {
+        q.k.inside = q.k.first = q.k.last = 0;
+        return;
+    }
+    q.k = marks<BACK>(a, v0, end);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t v = v0 + i < end ? v0 + i : end - 1, r = row<BACK>(a, v);
+        q.gate[i] = get<T, C>(a.gate, r * a.ldg, c);
+        q.in[i] = BACK ? get<T, C>(a.dh, r * a.lddh, c) : get<T, C>(a.x, r * a.ldx, c);
     }
 }
+
+template <int C>
+__device__ __forceinline__ void state_of(const float* p, int64_t ld, int32_t sequence, const Columns& c, float* v) {
+    if (p) {
+        get_wide<C>(p, int64_t(sequence) * ld, c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = 0.0f;
+    }
+}
+
+// (r: forward u = (1 - f) x, backward 1 - f.)
+//
+// A and B of a wave's rows; whether a sequence begins among them, and the last
+// such one's initial value.
+template <int C>
+struct Sum {
+    float A[C], B[C], kept[C];
+    bool fresh;
+};
+
+template <class T, int C, bool BACK>
+__device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK>& q, int64_t v0, const Columns& c, int64_t kept_row,
+                                         const float* kept, Sum<C>& s, float (*f)[C], float (*r)[C]) {
+    const auto step = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            gate_pair(float(q.gate[i].t[j]), f[i][j], r[i][j]);
+            const float in = float(q.in[i].t[j]);
+            if (!BACK) r[i][j] *= in;
+            s.B[j] = BACK ? f[i][j] * (s.B[j] + in) : fmaf(f[i][j], s.B[j], r[i][j]);
+            s.A[j] *= f[i][j];
+        }
+    };
+    if (q.k.inside == (1u << kRows) - 1 && q.k.first == 0) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) step(i);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (!(q.k.inside >> i & 1)) continue;
+        if (q.k.first >> i & 1) {
+            if (v0 + i == kept_row) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) s.kept[j] = kept[j];
+            } else {
+                state_of<C>(a.init, a.ldi, q.k.sequence(i), c, s.kept);
+            }
+#pragma unroll
+            for (int j = 0; j < C; ++j) s.B[j] = s.kept[j];
+            s.fresh = true;
+        }
+        step(i);
+    }
+}
+
+template <int C>
+__device__ __forceinline__ void clear(Sum<C>& s) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        s.A[j] = 1.0f;
+        s.B[j] = s.kept[j] = 0.0f;
+    }
+    s.fresh = false;
+}
+
+// A and B of each part but the last: a wave takes its share of the part's rows
+// in a row.
+template <class T, int C, bool BACK>
+__global__ __launch_bounds__(kThreads) void k_parts(Args a) {
+    __shared__ float sum[kWaves][3][kLanes * C];
+    __shared__ int64_t began[kWaves];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t block = dgc::block_number(), part = block / a.p.strips, strip = block % a.p.strips;
+    if (part >= a.p.count - 1) return;
+    const Columns c = columns_of<C>(a.s.d, strip);
+    const int64_t share = a.p.rows / kWaves;  // a part's rows are a multiple of a chunk's
+    const int64_t begin = part * a.p.rows + wave * share, end = begin + share;
+    Sum<C> s;
+    clear(s);
+    int64_t last = -1;
+    Raw<T, C, BACK> q, next;
+    fetch<T, C, BACK>(a, begin, end, c, q);
+    for (int64_t v = begin; v < end; v += kRows) {
+        fetch<T, C, BACK>(a, v + kRows, end, c, next);
+        float f[kRows][C], r[kRows][C];
+        add_rows<T, C, BACK>(a, q, v, c, -1, nullptr, s, f, r);
+        if (q.k.first) last = v + 31 - __builtin_clz(q.k.first);
+        q = next;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        sum[wave][0][lane * C + j] = s.A[j];
+        sum[wave][1][lane * C + j] = s.B[j];
+        sum[wave][2][lane * C + j] = s.kept[j];
+    }
+    if (lane == 0) began[wave] = last;
+    __syncthreads();
+    if (wave != 0) return;
+    clear(s);
+    last = -1;
+    for (int w = 0; w < kWaves; ++w) {
+        const int64_t first = began[w];
+        if (first >= 0) last = first;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const float A = sum[w][0][lane * C + j], B = sum[w][1][lane * C + j];
+            s.B[j] = first >= 0 ? B : fmaf(A, s.B[j], B);
+            s.A[j] *= A;
+            if (first >= 0) s.kept[j] = sum[w][2][lane * C + j];
+        }
+    }
+    if (c.mine) {
+        put_wide<C>(a.p.sums, part * 2 * a.s.d, c, s.A);
+        put_wide<C>(a.p.sums, (part * 2 + 1) * a.s.d, c, s.B);
+        put_wide<C>(a.p.kept, part * a.s.d, c, s.kept);
+    }
+    if (lane == 0) a.p.last[part * a.p.strips + strip] = last;
+}
+
+template <class T, int C, bool BACK>
+__global__ __launch_bounds__(kThreads) void k_along(Args a) {
+    __shared__ float sum[2][kWaves][2][kLanes * C];
+    __shared__ int fresh[2][kWaves];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t block = dgc::block_number(), part = block / a.p.strips, strip = block % a.p.strips;
+    if (part >= a.p.count) return;
+    const Columns c = columns_of<C>(a.s.d, strip);
+    const int64_t begin = part * a.p.rows, end = begin + a.p.rows < a.s.m ? begin + a.p.rows : a.s.m;
+    Raw<T, C, BACK> q, next;
+    fetch<T, C, BACK>(a, begin + wave * kRows, end, c, q);
+    float carry[C] = {}, kept[C] = {};
+    int64_t kept_row = -1;
+    if (a.p.split) {
+        for (int64_t p = 0; p < part; ++p) {
+            const bool began = a.p.last[p * a.p.strips + strip] >= 0;
+            float A[C], B[C];
+            get_wide<C>(a.p.sums, p * 2 * a.s.d, c, A);
+            get_wide<C>(a.p.sums, (p * 2 + 1) * a.s.d, c, B);
+#pragma unroll
+            for (int j = 0; j < C; ++j) carry[j] = began ? B[j] : fmaf(A[j], carry[j], B[j]);
+        }
+        // (of the last part no sequence goes on)
+        if (part < a.p.count - 1) {
+            kept_row = a.p.last[part * a.p.strips + strip];
+            get_wide<C>(a.p.kept, part * a.s.d, c, kept);
+        }
+    }
+    int turn = 0;
+    for (int64_t base = begin; base < end; base += kChunk, turn ^= 1) {
+        const int64_t v0 = base + wave * kRows;
+        Late<T, C, BACK> late;
+        fetch_late<T, C, BACK>(a, v0, end, c, late);
+        fetch<T, C, BACK>(a, v0 + kChunk, end, c, next);
+        Sum<C> s;
+        clear(s);
+        float f[kRows][C], r[kRows][C];
+        add_rows<T, C, BACK>(a, q, v0, c, kept_row, kept, s, f, r);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            sum[turn][wave][0][lane * C + j] = s.A[j];
+            sum[turn][wave][1][lane * C + j] = s.B[j];
+        }
+        if (lane == 0) fresh[turn][wave] = s.fresh;
+        __syncthreads();
+        float now[C];
+#pragma unroll 4
+        for (int w = 0; w < kWaves; ++w) {
+            const bool began = fresh[turn][w];
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                if (w == wave) now[j] = carry[j];
+                const float A = sum[turn][w][0][lane * C + j], B = sum[turn][w][1][lane * C + j];
+                carry[j] = began ? B : fmaf(A, carry[j], B);
+            }
+        }
+        const auto step = [&](int i, bool first, bool last) {
+            float y[C], z[C], start[C];
+            if (first) {
+                // the last one's initial value is at hand: it may have been overwritten by the rows behind
+                if (q.k.first >> i == 1) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) now[j] = s.kept[j];
+                } else {
+                    state_of<C>(a.init, a.ldi, q.k.sequence(i), c, now);
+                }
+            }
+            const int32_t sequence = last ? q.k.sequence(i) : 0;
+            if (BACK && last) state_of<C>(a.h0, a.ldh0, sequence, c, start);
+            const int64_t at = row<BACK>(a, v0 + i);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                if constexpr (BACK) {
+                    const float g = float(q.in[i].t[j]) + now[j], h = last ? start[j] : float(late.h[i].t[j]);
+                    y[j] = r[i][j] * g;
+                    z[j] = g * (h - float(late.x[i].t[j])) * (f[i][j] * r[i][j]);
+                    now[j] = f[i][j] * g;
+                } else {
+                    now[j] = fmaf(f[i][j], now[j], r[i][j]);
+                    y[j] = now[j];
+                }
+            }
+            if (!c.mine) return;
+            if (!BACK || a.out) put<T, C>(a.out, at * a.ldo, c, y);
+            if (BACK && a.out2) put<T, C>(a.out2, at * a.ldo2, c, z);
+            if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
+        };
+        if (q.k.inside == (1u << kRows) - 1 && (q.k.first | q.k.last) == 0) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) step(i, false, false);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (q.k.inside >> i & 1) step(i, q.k.first >> i & 1, q.k.last >> i & 1);
+        }
+        q = next;
+    }
+}
+
+// Short sequences of equal length: a lane goes along 8 columns of one, row by
+// row.
+template <class T, bool BACK>
+__global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans, int64_t tasks) {
+    const int tx = threadIdx.x & (across - 1), ty = threadIdx.x / across, each = 256 / across;
+    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const int64_t b = task / spans * each + ty, c = (task % spans * across + tx) * kRow;
+        const int valid = valid_of(a.s.d, c);
+        if (b >= a.s.batch || valid == 0) continue;
+        const int64_t begin = b * a.s.length;
+        float now[kRow] = {};
+        if (a.init) load8(a.init + b * a.ldi + c, valid, now);
+        for (int64_t i = 0; i < a.s.length; ++i) {
+            const int64_t t = BACK ? begin + a.s.length - 1 - i : begin + i;
+            float z[kRow], in[kRow], x[kRow], h[kRow] = {};
+            load8(static_cast<const T*>(a.gate) + t * a.ldg + c, valid, z);
+            load8(BACK ? static_cast<const T*>(a.dh) + t * a.lddh + c : static_cast<const T*>(a.x) + t * a.ldx + c, valid,
+                  in);
+            if (BACK) {
+                load8(static_cast<const T*>(a.x) + t * a.ldx + c, valid, x);
+                if (t > begin)
+                    load8(static_cast<const T*>(a.h) + (t - 1) * a.ldh + c, valid, h);
+                else if (a.h0)
+                    load8(a.h0 + b * a.ldh0 + c, valid, h);
+            }
+#pragma unroll
+            for (int j = 0; j < kRow; ++j) {
+                float f, r;
+                gate_pair(z[j], f, r);
+                if (BACK) {
+                    const float g = in[j] + now[j];
+                    z[j] = g * (h[j] - x[j]) * (f * r);
+                    x[j] = r * g;
+                    now[j] = f * g;
+                } else {
+                    now[j] = fmaf(f, now[j], r * in[j]);
+                    x[j] = now[j];
+                }
+            }
+            if (!BACK || a.out) store8(static_cast<T*>(a.out) + t * a.ldo + c, valid, x);
+            if (BACK && a.out2) store8(static_cast<T*>(a.out2) + t * a.ldo2 + c, valid, z);
+        }
+        if (a.final) store8(a.final + b * a.ldf + c, valid, now);
+    }
+}
+
+// Each row's sequence: the last one that does not begin behind it, if it
+// reaches it.  And the initial values of empty sequences are their final ones.
+__global__ __launch_bounds__(256) void k_owner(Rows s, int32_t* owner, const float* init, int64_t ldi, float* final,
+                                               int64_t ldf) {
+    const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+    if (s.offsets)
+        for (int64_t r = first; r < s.m; r += step) {
+            int64_t lo = 0, n = s.batch + 1;
+            while (n > 0) {
+                const int64_t half = n / 2;
+                if (row_of(s, lo + half) <= r) {
+                    lo += half + 1;
+                    n -= half + 1;
+                } else {
+                    n = half;
+                }
+            }
+            owner[r] = lo > 0 && lo <= s.batch && r < row_of(s, lo) ? int32_t(lo - 1) : -1;
+        }
+    if (!final) return;
+    for (int64_t b = blockIdx.x; b < s.batch; b += gridDim.x)
+        if (!s.offsets || row_of(s, b) >= row_of(s, b + 1))
+            for (int64_t c = threadIdx.x; c < s.d; c += 256)
+                final[b * ldf + c] = init ? init[b * ldi + c] : 0.0f;
+}
+
+// ---------------------------------------------------------------------- host
 
 bool rows_ok(int64_t type, int64_t index_type, int64_t m, int64_t d, int64_t batch, const void* offsets) {
     if (!type_ok(type) || !side_ok(m) || !side_ok(d) || !side_ok(batch)) return false;
@@ -117,7 +532,100 @@ bool rows_ok(int64_t type, int64_t index_type, int64_t m, int64_t d, int64_t bat
     return batch == 0 ? m == 0 : m % batch == 0;
 }
 
-dim3 grid(int64_t tasks) { return dim3(unsigned(std::min(tasks, kMostBlocks))); }
+int64_t strips_of(int64_t d, int columns) { return cdiv(d, kLanes * columns); }
+
+// Parts of whole chunks that fill the card.
+int64_t part_rows(int64_t m, int64_t strips) {
+    return std::max<int64_t>(cdiv(cdiv(m * strips, kFill), kChunk), 1) * kChunk;
+}
+
+struct Plan {
+    int columns;  // of a lane
+    Parts p{};
+};
+
+// most: columns that a lane may have.
+Plan plan(int64_t m, int64_t d, int64_t batch, bool even, int most) {
+    Plan k;
+    if (d % 2 != 0) most = 1;
+    // sequences of equal length, as many in a part as fill the card
+    if (even)
+        for (int columns = most; columns > 0; --columns) {
+            const int64_t strips = strips_of(d, columns), length = m / batch;
+            const int64_t rows = std::max<int64_t>(part_rows(m, strips) / length, 1) * length;
+            k.columns = columns;
+            k.p.rows = rows;
+            k.p.strips = strips;
+            k.p.count = cdiv(m, rows);
+            if (k.p.count * strips >= kFill || m <= kChunk) return k;
+        }
+    if (even && k.p.count * k.p.strips >= kFill / 2) return k;
+    k.columns = most;
+    k.p.strips = strips_of(d, k.columns);
+    k.p.rows = part_rows(m, k.p.strips);
+    k.p.count = cdiv(m, k.p.rows);
+    k.p.split = k.p.count > 1;
+    return k;
+}
+
+struct Space {
+    size_t owner, sums, kept, last, total;
+};
+
+Space space(int64_t m, int64_t d) {
+    Space s{};
+    int64_t parts = 0, strips = strips_of(d, 1);
+    for (int columns = 1; columns <= 2; ++columns)
+        parts = std::max(parts, cdiv(m, part_rows(m, strips_of(d, columns))));
+    s.owner = 0;
+    s.sums = round_up(size_t(m) * 4);
+    s.kept = s.sums + round_up(size_t(parts) * 2 * size_t(d) * 4);
+    s.last = s.kept + round_up(size_t(parts) * size_t(d) * 4);
+    s.total = s.last + round_up(size_t(parts) * size_t(strips) * 8);
+    return s;
+}
+
+template <bool BACK>
+int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
+    int32_t* const owner = reinterpret_cast<int32_t*>(ws + sp.owner);
+    if (a.s.offsets || a.s.m == 0) {
+        const int64_t blocks = std::max(cdiv(a.s.m, 256), std::min<int64_t>(a.s.batch, 1024));
+        k_owner<<<dim3(unsigned(std::min(blocks, kMostBlocks))), 256, 0, stream>>>(a.s, owner, a.init, a.ldi, a.final,
+                                                                                    a.ldf);
+        if (a.s.m == 0) return launched();
+    }
+    a.s.length = uint32_t(a.s.offsets ? 1 : a.s.m / a.s.batch);
+    if (!a.s.offsets && a.s.length <= kShort) {
+        int across = 256;
+        while (across > 1 && across / 2 * kRow >= a.s.d) across /= 2;
+        const int64_t spans = cdiv(a.s.d, int64_t(across) * kRow), tasks = spans * cdiv(a.s.batch, 256 / across);
+        return with_type(type, [&](auto t) {
+            k_short<decltype(t), BACK>
+                <<<dim3(unsigned(std::min(tasks, kMostBlocks))), 256, 0, stream>>>(a, across, spans, tasks);
+            return launched();
+        });
+    }
+    // (two columns of the backward pass or of binary32 do not fit a lane's registers)
+    const Plan k = plan(a.s.m, a.s.d, a.s.batch, !a.s.offsets, !BACK && type != DGC_FP32 ? 2 : 1);
+    a.p = k.p;
+    a.p.sums = reinterpret_cast<float*>(ws + sp.sums);
+    a.p.kept = reinterpret_cast<float*>(ws + sp.kept);
+    a.p.last = reinterpret_cast<int64_t*>(ws + sp.last);
+    a.s.owner = a.s.offsets ? owner : nullptr;
+    const auto with = [&](auto t, auto columns) {
+        typedef decltype(t) T;
+        constexpr int C = decltype(columns)::value;
+        if (a.p.split)
+            k_parts<T, C, BACK><<<dgc::grid_of((a.p.count - 1) * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        k_along<T, C, BACK><<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        return launched();
+    };
+    return with_type(type, [&](auto t) {
+        if constexpr (!BACK && sizeof(t) == 2)
+            if (k.columns == 2) return with(t, std::integral_constant<int, 2>());
+        return with(t, std::integral_constant<int, 1>());
+    });
+}
 
 }  // namespace
 
@@ -125,7 +633,7 @@ extern "C" {
 
 int dgc_recurrence_workspace_bytes(int64_t m, int64_t d, int64_t batch, int32_t, size_t* bytes) {
     if (!bytes || !side_ok(m) || !side_ok(d) || !side_ok(batch) || (d > 0 && m > kMostArea / d)) return DGC_EINVAL;
-    *bytes = 0;
+    *bytes = m > 0 && d > 0 && batch > 0 ? space(m, d).total : 0;
     return DGC_OK;
 }
 
@@ -135,16 +643,20 @@ int dgc_recurrence(const dgc_recurrence_args* a, void* workspace, size_t workspa
     const int size = size_of(a->type);
     if (!mat_ok(a->gate, a->ldg, m, d, size) || !mat_ok(a->x, a->ldx, m, d, size) ||
         !optional_ok(a->h0, a->ldh0, n, d, 4) || !mat_ok(a->h, a->ldh, m, d, size) ||
-        !optional_ok(a->state, a->lds, n, d, 4))
+        !optional_ok(a->state, a->lds, n, d, 4) || (d > 0 && m > kMostArea / d))
         return DGC_EINVAL;
     if (n == 0 || d == 0) return DGC_OK;
-    const Forward f{{m, d, n, a->index_type == DGC_INT64, a->offsets}, a->gate, a->ldg, a->x, a->ldx, a->h0, a->ldh0,
-                    a->h, a->ldh, a->state, a->lds};
-    const int64_t strips = cdiv(d, kLanes);
-    return with_type(a->type, [&](auto t) {
-        k_forward<decltype(t)><<<grid(n * strips), kLanes, 0, stream>>>(f, strips);
-        return launched();
-    });
+    const Space sp = space(m, d);
+    const int rc = space_ok(workspace, workspace_bytes, m > 0 ? sp.total : 0);
+    if (rc != DGC_OK) return rc;
+    Args k{};
+    k.s = {m, d, n, a->index_type == DGC_INT64, a->offsets, 0, nullptr};
+    k.gate = a->gate, k.ldg = a->ldg;
+    k.x = a->x, k.ldx = a->ldx;
+    k.init = a->h0, k.ldi = a->ldh0;
+    k.final = a->state, k.ldf = a->lds;
+    k.out = a->h, k.ldo = a->ldh;
+    return run<false>(a->type, k, static_cast<char*>(workspace), sp, stream);
 }
 
 int dgc_recurrence_backward(const dgc_recurrence_backward_args* a, void* workspace, size_t workspace_bytes,
@@ -156,17 +668,24 @@ int dgc_recurrence_backward(const dgc_recurrence_backward_args* a, void* workspa
         !mat_ok(a->x, a->ldx, m, d, size) || !mat_ok(a->h, a->ldh, m, d, size) ||
         !optional_ok(a->h0, a->ldh0, n, d, 4) || !optional_ok(a->dstate, a->ldds, n, d, 4) ||
         !optional_ok(a->dgate, a->lddg, m, d, size) || !optional_ok(a->dx, a->lddx, m, d, size) ||
-        !optional_ok(a->dh0, a->lddh0, n, d, 4))
+        !optional_ok(a->dh0, a->lddh0, n, d, 4) || (d > 0 && m > kMostArea / d))
         return DGC_EINVAL;
     if (n == 0 || d == 0) return DGC_OK;
-    const Backward b{{m, d, n, a->index_type == DGC_INT64, a->offsets}, a->dh, a->lddh, a->gate, a->ldg, a->x, a->ldx,
-                     a->h, a->ldh, a->h0, a->ldh0, a->dstate, a->ldds, a->dgate, a->lddg, a->dx, a->lddx, a->dh0,
-                     a->lddh0};
-    const int64_t strips = cdiv(d, kLanes);
-    return with_type(a->type, [&](auto t) {
-        k_backward<decltype(t)><<<grid(n * strips), kLanes, 0, stream>>>(b, strips);
-        return launched();
-    });
+    const Space sp = space(m, d);
+    const int rc = space_ok(workspace, workspace_bytes, m > 0 ? sp.total : 0);
+    if (rc != DGC_OK) return rc;
+    Args k{};
+    k.s = {m, d, n, a->index_type == DGC_INT64, a->offsets, 0, nullptr};
+    k.dh = a->dh, k.lddh = a->lddh;
+    k.gate = a->gate, k.ldg = a->ldg;
+    k.x = a->x, k.ldx = a->ldx;
+    k.h = a->h, k.ldh = a->ldh;
+    k.h0 = a->h0, k.ldh0 = a->ldh0;
+    k.init = a->dstate, k.ldi = a->ldds;
+    k.final = a->dh0, k.ldf = a->lddh0;
+    k.out = a->dx, k.ldo = a->lddx;
+    k.out2 = a->dgate, k.ldo2 = a->lddg;
+    return run<true>(a->type, k, static_cast<char*>(workspace), sp, stream);
 }
 
 }  // extern "C"
