@@ -82,28 +82,28 @@ __device__ __forceinline__ int64_t row_of(const Rows& s, int64_t b) {
     return r < 0 ? 0 : r > s.m ? s.m : r;
 }
 
-// f = sigmoid(z) and r = 1 - f, each accurate relative to itself: exp(-|z|) as a
-// power of 2, whose exponent's rounding is made good to first order, and a
-// reciprocal with one step of Newton's.
+// f = sigmoid(z) = 1 / (1 + E) and r = 1 - f = E f, E = exp(-z) as a power of 2.
+// The exponent's rounding makes E off by |z| 2^-24 of itself, which for 16-bit
+// rows is far below the rounding of what is stored, and moves h by as much at
+// most, however long its memory (f is off by r of that).  For binary32 rows it is
+// made good to first order, and the reciprocal gets one step of Newton's.  Where E
+// would leave the range f is below 2^-125 and counts as 0.  A NaN stays.
+template <bool EXACT>
 __device__ __forceinline__ void gate_pair(float z, float& f, float& r) {
-    float a = -fabsf(z);
-    a = a < -150.0f ? -150.0f : a;  // (a NaN stays)
-    const float t = a * 1.44269502f;
-    const float rest = fmaf(a, 1.44269502f, -t) + a * 1.92596303e-8f;
+    float t = z * -1.44269502f;
+    const bool none = t > 125.0f;
+    t = none ? 125.0f : t;
     float e = __builtin_amdgcn_exp2f(t);
-    e = fmaf(e, rest * 0.693147182f, e);
+    if constexpr (EXACT) {
+        const float rest = fmaf(z, -1.92596303e-8f, fmaf(z, -1.44269502f, -t));
+        e = none ? e : fmaf(e, rest * 0.693147182f, e);
+    }
     const float one = 1.0f + e;
     float s = __builtin_amdgcn_rcpf(one);
-    s = fmaf(fmaf(-one, s, 1.0f), s, s);
-    const float small = e * s;
-    f = z >= 0.0f ? s : small;
-    r = z >= 0.0f ? small : s;
+    if constexpr (EXACT) s = fmaf(fmaf(-one, s, 1.0f), s, s);
+    r = e * s;
+    f = none ? 0.0f : s;
 }
-
-template <class T, int C>
-struct Some {
-    T t[C];
-};
 
 // A workgroup's columns: `base` is the first lane's first one, the same for a
 // whole wave, as rows are, so that an address is a scalar and a lane's small part.
@@ -123,26 +123,47 @@ __device__ __forceinline__ Columns columns_of(int64_t d, int64_t strip) {
     return c;
 }
 
+// C columns of a row, 32 bits in all or 16 in a register of their own (two rows'
+// halves in one register would have to wait for each other).
 template <class T, int C>
-struct __attribute__((packed, aligned(sizeof(T) == 2 ? 2 : 4), may_alias)) Packed {
-    T t[C];
+struct Some {
+    static_assert(sizeof(T) * C <= 4, "a register");
+    uint32_t bits;
+    __device__ float at(int j) const {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(float, bits);
+        else
+            return float(__builtin_bit_cast(T, uint16_t(j ? bits >> 16 : bits & 0xFFFF)));
+    }
 };
 
-// C columns of a row, at any address that an element can have.
+typedef uint16_t Half __attribute__((may_alias));
+typedef uint32_t Word2 __attribute__((aligned(2), may_alias));
+
 template <class T, int C>
 __device__ __forceinline__ Some<T, C> get(const void* p, int64_t at, const Columns& c) {
-    const T* const base = static_cast<const T*>(p) + (at + c.base);
-    Some<T, C> s;
-    __builtin_memcpy(&s, reinterpret_cast<const Packed<T, C>*>(base + c.lane), sizeof(s));
-    return s;
+    const char* const q = reinterpret_cast<const char*>(static_cast<const T*>(p) + (at + c.base)) +
+                          uint64_t(uint32_t(c.lane * sizeof(T)));
+    if constexpr (sizeof(T) * C == 2)
+        return {*reinterpret_cast<const Half*>(q)};
+    else
+        return {*reinterpret_cast<const Word2*>(q)};
 }
 
 template <class T, int C>
 __device__ __forceinline__ void put(void* p, int64_t at, const Columns& c, const float* v) {
-    Packed<T, C> s;
+    char* const q =
+        reinterpret_cast<char*>(static_cast<T*>(p) + (at + c.base)) + uint64_t(uint32_t(c.lane * sizeof(T)));
+    T t[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) s.t[i] = T(v[i]);
-    *reinterpret_cast<Packed<T, C>*>(static_cast<T*>(p) + (at + c.base) + c.lane) = s;
+    for (int i = 0; i < C; ++i) t[i] = T(v[i]);
+    if constexpr (sizeof(T) * C == 2) {
+        *reinterpret_cast<Half*>(q) = __builtin_bit_cast(uint16_t, t[0]);
+    } else {
+        uint32_t w;
+        __builtin_memcpy(&w, t, 4);
+        *reinterpret_cast<Word2*>(q) = w;
+    }
 }
 
 // ... of a matrix in binary32.
@@ -158,17 +179,38 @@ __device__ __forceinline__ void put_wide(float* p, int64_t at, const Columns& c,
     for (int i = 0; i < C; ++i) p[at + c.base + c.lane + i] = v[i];
 }
 
-// Rows in the order of the recurrence: backward from the last to the first.
-template <bool BACK>
-__device__ __forceinline__ int64_t row(const Args& a, int64_t v) {
-    return BACK ? a.s.m - 1 - v : v;
-}
+// Rows in the order of the recurrence: backward from the last to the first.  (32
+// bits without a sign, which a matrix's end and a chunk do not leave: the scalar
+// unit compares no 64 bits, and a row that is not a scalar costs ten vector
+// instructions for each address.)
+typedef uint32_t Row;
 
 template <bool BACK>
+__device__ __forceinline__ Row row(const Args& a, Row v) {
+    return BACK ? Row(a.s.m) - 1 - v : v;
+}
+
+// A row's sequence.  (v: from -1 up to m and beyond.  EVEN, for equally long ones, is
+// known when it is compiled: a register that a load may still be on its way into
+// would be waited for.)
+template <bool BACK, bool EVEN>
 __device__ __forceinline__ int32_t owner(const Args& a, int64_t v) {
     if (v < 0 || v >= a.s.m) return -1;
-    const int64_t r = row<BACK>(a, v);
-    return a.s.owner ? a.s.owner[r] : int32_t(uint32_t(r) / a.s.length);
+    const Row r = row<BACK>(a, Row(v));
+    return EVEN ? int32_t(r / a.s.length) : a.s.owner[r];
+}
+
+// A workgroup's part and strip of columns.
+struct Place {
+    uint32_t part, strip;
+};
+
+__device__ __forceinline__ Place place(const Args& a) {
+    const uint32_t block = uint32_t(dgc::block_number()), part = block / uint32_t(a.p.strips);
+    Place w;
+    w.part = __builtin_amdgcn_readfirstlane(part);
+    w.strip = __builtin_amdgcn_readfirstlane(block - part * uint32_t(a.p.strips));
+    return w;
 }
 
 // What a wave's rows v0 .. v0 + kRows - 1, as far as they lie before `end`, are.
@@ -176,18 +218,20 @@ struct Marks {
     uint32_t inside, first, last;  // of any sequence; in the order of the recurrence its first, its last
     int32_t own;                   // lane i + 1: row i's sequence
     __device__ int32_t sequence(int i) const { return __builtin_amdgcn_readlane(own, i + 1); }
+    // rows of a sequence that began before them and goes on behind them
+    __device__ bool plain() const { return inside == (1u << kRows) - 1 && (first | last) == 0; }
 };
 
-template <bool BACK>
-__device__ __forceinline__ Marks marks(const Args& a, int64_t v0, int64_t end) {
+// own: lane i + 1 holds row i's sequence, for i from -1 to kRows.
+__device__ __forceinline__ Marks marks(int32_t own, Row v0, Row end) {
     const int lane = threadIdx.x & 63;
     Marks k;
-    k.own = lane < kRows + 2 ? owner<BACK>(a, v0 - 1 + lane) : -1;
-    const int32_t before = __shfl(k.own, (lane + 63) & 63), behind = __shfl(k.own, (lane + 1) & 63);
-    const bool mine = lane >= 1 && lane <= kRows && v0 - 1 + lane < end && k.own >= 0;
+    k.own = own;
+    const int32_t before = __shfl(own, (lane + 63) & 63), behind = __shfl(own, (lane + 1) & 63);
+    const bool mine = lane >= 1 && lane <= kRows && v0 + (lane - 1) < end && own >= 0;
     k.inside = uint32_t(__ballot(mine) >> 1);
-    k.first = uint32_t(__ballot(mine && before != k.own) >> 1);
-    k.last = uint32_t(__ballot(mine && behind != k.own) >> 1);
+    k.first = uint32_t(__ballot(mine && before != own) >> 1);
+    k.last = uint32_t(__ballot(mine && behind != own) >> 1);
     return k;
 }
 
@@ -195,7 +239,7 @@ __device__ __forceinline__ Marks marks(const Args& a, int64_t v0, int64_t end) {
 template <class T, int C, bool BACK>
 struct Raw {
     Some<T, C> gate[kRows], in[kRows];  // in: x, backward dh
-    Marks k;
+    int32_t own;                        // see marks()
 };
 
 // What the backward pass needs beside that, once it knows what comes in: x, and
@@ -206,28 +250,26 @@ struct Late {
 };
 
 template <class T, int C, bool BACK>
-__device__ __forceinline__ void fetch_late(const Args& a, int64_t v0, int64_t end, const Columns& c, Late<T, C, BACK>& q) {
+__device__ __forceinline__ void fetch_late(const Args& a, Row v0, Row end, const Columns& c, Late<T, C, BACK>& q) {
     if constexpr (BACK) {
-        if (v0 >= end) return;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int64_t v = v0 + i < end ? v0 + i : end - 1, r = row<BACK>(a, v);
+            const Row v = v0 + i < end ? v0 + i : end - 1;
+            const int64_t r = row<BACK>(a, v);
             q.x[i] = get<T, C>(a.x, r * a.ldx, c);
             q.h[i] = get<T, C>(a.h, (r > 0 ? r - 1 : 0) * a.ldh, c);
         }
     }
 }
 
-template <class T, int C, bool BACK>
-__device__ __forceinline__ void fetch(const Args& a, int64_t v0, int64_t end, const Columns& c, Raw<T, C, BACK>& q) {
-    if (v0 >= end) {
-        q.k.inside = q.k.first = q.k.last = 0;
-        return;
-    }
-    q.k = marks<BACK>(a, v0, end);
+template <class T, int C, bool BACK, bool EVEN>
+__device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK>& q) {
+    const int lane = threadIdx.x & 63;
+    q.own = v0 < end && lane < kRows + 2 ? owner<BACK, EVEN>(a, int64_t(v0) - 1 + lane) : -1;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const int64_t v = v0 + i < end ? v0 + i : end - 1, r = row<BACK>(a, v);
+        const Row v = v0 + i < end ? v0 + i : end - 1;
+        const int64_t r = row<BACK>(a, v);
         q.gate[i] = get<T, C>(a.gate, r * a.ldg, c);
         q.in[i] = BACK ? get<T, C>(a.dh, r * a.lddh, c) : get<T, C>(a.x, r * a.ldx, c);
     }
@@ -253,39 +295,33 @@ struct Sum {
     bool fresh;
 };
 
-template <class T, int C, bool BACK>
-__device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK>& q, int64_t v0, const Columns& c, int64_t kept_row,
-                                         const float* kept, Sum<C>& s, float (*f)[C], float (*r)[C]) {
-    const auto step = [&](int i) {
+template <bool PLAIN, class T, int C, bool BACK>
+__device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK>& q, const Marks& k, Row v0, const Columns& c,
+                                         int64_t kept_row, const float* kept, Sum<C>& s, float (*f)[C], float (*r)[C]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (!PLAIN) {
+            if (!(k.inside >> i & 1)) continue;
+            if (k.first >> i & 1) {
+                if (int64_t(v0) + i == kept_row) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) s.kept[j] = kept[j];
+                } else {
+                    state_of<C>(a.init, a.ldi, k.sequence(i), c, s.kept);
+                }
+#pragma unroll
+                for (int j = 0; j < C; ++j) s.B[j] = s.kept[j];
+                s.fresh = true;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            gate_pair(float(q.gate[i].t[j]), f[i][j], r[i][j]);
-            const float in = float(q.in[i].t[j]);
+            gate_pair<sizeof(T) == 4>(q.gate[i].at(j), f[i][j], r[i][j]);
+            const float in = q.in[i].at(j);
             if (!BACK) r[i][j] *= in;
             s.B[j] = BACK ? f[i][j] * (s.B[j] + in) : fmaf(f[i][j], s.B[j], r[i][j]);
             s.A[j] *= f[i][j];
         }
-    };
-    if (q.k.inside == (1u << kRows) - 1 && q.k.first == 0) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) step(i);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        if (!(q.k.inside >> i & 1)) continue;
-        if (q.k.first >> i & 1) {
-            if (v0 + i == kept_row) {
-#pragma unroll
-                for (int j = 0; j < C; ++j) s.kept[j] = kept[j];
-            } else {
-                state_of<C>(a.init, a.ldi, q.k.sequence(i), c, s.kept);
-            }
-#pragma unroll
-            for (int j = 0; j < C; ++j) s.B[j] = s.kept[j];
-            s.fresh = true;
-        }
-        step(i);
     }
 }
 
@@ -301,26 +337,31 @@ __device__ __forceinline__ void clear(Sum<C>& s) {
 
 // A and B of each part but the last: a wave takes its share of the part's rows
 // in a row.
-template <class T, int C, bool BACK>
+template <class T, int C, bool BACK, bool EVEN>
 __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     __shared__ float sum[kWaves][3][kLanes * C];
     __shared__ int64_t began[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t block = dgc::block_number(), part = block / a.p.strips, strip = block % a.p.strips;
+    const Place w = place(a);
+    const int64_t part = w.part, strip = w.strip;
     if (part >= a.p.count - 1) return;
     const Columns c = columns_of<C>(a.s.d, strip);
-    const int64_t share = a.p.rows / kWaves;  // a part's rows are a multiple of a chunk's
-    const int64_t begin = part * a.p.rows + wave * share, end = begin + share;
+    const Row share = Row(a.p.rows) / kWaves;  // a part's rows are a multiple of a chunk's
+    const Row begin = w.part * Row(a.p.rows) + wave * share, end = begin + share;
     Sum<C> s;
     clear(s);
     int64_t last = -1;
     Raw<T, C, BACK> q, next;
-    fetch<T, C, BACK>(a, begin, end, c, q);
-    for (int64_t v = begin; v < end; v += kRows) {
-        fetch<T, C, BACK>(a, v + kRows, end, c, next);
+    fetch<T, C, BACK, EVEN>(a, begin, end, c, q);
+    for (Row v = begin; v < end; v += kRows) {
+        fetch<T, C, BACK, EVEN>(a, v + kRows, end, c, next);
+        const Marks k = marks(q.own, v, end);
         float f[kRows][C], r[kRows][C];
-        add_rows<T, C, BACK>(a, q, v, c, -1, nullptr, s, f, r);
-        if (q.k.first) last = v + 31 - __builtin_clz(q.k.first);
+        if (k.plain())
+            add_rows<true, T, C, BACK>(a, q, k, v, c, -1, nullptr, s, f, r);
+        else
+            add_rows<false, T, C, BACK>(a, q, k, v, c, -1, nullptr, s, f, r);
+        if (k.first) last = int64_t(v) + 31 - __builtin_clz(k.first);
         q = next;
     }
 #pragma unroll
@@ -353,17 +394,19 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     if (lane == 0) a.p.last[part * a.p.strips + strip] = last;
 }
 
-template <class T, int C, bool BACK>
+template <class T, int C, bool BACK, bool EVEN>
 __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     __shared__ float sum[2][kWaves][2][kLanes * C];
     __shared__ int fresh[2][kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t block = dgc::block_number(), part = block / a.p.strips, strip = block % a.p.strips;
+    const Place spot = place(a);
+    const int64_t part = spot.part, strip = spot.strip;
     if (part >= a.p.count) return;
     const Columns c = columns_of<C>(a.s.d, strip);
-    const int64_t begin = part * a.p.rows, end = begin + a.p.rows < a.s.m ? begin + a.p.rows : a.s.m;
+    const Row m = Row(a.s.m), begin = spot.part * Row(a.p.rows);
+    const Row end = m - begin > Row(a.p.rows) ? begin + Row(a.p.rows) : m;
     Raw<T, C, BACK> q, next;
-    fetch<T, C, BACK>(a, begin + wave * kRows, end, c, q);
+    fetch<T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
     float carry[C] = {}, kept[C] = {};
     int64_t kept_row = -1;
     if (a.p.split) {
@@ -381,16 +424,17 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
             get_wide<C>(a.p.kept, part * a.s.d, c, kept);
         }
     }
+    // A chunk; the next one's rows are on their way into `next` meanwhile.
     int turn = 0;
-    for (int64_t base = begin; base < end; base += kChunk, turn ^= 1) {
-        const int64_t v0 = base + wave * kRows;
+    const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK>& q, Raw<T, C, BACK>& next) {
+        constexpr bool PLAIN = decltype(plain)::value;
         Late<T, C, BACK> late;
         fetch_late<T, C, BACK>(a, v0, end, c, late);
-        fetch<T, C, BACK>(a, v0 + kChunk, end, c, next);
+        fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
         Sum<C> s;
         clear(s);
         float f[kRows][C], r[kRows][C];
-        add_rows<T, C, BACK>(a, q, v0, c, kept_row, kept, s, f, r);
+        add_rows<PLAIN, T, C, BACK>(a, q, k, v0, c, kept_row, kept, s, f, r);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             sum[turn][wave][0][lane * C + j] = s.A[j];
@@ -409,46 +453,61 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
                 carry[j] = began ? B : fmaf(A, carry[j], B);
             }
         }
-        const auto step = [&](int i, bool first, bool last) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (!PLAIN && !(k.inside >> i & 1)) continue;
+            const bool first = !PLAIN && (k.first >> i & 1), last = !PLAIN && (k.last >> i & 1);
             float y[C], z[C], start[C];
             if (first) {
                 // the last one's initial value is at hand: it may have been overwritten by the rows behind
-                if (q.k.first >> i == 1) {
+                if (k.first >> i == 1) {
 #pragma unroll
                     for (int j = 0; j < C; ++j) now[j] = s.kept[j];
                 } else {
-                    state_of<C>(a.init, a.ldi, q.k.sequence(i), c, now);
+                    state_of<C>(a.init, a.ldi, k.sequence(i), c, now);
                 }
             }
-            const int32_t sequence = last ? q.k.sequence(i) : 0;
+            const int32_t sequence = last ? k.sequence(i) : 0;
             if (BACK && last) state_of<C>(a.h0, a.ldh0, sequence, c, start);
             const int64_t at = row<BACK>(a, v0 + i);
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 if constexpr (BACK) {
-                    const float g = float(q.in[i].t[j]) + now[j], h = last ? start[j] : float(late.h[i].t[j]);
+                    const float g = q.in[i].at(j) + now[j], h = last ? start[j] : late.h[i].at(j);
                     y[j] = r[i][j] * g;
-                    z[j] = g * (h - float(late.x[i].t[j])) * (f[i][j] * r[i][j]);
+                    z[j] = g * (h - late.x[i].at(j)) * (f[i][j] * r[i][j]);
                     now[j] = f[i][j] * g;
                 } else {
                     now[j] = fmaf(f[i][j], now[j], r[i][j]);
                     y[j] = now[j];
                 }
             }
-            if (!c.mine) return;
+            if (!c.mine) continue;
             if (!BACK || a.out) put<T, C>(a.out, at * a.ldo, c, y);
             if (BACK && a.out2) put<T, C>(a.out2, at * a.ldo2, c, z);
             if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
-        };
-        if (q.k.inside == (1u << kRows) - 1 && (q.k.first | q.k.last) == 0) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) step(i, false, false);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-                if (q.k.inside >> i & 1) step(i, q.k.first >> i & 1, q.k.last >> i & 1);
         }
-        q = next;
+        turn ^= 1;
+    };
+    // Loads and stores are counted together and in order.  Where every way into a
+    // chunk but that from a plain one has waited for all of them, a wait for the
+    // chunk's loads does not wait for the stores behind them.
+    const auto wait = [] { __builtin_amdgcn_s_waitcnt(0x0F70); };  // vmcnt(0)
+    const auto take = [&](Row base, const Raw<T, C, BACK>& q, Raw<T, C, BACK>& next) {
+        const Row v0 = base + wave * kRows;
+        const Marks k = marks(q.own, v0, end);
+        if (k.plain()) {
+            chunk(std::true_type(), k, v0, q, next);
+        } else {
+            chunk(std::false_type(), k, v0, q, next);
+            wait();
+        }
+    };
+    wait();
+    for (Row base = begin; base < end; base += Row(2 * kChunk)) {
+        take(base, q, next);
+        if (base + Row(kChunk) >= end) break;
+        take(base + Row(kChunk), next, q);
     }
 }
 
@@ -480,7 +539,7 @@ __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans
 #pragma unroll
             for (int j = 0; j < kRow; ++j) {
                 float f, r;
-                gate_pair(z[j], f, r);
+                gate_pair<sizeof(T) == 4>(z[j], f, r);
                 if (BACK) {
                     const float g = in[j] + now[j];
                     z[j] = g * (h[j] - x[j]) * (f * r);
@@ -612,18 +671,23 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
     a.p.kept = reinterpret_cast<float*>(ws + sp.kept);
     a.p.last = reinterpret_cast<int64_t*>(ws + sp.last);
     a.s.owner = a.s.offsets ? owner : nullptr;
-    const auto with = [&](auto t, auto columns) {
+    const auto with = [&](auto t, auto columns, auto even) {
         typedef decltype(t) T;
         constexpr int C = decltype(columns)::value;
+        constexpr bool EVEN = decltype(even)::value;
         if (a.p.split)
-            k_parts<T, C, BACK><<<dgc::grid_of((a.p.count - 1) * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
-        k_along<T, C, BACK><<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+            k_parts<T, C, BACK, EVEN>
+                <<<dgc::grid_of((a.p.count - 1) * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        k_along<T, C, BACK, EVEN><<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
         return launched();
+    };
+    const auto wide = [&](auto t, auto columns) {
+        return a.s.offsets ? with(t, columns, std::false_type()) : with(t, columns, std::true_type());
     };
     return with_type(type, [&](auto t) {
         if constexpr (!BACK && sizeof(t) == 2)
-            if (k.columns == 2) return with(t, std::integral_constant<int, 2>());
-        return with(t, std::integral_constant<int, 1>());
+            if (k.columns == 2) return wide(t, std::integral_constant<int, 2>());
+        return wide(t, std::integral_constant<int, 1>());
     });
 }
 

@@ -87,8 +87,17 @@ def kept(p):
     return int(np.floor((1 - p) * 65536 + 0.5))
 
 
-# Of f and 1 - f: an exponential within 2 steps, a sum, a quotient and a product.
-GATE = 8 * U
+def gate_errors(z, f, r, dtype):
+    """Of f = 1 / (1 + E) and r = E f, relative to them, E = exp(-z) as a power of 2.
+
+    E is off by its own step, 2 U, and by its exponent's rounding: z * log2(e) is off by half a step of itself,
+    so E by |z| U, and by the constant's own share, 2^-25.2 of |z|, 0.4 |z| U; for binary32 rows both are made good to first
+    order: 4 U in all.  Through 1 + E this reaches f by the share r = E / (1 + E) and r = E f by f.  To that come
+    the sum's rounding, U, the reciprocal's step, 2 U, and r's product, U."""
+    exponent = (4 * U if dtype == torch.float32 else (1.4 * z.abs() + 2) * U)
+    return r * exponent + 3 * U, f * exponent + 4 * U
+
+
 # Additions between parts of a sequence, on the way of any term.
 PARTS = 40 * U
 
@@ -115,10 +124,12 @@ def back(v, row, valid, m):
 def recurrence(gate, x, h0, offsets):
     """(h, its error, state, its error), row by row.
 
-    A term that is t steps old has gone through t products with an f: each adds GATE and a rounding of its share.
+    A term that is t steps old has gone through t products with an f: each adds the error of that and a rounding.
     The magnitudes' own recurrence carries that along."""
     m, d = x.shape
     row, valid = places(offsets, m)
+    gf, gr = gate_errors(*(lay(v, row, valid, 0.0) for v in (gate, torch.sigmoid(gate.double()), torch.sigmoid(-gate.double()))),
+                         x.dtype)
     f, r = lay(torch.sigmoid(gate.double()), row, valid, 1.0), lay(torch.sigmoid(-gate.double()), row, valid, 0.0)
     xs = lay(x, row, valid, 0.0)
     now = torch.zeros(len(offsets) - 1, d, dtype=torch.float64, device="cuda")
@@ -127,7 +138,7 @@ def recurrence(gate, x, h0, offsets):
     h, eh = torch.zeros_like(f), torch.zeros_like(f)
     for t in range(row.shape[1]):
         on = valid[:, t, None]
-        e = torch.where(on, f[:, t] * (e + (GATE + 2 * U) * size) + (GATE + 2 * U) * r[:, t] * xs[:, t].abs(), e)
+        e = torch.where(on, f[:, t] * (e + (gf[:, t] + 2 * U) * size) + (gr[:, t] + 2 * U) * r[:, t] * xs[:, t].abs(), e)
         now = f[:, t] * now + r[:, t] * xs[:, t]
         size = f[:, t] * size + r[:, t] * xs[:, t].abs()
         h[:, t], eh[:, t] = now, e + PARTS * size
@@ -138,6 +149,8 @@ def recurrence_backward(dh, gate, x, h, h0, dstate, offsets):
     """{name: (value, its error)} of dgate, dx and dh0."""
     m, d = x.shape
     row, valid = places(offsets, m)
+    gf, gr = gate_errors(*(lay(v, row, valid, 0.0) for v in (gate, torch.sigmoid(gate.double()), torch.sigmoid(-gate.double()))),
+                         x.dtype)
     f, r = lay(torch.sigmoid(gate.double()), row, valid, 1.0), lay(torch.sigmoid(-gate.double()), row, valid, 0.0)
     xs, dhs, hs = (lay(v, row, valid, 0.0) for v in (x, dh, h))
     n = len(offsets) - 1
@@ -153,11 +166,11 @@ def recurrence_backward(dh, gate, x, h, h0, dstate, offsets):
         g[:, t] = now + dhs[:, t]
         size = size + dhs[:, t].abs()
         eg[:, t] = e + PARTS * size
-        e = torch.where(on, f[:, t] * (e + (GATE + 2 * U) * size), e)
+        e = torch.where(on, f[:, t] * (e + (gf[:, t] + 2 * U) * size), e)
         now, size = f[:, t] * g[:, t], f[:, t] * size
-    dx, edx = r * g, r * (eg + (GATE + 2 * U) * g.abs())
+    dx, edx = r * g, r * (eg + (gr + 2 * U) * g.abs())
     off = before - xs
     dgate = g * off * f * r
-    edgate = f * r * off.abs() * (eg + (2 * GATE + 6 * U) * g.abs())
+    edgate = f * r * off.abs() * (eg + (gf + gr + 6 * U) * g.abs())
     return {"dgate": (back(dgate, row, valid, m), back(edgate, row, valid, m)),
             "dx": (back(dx, row, valid, m), back(edx, row, valid, m)), "dh0": (now, e + PARTS * size)}
