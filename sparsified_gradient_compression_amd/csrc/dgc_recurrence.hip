@@ -31,7 +31,7 @@ constexpr int kWaves = 16;
 constexpr int kThreads = kLanes * kWaves;
 constexpr int kRows = 8;                       // of a wave at a time
 constexpr int64_t kChunk = kWaves * kRows;     // rows of a workgroup at a time
-constexpr int64_t kShort = 4;                  // rows of a sequence, see run()
+constexpr int64_t kShort = 8;                  // rows of a sequence, see run()
 constexpr int64_t kFill = 256;                 // workgroups that fill the card
 constexpr int64_t kMostBlocks = 1 << 20;       // of a launch: workgroups take what is left in turn
 
@@ -105,6 +105,40 @@ __device__ __forceinline__ void gate_pair(float z, float& f, float& r) {
     f = none ? 0.0f : s;
 }
 
+// Rows in the order of the recurrence: backward from the last to the first.  (32
+// bits without a sign, which a matrix's end and a chunk do not leave: the scalar
+// unit compares no 64 bits, and a row that is not a scalar costs ten vector
+// instructions for each address.)
+typedef uint32_t Row;
+
+template <bool BACK>
+__device__ __forceinline__ Row row(const Args& a, Row v) {
+    return BACK ? Row(a.s.m) - 1 - v : v;
+}
+
+// A row's sequence.  (v: from -1 up to m and beyond.  EVEN, for equally long ones, is
+// known when it is compiled: a register that a load may still be on its way into
+// would be waited for.)
+template <bool BACK, bool EVEN>
+__device__ __forceinline__ int32_t owner(const Args& a, int64_t v) {
+    if (v < 0 || v >= a.s.m) return -1;
+    const Row r = row<BACK>(a, Row(v));
+    return EVEN ? int32_t(r / a.s.length) : a.s.owner[r];
+}
+
+// A workgroup's part and strip of columns.
+struct Place {
+    uint32_t part, strip;
+};
+
+__device__ __forceinline__ Place place(const Args& a) {
+    const uint32_t block = uint32_t(dgc::block_number()), part = block / uint32_t(a.p.strips);
+    Place w;
+    w.part = __builtin_amdgcn_readfirstlane(part);
+    w.strip = __builtin_amdgcn_readfirstlane(block - part * uint32_t(a.p.strips));
+    return w;
+}
+
 // A workgroup's columns: `base` is the first lane's first one, the same for a
 // whole wave, as rows are, so that an address is a scalar and a lane's small part.
 struct Columns {
@@ -140,10 +174,21 @@ struct Some {
 typedef uint16_t Half __attribute__((may_alias));
 typedef uint32_t Word2 __attribute__((aligned(2), may_alias));
 
+// A matrix's row, for a whole wave, and the way to the next.
+struct Walk {
+    const char* p;
+    int64_t step;
+};
+
+template <class T, bool BACK>
+__device__ __forceinline__ Walk walk(const void* p, int64_t ld, Row r, const Columns& c) {
+    const int64_t bytes = ld * int64_t(sizeof(T));
+    return {reinterpret_cast<const char*>(static_cast<const T*>(p) + c.base) + int64_t(r) * bytes, BACK ? -bytes : bytes};
+}
+
 template <class T, int C>
-__device__ __forceinline__ Some<T, C> get(const void* p, int64_t at, const Columns& c) {
-    const char* const q = reinterpret_cast<const char*>(static_cast<const T*>(p) + (at + c.base)) +
-                          uint64_t(uint32_t(c.lane * sizeof(T)));
+__device__ __forceinline__ Some<T, C> get(const Walk& w, const Columns& c) {
+    const char* const q = w.p + uint64_t(uint32_t(c.lane * sizeof(T)));
     if constexpr (sizeof(T) * C == 2)
         return {*reinterpret_cast<const Half*>(q)};
     else
@@ -151,18 +196,17 @@ __device__ __forceinline__ Some<T, C> get(const void* p, int64_t at, const Colum
 }
 
 template <class T, int C>
-__device__ __forceinline__ void put(void* p, int64_t at, const Columns& c, const float* v) {
-    char* const q =
-        reinterpret_cast<char*>(static_cast<T*>(p) + (at + c.base)) + uint64_t(uint32_t(c.lane * sizeof(T)));
+__device__ __forceinline__ void put(const Walk& w, const Columns& c, const float* v) {
+    char* const q = const_cast<char*>(w.p) + uint64_t(uint32_t(c.lane * sizeof(T)));
     T t[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = T(v[i]);
     if constexpr (sizeof(T) * C == 2) {
         *reinterpret_cast<Half*>(q) = __builtin_bit_cast(uint16_t, t[0]);
     } else {
-        uint32_t w;
-        __builtin_memcpy(&w, t, 4);
-        *reinterpret_cast<Word2*>(q) = w;
+        uint32_t w32;
+        __builtin_memcpy(&w32, t, 4);
+        *reinterpret_cast<Word2*>(q) = w32;
     }
 }
 
@@ -177,40 +221,6 @@ template <int C>
 __device__ __forceinline__ void put_wide(float* p, int64_t at, const Columns& c, const float* v) {
 #pragma unroll
     for (int i = 0; i < C; ++i) p[at + c.base + c.lane + i] = v[i];
-}
-
-// Rows in the order of the recurrence: backward from the last to the first.  (32
-// bits without a sign, which a matrix's end and a chunk do not leave: the scalar
-// unit compares no 64 bits, and a row that is not a scalar costs ten vector
-// instructions for each address.)
-typedef uint32_t Row;
-
-template <bool BACK>
-__device__ __forceinline__ Row row(const Args& a, Row v) {
-    return BACK ? Row(a.s.m) - 1 - v : v;
-}
-
-// A row's sequence.  (v: from -1 up to m and beyond.  EVEN, for equally long ones, is
-// known when it is compiled: a register that a load may still be on its way into
-// would be waited for.)
-template <bool BACK, bool EVEN>
-__device__ __forceinline__ int32_t owner(const Args& a, int64_t v) {
-    if (v < 0 || v >= a.s.m) return -1;
-    const Row r = row<BACK>(a, Row(v));
-    return EVEN ? int32_t(r / a.s.length) : a.s.owner[r];
-}
-
-// A workgroup's part and strip of columns.
-struct Place {
-    uint32_t part, strip;
-};
-
-__device__ __forceinline__ Place place(const Args& a) {
-    const uint32_t block = uint32_t(dgc::block_number()), part = block / uint32_t(a.p.strips);
-    Place w;
-    w.part = __builtin_amdgcn_readfirstlane(part);
-    w.strip = __builtin_amdgcn_readfirstlane(block - part * uint32_t(a.p.strips));
-    return w;
 }
 
 // What a wave's rows v0 .. v0 + kRows - 1, as far as they lie before `end`, are.
@@ -235,43 +245,39 @@ __device__ __forceinline__ Marks marks(int32_t own, Row v0, Row end) {
     return k;
 }
 
-// A wave's rows as they are in memory: what A and B are made of.
-template <class T, int C, bool BACK>
+// A wave's rows as they are in memory.  ALL: what the backward pass needs beside A
+// and B too.
+template <class T, int C, bool BACK, bool ALL>
 struct Raw {
+    static constexpr int kMore = BACK && ALL ? kRows : 1;
     Some<T, C> gate[kRows], in[kRows];  // in: x, backward dh
+    Some<T, C> x[kMore], h[kMore];      // h: of the row before
     int32_t own;                        // see marks()
 };
 
-// What the backward pass needs beside that, once it knows what comes in: x, and
-// h of the row before.
-template <class T, int C, bool BACK>
-struct Late {
-    Some<T, C> x[BACK ? kRows : 1], h[BACK ? kRows : 1];
-};
-
-template <class T, int C, bool BACK>
-__device__ __forceinline__ void fetch_late(const Args& a, Row v0, Row end, const Columns& c, Late<T, C, BACK>& q) {
-    if constexpr (BACK) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const Row v = v0 + i < end ? v0 + i : end - 1;
-            const int64_t r = row<BACK>(a, v);
-            q.x[i] = get<T, C>(a.x, r * a.ldx, c);
-            q.h[i] = get<T, C>(a.h, (r > 0 ? r - 1 : 0) * a.ldh, c);
-        }
-    }
-}
-
-template <class T, int C, bool BACK, bool EVEN>
-__device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK>& q) {
+// Behind `end` the last row again and again: every lane loads at all times.
+template <class T, int C, bool BACK, bool EVEN, bool ALL>
+__device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
     const int lane = threadIdx.x & 63;
     q.own = v0 < end && lane < kRows + 2 ? owner<BACK, EVEN>(a, int64_t(v0) - 1 + lane) : -1;
+    const Row r = row<BACK>(a, v0 < end ? v0 : end - 1);
+    Walk gate = walk<T, BACK>(a.gate, a.ldg, r, c), x = walk<T, BACK>(a.x, a.ldx, r, c);
+    Walk dh = walk<T, BACK>(a.dh, a.lddh, r, c), h = walk<T, BACK>(a.h, a.ldh, r > 0 ? r - 1 : 0, c);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const Row v = v0 + i < end ? v0 + i : end - 1;
-        const int64_t r = row<BACK>(a, v);
-        q.gate[i] = get<T, C>(a.gate, r * a.ldg, c);
-        q.in[i] = BACK ? get<T, C>(a.dh, r * a.lddh, c) : get<T, C>(a.x, r * a.ldx, c);
+        if (i > 0) {
+            const bool more = v0 + i < end;
+            gate.p += more ? gate.step : 0;
+            x.p += more ? x.step : 0;
+            dh.p += more ? dh.step : 0;
+            h.p += more && v0 + i < Row(a.s.m) - 1 ? h.step : 0;
+        }
+        q.gate[i] = get<T, C>(gate, c);
+        q.in[i] = get<T, C>(BACK ? dh : x, c);
+        if constexpr (BACK && ALL) {
+            q.x[i] = get<T, C>(x, c);
+            q.h[i] = get<T, C>(h, c);
+        }
     }
 }
 
@@ -295,8 +301,8 @@ struct Sum {
     bool fresh;
 };
 
-template <bool PLAIN, class T, int C, bool BACK>
-__device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK>& q, const Marks& k, Row v0, const Columns& c,
+template <bool PLAIN, class T, int C, bool BACK, bool ALL>
+__device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK, ALL>& q, const Marks& k, Row v0, const Columns& c,
                                          int64_t kept_row, const float* kept, Sum<C>& s, float (*f)[C], float (*r)[C]) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -351,16 +357,16 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     Sum<C> s;
     clear(s);
     int64_t last = -1;
-    Raw<T, C, BACK> q, next;
+    Raw<T, C, BACK, false> q, next;
     fetch<T, C, BACK, EVEN>(a, begin, end, c, q);
     for (Row v = begin; v < end; v += kRows) {
         fetch<T, C, BACK, EVEN>(a, v + kRows, end, c, next);
         const Marks k = marks(q.own, v, end);
         float f[kRows][C], r[kRows][C];
         if (k.plain())
-            add_rows<true, T, C, BACK>(a, q, k, v, c, -1, nullptr, s, f, r);
+            add_rows<true>(a, q, k, v, c, -1, nullptr, s, f, r);
         else
-            add_rows<false, T, C, BACK>(a, q, k, v, c, -1, nullptr, s, f, r);
+            add_rows<false>(a, q, k, v, c, -1, nullptr, s, f, r);
         if (k.first) last = int64_t(v) + 31 - __builtin_clz(k.first);
         q = next;
     }
@@ -405,18 +411,27 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const Columns c = columns_of<C>(a.s.d, strip);
     const Row m = Row(a.s.m), begin = spot.part * Row(a.p.rows);
     const Row end = m - begin > Row(a.p.rows) ? begin + Row(a.p.rows) : m;
-    Raw<T, C, BACK> q, next;
+    Raw<T, C, BACK, true> q, next;
     fetch<T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
     float carry[C] = {}, kept[C] = {};
     int64_t kept_row = -1;
     if (a.p.split) {
-        for (int64_t p = 0; p < part; ++p) {
-            const bool began = a.p.last[p * a.p.strips + strip] >= 0;
-            float A[C], B[C];
-            get_wide<C>(a.p.sums, p * 2 * a.s.d, c, A);
-            get_wide<C>(a.p.sums, (p * 2 + 1) * a.s.d, c, B);
+        constexpr int kBatch = 8;  // parts whose sums are under way together
+        for (int64_t p = 0; p < part; p += kBatch) {
+            float A[kBatch][C], B[kBatch][C];
+            int64_t began[kBatch];
 #pragma unroll
-            for (int j = 0; j < C; ++j) carry[j] = began ? B[j] : fmaf(A[j], carry[j], B[j]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t at = p + i < part ? p + i : part - 1;
+                began[i] = a.p.last[at * a.p.strips + strip];
+                get_wide<C>(a.p.sums, at * 2 * a.s.d, c, A[i]);
+                get_wide<C>(a.p.sums, (at * 2 + 1) * a.s.d, c, B[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (p + i < part)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) carry[j] = began[i] >= 0 ? B[i][j] : fmaf(A[i][j], carry[j], B[i][j]);
         }
         // (of the last part no sequence goes on)
         if (part < a.p.count - 1) {
@@ -426,15 +441,13 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     }
     // A chunk; the next one's rows are on their way into `next` meanwhile.
     int turn = 0;
-    const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK>& q, Raw<T, C, BACK>& next) {
+    const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         constexpr bool PLAIN = decltype(plain)::value;
-        Late<T, C, BACK> late;
-        fetch_late<T, C, BACK>(a, v0, end, c, late);
         fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
         Sum<C> s;
         clear(s);
         float f[kRows][C], r[kRows][C];
-        add_rows<PLAIN, T, C, BACK>(a, q, k, v0, c, kept_row, kept, s, f, r);
+        add_rows<PLAIN>(a, q, k, v0, c, kept_row, kept, s, f, r);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             sum[turn][wave][0][lane * C + j] = s.A[j];
@@ -442,6 +455,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
         }
         if (lane == 0) fresh[turn][wave] = s.fresh;
         __syncthreads();
+        const Row r0 = row<BACK>(a, v0);
+        Walk out = walk<T, BACK>(a.out, a.ldo, r0, c), out2 = walk<T, BACK>(a.out2, a.ldo2, r0, c);
         float now[C];
 #pragma unroll 4
         for (int w = 0; w < kWaves; ++w) {
@@ -454,7 +469,7 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
+        for (int i = 0; i < kRows; ++i, out.p += out.step, out2.p += out2.step) {
             if (!PLAIN && !(k.inside >> i & 1)) continue;
             const bool first = !PLAIN && (k.first >> i & 1), last = !PLAIN && (k.last >> i & 1);
             float y[C], z[C], start[C];
@@ -469,13 +484,12 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
             }
             const int32_t sequence = last ? k.sequence(i) : 0;
             if (BACK && last) state_of<C>(a.h0, a.ldh0, sequence, c, start);
-            const int64_t at = row<BACK>(a, v0 + i);
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 if constexpr (BACK) {
-                    const float g = q.in[i].at(j) + now[j], h = last ? start[j] : late.h[i].at(j);
+                    const float g = q.in[i].at(j) + now[j], h = last ? start[j] : q.h[i].at(j);
                     y[j] = r[i][j] * g;
-                    z[j] = g * (h - late.x[i].at(j)) * (f[i][j] * r[i][j]);
+                    z[j] = g * (h - q.x[i].at(j)) * (f[i][j] * r[i][j]);
                     now[j] = f[i][j] * g;
                 } else {
                     now[j] = fmaf(f[i][j], now[j], r[i][j]);
@@ -483,8 +497,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
                 }
             }
             if (!c.mine) continue;
-            if (!BACK || a.out) put<T, C>(a.out, at * a.ldo, c, y);
-            if (BACK && a.out2) put<T, C>(a.out2, at * a.ldo2, c, z);
+            if (!BACK || a.out) put<T, C>(out, c, y);
+            if (BACK && a.out2) put<T, C>(out2, c, z);
             if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
         }
         turn ^= 1;
@@ -493,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     // chunk but that from a plain one has waited for all of them, a wait for the
     // chunk's loads does not wait for the stores behind them.
     const auto wait = [] { __builtin_amdgcn_s_waitcnt(0x0F70); };  // vmcnt(0)
-    const auto take = [&](Row base, const Raw<T, C, BACK>& q, Raw<T, C, BACK>& next) {
+    const auto take = [&](Row base, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         const Row v0 = base + wave * kRows;
         const Marks k = marks(q.own, v0, end);
         if (k.plain()) {
@@ -513,7 +527,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
 
 // Short sequences of equal length: a lane goes along 8 columns of one, row by
 // row.
-template <class T, bool BACK>
+// kAtOnce: rows whose loads are under way together.
+template <class T, bool BACK, int kAtOnce>
 __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans, int64_t tasks) {
     const int tx = threadIdx.x & (across - 1), ty = threadIdx.x / across, each = 256 / across;
     for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
@@ -523,35 +538,57 @@ __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans
         const int64_t begin = b * a.s.length;
         float now[kRow] = {};
         if (a.init) load8(a.init + b * a.ldi + c, valid, now);
-        for (int64_t i = 0; i < a.s.length; ++i) {
-            const int64_t t = BACK ? begin + a.s.length - 1 - i : begin + i;
-            float z[kRow], in[kRow], x[kRow], h[kRow] = {};
-            load8(static_cast<const T*>(a.gate) + t * a.ldg + c, valid, z);
-            load8(BACK ? static_cast<const T*>(a.dh) + t * a.lddh + c : static_cast<const T*>(a.x) + t * a.ldx + c, valid,
-                  in);
-            if (BACK) {
-                load8(static_cast<const T*>(a.x) + t * a.ldx + c, valid, x);
-                if (t > begin)
-                    load8(static_cast<const T*>(a.h) + (t - 1) * a.ldh + c, valid, h);
-                else if (a.h0)
-                    load8(a.h0 + b * a.ldh0 + c, valid, h);
-            }
+        const int64_t end = begin + a.s.length;
+        for (int64_t i = 0; i < a.s.length; i += kAtOnce) {
+            Eight<T> gate[kAtOnce], in[kAtOnce], xs[BACK ? kAtOnce : 1], hs[BACK ? kAtOnce : 1];
 #pragma unroll
-            for (int j = 0; j < kRow; ++j) {
-                float f, r;
-                gate_pair<sizeof(T) == 4>(z[j], f, r);
-                if (BACK) {
-                    const float g = in[j] + now[j];
-                    z[j] = g * (h[j] - x[j]) * (f * r);
-                    x[j] = r * g;
-                    now[j] = f * g;
-                } else {
-                    now[j] = fmaf(f, now[j], r * in[j]);
-                    x[j] = now[j];
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int64_t t = BACK ? (end - 1 - i - k > begin ? end - 1 - i - k : begin)
+                                       : (begin + i + k < end ? begin + i + k : end - 1);
+                gate[k] = read8(static_cast<const T*>(a.gate) + t * a.ldg + c, valid);
+                in[k] = read8(BACK ? static_cast<const T*>(a.dh) + t * a.lddh + c
+                                   : static_cast<const T*>(a.x) + t * a.ldx + c, valid);
+                if constexpr (BACK) {
+                    xs[k] = read8(static_cast<const T*>(a.x) + t * a.ldx + c, valid);
+                    hs[k] = read8(static_cast<const T*>(a.h) + (t > begin ? t - 1 : t) * a.ldh + c, valid);
                 }
             }
-            if (!BACK || a.out) store8(static_cast<T*>(a.out) + t * a.ldo + c, valid, x);
-            if (BACK && a.out2) store8(static_cast<T*>(a.out2) + t * a.ldo2 + c, valid, z);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (i + k >= a.s.length) break;
+                const int64_t t = BACK ? end - 1 - i - k : begin + i + k;
+                float z[kRow], u[kRow], x[kRow], h[kRow];
+                widen(gate[k], z);
+                widen(in[k], u);
+                if constexpr (BACK) {
+                    widen(xs[k], x);
+                    widen(hs[k], h);
+                    if (t == begin) {
+                        if (a.h0) {
+                            load8(a.h0 + b * a.ldh0 + c, valid, h);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < kRow; ++j) h[j] = 0.0f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kRow; ++j) {
+                    float f, r;
+                    gate_pair<sizeof(T) == 4>(z[j], f, r);
+                    if (BACK) {
+                        const float g = u[j] + now[j];
+                        z[j] = g * (h[j] - x[j]) * (f * r);
+                        x[j] = r * g;
+                        now[j] = f * g;
+                    } else {
+                        now[j] = fmaf(f, now[j], r * u[j]);
+                        x[j] = now[j];
+                    }
+                }
+                if (!BACK || a.out) store8(static_cast<T*>(a.out) + t * a.ldo + c, valid, x);
+                if (BACK && a.out2) store8(static_cast<T*>(a.out2) + t * a.ldo2 + c, valid, z);
+            }
         }
         if (a.final) store8(a.final + b * a.ldf + c, valid, now);
     }
@@ -618,7 +655,7 @@ Plan plan(int64_t m, int64_t d, int64_t batch, bool even, int most) {
             k.p.count = cdiv(m, rows);
             if (k.p.count * strips >= kFill || m <= kChunk) return k;
         }
-    if (even && k.p.count * k.p.strips >= kFill / 2) return k;
+    if (even && k.p.count * k.p.strips >= kFill * 3 / 4) return k;
     k.columns = most;
     k.p.strips = strips_of(d, k.columns);
     k.p.rows = part_rows(m, k.p.strips);
@@ -659,8 +696,8 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
         while (across > 1 && across / 2 * kRow >= a.s.d) across /= 2;
         const int64_t spans = cdiv(a.s.d, int64_t(across) * kRow), tasks = spans * cdiv(a.s.batch, 256 / across);
         return with_type(type, [&](auto t) {
-            k_short<decltype(t), BACK>
-                <<<dim3(unsigned(std::min(tasks, kMostBlocks))), 256, 0, stream>>>(a, across, spans, tasks);
+            const auto kernel = a.s.length <= 4 ? k_short<decltype(t), BACK, 1> : k_short<decltype(t), BACK, 4>;
+            kernel<<<dim3(unsigned(std::min(tasks, kMostBlocks))), 256, 0, stream>>>(a, across, spans, tasks);
             return launched();
         });
     }
