@@ -1,6 +1,7 @@
 // dgc_norm.hip -- layer norm and its gradients.  See include/dgc.h for the
 // contract of every function.
 #include <algorithm>
+#include <type_traits>
 
 #include "tokens.hpp"
 
@@ -12,6 +13,7 @@ constexpr int kThreads = 256;
 constexpr int64_t kMostBlocks = 1 << 20;  // of a launch: workgroups take what is left in turn
 constexpr int64_t kMostParts = 512;       // stripes of rows whose column sums are joined
 constexpr int64_t kPartRows = 16;         // rows of a stripe, at least
+constexpr int kJoin = 16;                 // parts that a wave of k_norm_join reads together
 constexpr int kColumns = 512;             // of a workgroup of the column sums: 64 lanes, 8 each
 
 struct Forward {
@@ -48,6 +50,89 @@ struct Backward {
     float* part;  // [parts][2][d]: the stripes' column sums
     int64_t parts;
 };
+
+// Sums over the LANES threads (a power of two) that have a row together, of a
+// workgroup of THREADS; all of them get it.  lds: [THREADS / 64], for rows that
+// go over waves.
+template <int LANES, int THREADS>
+__device__ __forceinline__ float sum_row(float s, float* lds) {
+    s = sum_lanes<(LANES < 64 ? LANES : 64)>(s);
+    if constexpr (LANES <= 64) return s;
+    const int wave = threadIdx.x >> 6, first = wave / (LANES / 64) * (LANES / 64);
+    if ((threadIdx.x & 63) == 0) lds[wave] = s;
+    __syncthreads();
+    s = lds[first];
+#pragma unroll
+    for (int w = 1; w < LANES / 64; ++w) s += lds[first + w];
+    return s;
+}
+
+// Rows of at least 8 columns that LANES threads hold in registers, K times 8
+// columns each: read once.  The next row is on its way meanwhile.
+template <class T, int LANES, int K, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_norm(Forward a) {
+    constexpr int kEach = THREADS / LANES;
+    __shared__ float lds[2][THREADS / 64];
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const int64_t step = int64_t(gridDim.x) * kEach;
+    Span at[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) at[k] = span_of(a.d, int64_t(k * LANES + lane) * kRow);
+    const auto read = [&](int64_t r, Eight<T>* e) {
+        const T* const p = static_cast<const T*>(a.x) + (r < a.m ? r : a.m - 1) * a.ldx;
+#pragma unroll
+        for (int k = 0; k < K; ++k) e[k] = read8(p + at[k].at);
+    };
+    Eight<T> row[K];
+    read(int64_t(blockIdx.x) * kEach + group, row);
+    float w[K][kRow], b[K][kRow];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int i = 0; i < kRow; ++i) {
+            w[k][i] = 1.0f;
+            b[k][i] = 0.0f;
+        }
+        if (a.weight) load8_either<T>(a.weight, at[k].at, a.wide, kRow, w[k]);
+        if (a.bias) load8_either<T>(a.bias, at[k].at, a.wide, kRow, b[k]);
+    }
+    const float share = 1.0f / float(a.d);
+    for (int64_t first = int64_t(blockIdx.x) * kEach; first < a.m; first += step) {
+        const int64_t r = first + group;
+        float v[K][kRow], s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            widen(row[k], v[k]);
+            hide(at[k], v[k]);
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) s += v[k][i];
+        }
+        read(r + step, row);
+        const float mean = sum_row<LANES, THREADS>(s, lds[0]) * share;
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) v[k][i] -= mean;
+            hide(at[k], v[k]);
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) s = fmaf(v[k][i], v[k][i], s);
+        }
+        const float rstd = 1.0f / sqrtf(sum_row<LANES, THREADS>(s, lds[1]) * share + a.eps);
+        if (r >= a.m) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+        T* const y = static_cast<T*>(a.y) + r * a.ldy;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) v[k][i] = fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
+            store_span(y, at[k], v[k]);
+        }
+    }
+}
 
 // A workgroup per row, which is read three times: rows of any length.  Sums in
 // binary64: a thread's share of a long row has many terms.
@@ -149,6 +234,153 @@ __global__ __launch_bounds__(kThreads) void k_norm_back_long(Backward a) {
     }
 }
 
+// Rows in registers as in k_norm, and the column sums of all of a workgroup's rows,
+// which it leaves for k_norm_join.
+template <class T, int LANES, int K, int THREADS, bool SUMS, bool RESIDUAL>
+__global__ __launch_bounds__(THREADS) void k_norm_back(Backward a) {
+    constexpr int kEach = THREADS / LANES;
+    constexpr int kGroups = LANES < 64 ? THREADS / 64 : kEach;
+    __shared__ float lds[4][THREADS / 64];
+    __shared__ float joined[SUMS && kGroups > 1 ? 2 * kRow * K : 1][kGroups * LANES];
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const int64_t step = int64_t(gridDim.x) * kEach;
+    Span at[K];
+    float w[K][kRow], sw[K][kRow] = {}, sb[K][kRow] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        at[k] = span_of(a.d, int64_t(k * LANES + lane) * kRow);
+        if (a.weight) {
+            load8_either<T>(a.weight, at[k].at, a.wide, kRow, w[k]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) w[k][i] = 1.0f;
+        }
+    }
+    Eight<T> rdy[K], rx[K];
+    float mean, rstd;
+    const auto read = [&](int64_t r) {
+        r = r < a.m ? r : a.m - 1;
+        const T* const dy = static_cast<const T*>(a.dy) + r * a.lddy;
+        const T* const x = static_cast<const T*>(a.x) + r * a.ldx;
+        mean = a.mean[r];
+        rstd = a.rstd[r];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            rdy[k] = read8(dy + at[k].at);
+            rx[k] = read8(x + at[k].at);
+        }
+    };
+    read(int64_t(blockIdx.x) * kEach + group);
+    const float share = 1.0f / float(a.d);
+    int turn = 0;
+    for (int64_t first = int64_t(blockIdx.x) * kEach; first < a.m; first += step, turn ^= 2) {
+        const int64_t r = first + group;
+        const bool mine = r < a.m;
+        float g[K][kRow], n[K][kRow], sg = 0.0f, sgn = 0.0f;
+        const float rs = rstd;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            widen(rdy[k], g[k]);
+            widen(rx[k], n[k]);
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) n[k][i] = (n[k][i] - mean) * rs;
+            hide(at[k], g[k]);
+            hide(at[k], n[k]);
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) {
+                if (SUMS && mine) {
+                    sw[k][i] = fmaf(g[k][i], n[k][i], sw[k][i]);
+                    sb[k][i] += g[k][i];
+                }
+                g[k][i] *= w[k][i];
+                sg += g[k][i];
+                sgn = fmaf(g[k][i], n[k][i], sgn);
+            }
+        }
+        Eight<T> res[K];
+        if (RESIDUAL) {
+            const T* const p = static_cast<const T*>(a.residual) + (mine ? r : a.m - 1) * a.ldr;
+#pragma unroll
+            for (int k = 0; k < K; ++k) res[k] = read8(p + at[k].at);
+        }
+        read(r + step);
+        if (!a.dx) continue;
+        // (one barrier for both sums; the next row's go elsewhere)
+        sg = sum_lanes<(LANES < 64 ? LANES : 64)>(sg);
+        sgn = sum_lanes<(LANES < 64 ? LANES : 64)>(sgn);
+        if constexpr (LANES > 64) {
+            const int wave = threadIdx.x >> 6, from = wave / (LANES / 64) * (LANES / 64);
+            if ((threadIdx.x & 63) == 0) {
+                lds[turn][wave] = sg;
+                lds[turn + 1][wave] = sgn;
+            }
+            __syncthreads();
+            sg = lds[turn][from];
+            sgn = lds[turn + 1][from];
+#pragma unroll
+            for (int v = 1; v < LANES / 64; ++v) {
+                sg += lds[turn][from + v];
+                sgn += lds[turn + 1][from + v];
+            }
+        }
+        if (!mine) continue;
+        sg *= share;
+        sgn *= share;
+        T* const dx = static_cast<T*>(a.dx) + r * a.lddx;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) {
+                g[k][i] = rs * (g[k][i] - sg - n[k][i] * sgn);
+                if (RESIDUAL) g[k][i] += float(res[k].t[i]);
+            }
+            store_span(dx, at[k], g[k]);
+        }
+    }
+    if constexpr (SUMS) {
+        if constexpr (LANES < 64) {
+            // over a wave's rows
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < kRow; ++i)
+#pragma unroll
+                    for (int far = LANES; far < 64; far *= 2) {
+                        sw[k][i] += __shfl_xor(sw[k][i], far);
+                        sb[k][i] += __shfl_xor(sb[k][i], far);
+                    }
+        }
+        if constexpr (kGroups > 1) {
+            // over waves, or groups of them
+            const int from = LANES < 64 ? threadIdx.x >> 6 : group;
+            if (LANES >= 64 || (threadIdx.x & 63) < LANES)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < kRow; ++i) {
+                        joined[(k * kRow + i) * 2][from * LANES + lane] = sw[k][i];
+                        joined[(k * kRow + i) * 2 + 1][from * LANES + lane] = sb[k][i];
+                    }
+            __syncthreads();
+            if (group > 0) return;
+            for (int v = 1; v < kGroups; ++v)
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int i = 0; i < kRow; ++i) {
+                        sw[k][i] += joined[(k * kRow + i) * 2][v * LANES + lane];
+                        sb[k][i] += joined[(k * kRow + i) * 2 + 1][v * LANES + lane];
+                    }
+        }
+        float* const part = a.part + int64_t(blockIdx.x) * 2 * a.d;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            store_span(part, at[k], sw[k]);
+            store_span(part + a.d, at[k], sb[k]);
+        }
+    }
+}
+
 // Column sums of dy n and dy over a stripe of rows: 64 lanes of 8 columns by 4
 // rows at a time.
 template <class T>
@@ -201,8 +433,18 @@ __global__ __launch_bounds__(1024) void k_norm_join(Backward a) {
     for (int64_t first = int64_t(blockIdx.x) * 64; first < 2 * a.d; first += int64_t(gridDim.x) * 64) {
         const int64_t c = first + lane;  // of dweight's columns, then dbias's
         double s = 0.0;
-        if (c < 2 * a.d)
-            for (int64_t p = y; p < a.parts; p += 16) s += double(a.part[p * 2 * a.d + c]);
+        const float* const column = a.part + (c < 2 * a.d ? c : 2 * a.d - 1);
+        for (int64_t p = y; p < a.parts; p += 16 * kJoin) {
+            float v[kJoin];
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i) {
+                const int64_t at = p + 16 * i;
+                v[i] = column[(at < a.parts ? at : p) * 2 * a.d];
+            }
+#pragma unroll
+            for (int i = 0; i < kJoin; ++i)
+                if (p + 16 * i < a.parts) s += double(v[i]);
+        }
         __syncthreads();
         lds[y][lane] = s;
         __syncthreads();
@@ -217,11 +459,72 @@ __global__ __launch_bounds__(1024) void k_norm_join(Backward a) {
     }
 }
 
-int64_t parts_of(int64_t m) { return std::min(kMostParts, std::max<int64_t>(cdiv(m, kPartRows), 1)); }
+// Parts that the workspace has room for, and stripes of k_norm_columns.
+int64_t most_parts(int64_t m) { return std::min(kMostParts, std::max<int64_t>(m, 1)); }
+int64_t stripes(int64_t m) { return std::min(kMostParts, std::max<int64_t>(cdiv(m, kPartRows), 1)); }
 
-size_t back_bytes(int64_t m, int64_t d) { return d == 0 ? 0 : round_up(size_t(parts_of(m)) * 2 * size_t(d) * 4); }
+size_t back_bytes(int64_t m, int64_t d) { return d == 0 ? 0 : round_up(size_t(most_parts(m)) * 2 * size_t(d) * 4); }
 
 dim3 rows_grid(int64_t m) { return dim3(unsigned(std::min(m, kMostBlocks))); }
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// f(lanes of a row, eights of columns of a lane, threads of a workgroup) for rows
+// that fit into registers; else g().  A row stays within a wave as long as
+// its registers go: it needs no barrier then.  bf16, gain and bias in binary32,
+// microseconds by lanes x eights:
+//   16384 x 1152   64 x 3  14.6   64 x 4  21.3   256 x 1  26.4
+//   16384 x 2048   64 x 4  27.9   256 x 1 27.6
+//   16384 x 4096   256 x 2 51.0   512 x 1 52.6   64 x 8   96
+template <class F, class G>
+int forward_shape(int64_t d, F f, G g) {
+    if (d < kRow) return g();
+    if (d <= 64) return f(Int<8>(), Int<1>(), Int<256>());
+    if (d <= 128) return f(Int<16>(), Int<1>(), Int<256>());
+    if (d <= 256) return f(Int<32>(), Int<1>(), Int<256>());
+    if (d <= 512) return f(Int<64>(), Int<1>(), Int<256>());
+    if (d <= 1024) return f(Int<64>(), Int<2>(), Int<256>());
+    if (d <= 1536) return f(Int<64>(), Int<3>(), Int<256>());
+    if (d <= 2048) return f(Int<256>(), Int<1>(), Int<256>());
+    if (d <= 4096) return f(Int<256>(), Int<2>(), Int<256>());
+    if (d <= 8192) return f(Int<256>(), Int<4>(), Int<256>());
+    if (d <= 16384) return f(Int<512>(), Int<4>(), Int<512>());
+    return g();
+}
+
+// Backward, with the residual:
+//   16384 x 1152   64 x 3  40.9   128 x 2 49.9   256 x 1  61
+//   16384 x 4096   256 x 2 104    512 x 1 111    512 x 2  145
+//   8192 x 8192    512 x 2 104    256 x 4 109
+//   4096 x 16384   512 x 4 196    256 x 8 302 (its sums leave the registers)
+template <class F, class G>
+int backward_shape(int64_t d, F f, G g) {
+    if (d < kRow) return g();
+    if (d <= 64) return f(Int<8>(), Int<1>(), Int<256>());
+    if (d <= 128) return f(Int<16>(), Int<1>(), Int<256>());
+    if (d <= 256) return f(Int<32>(), Int<1>(), Int<256>());
+    if (d <= 512) return f(Int<64>(), Int<1>(), Int<256>());
+    if (d <= 1024) return f(Int<64>(), Int<2>(), Int<256>());
+    if (d <= 1536) return f(Int<64>(), Int<3>(), Int<256>());
+    if (d <= 2048) return f(Int<256>(), Int<1>(), Int<256>());
+    if (d <= 4096) return f(Int<256>(), Int<2>(), Int<256>());
+    if (d <= 8192) return f(Int<512>(), Int<2>(), Int<512>());
+    if (d <= 16384) return f(Int<512>(), Int<4>(), Int<512>());
+    return g();
+}
+
+// Workgroups of k_norm: as many as are resident, each with its gain and bias in
+// registers for all its rows (read again for every row, gain and bias of 4096
+// columns would be twice the row's own bytes: 16384 x 4096 then takes 64 us).
+int64_t resident(int k, int threads) { return (k == 1 ? 2048 : k < 4 ? 1024 : 512) * 256 / threads; }
+
+// Workgroups of k_norm_back.  Each leaves two rows of sums for k_norm_join, so
+// two per compute unit do (16384 x 4096: 104 us; one 119; three 119; four 139), one
+// of 512 threads, and one where there is little to do (2048 x 1280: 13.9 us; two 15.2).
+int64_t back_parts(int64_t m, int64_t d, int threads) {
+    return threads > 256 || m * d < (int64_t(1) << 22) ? 256 : 512;
+}
 
 }  // namespace
 
@@ -247,8 +550,19 @@ int dgc_layer_norm(const dgc_layer_norm_args* a, hipStream_t stream) {
     const Forward f{m, d, float(a->eps), a->x, a->ldx, a->weight, a->bias, a->weight_type == DGC_FP32,
                     a->y, a->ldy, a->mean, a->rstd};
     return with_type(a->type, [&](auto t) {
-        k_norm_long<decltype(t)><<<rows_grid(m), kThreads, 0, stream>>>(f);
-        return launched();
+        typedef decltype(t) T;
+        return forward_shape(
+            d,
+            [&](auto lanes, auto k, auto threads) {
+                constexpr int L = decltype(lanes)::value, K = decltype(k)::value, N = decltype(threads)::value;
+                const int64_t blocks = std::min(cdiv(m, N / L), resident(K, N));
+                k_norm<T, L, K, N><<<dim3(unsigned(blocks)), N, 0, stream>>>(f);
+                return launched();
+            },
+            [&] {
+                k_norm_long<T><<<rows_grid(m), kThreads, 0, stream>>>(f);
+                return launched();
+            });
     });
 }
 
@@ -270,18 +584,36 @@ int dgc_layer_norm_backward(const dgc_layer_norm_backward_args* a, void* workspa
     const int rc = space_ok(workspace, workspace_bytes, sums ? back_bytes(m, d) : 0);
     if (rc != DGC_OK) return rc;
     if (d == 0) return DGC_OK;
-    const Backward b{m, d, a->dy, a->lddy, a->x, a->ldx, a->mean, a->rstd, a->weight, a->weight_type == DGC_FP32,
+    Backward b{m, d, a->dy, a->lddy, a->x, a->ldx, a->mean, a->rstd, a->weight, a->weight_type == DGC_FP32,
                      a->residual, a->ldr, a->dx, a->lddx, a->dweight, a->dbias, a->grad_type == DGC_FP32,
-                     static_cast<float*>(workspace), parts_of(m)};
+                     static_cast<float*>(workspace), stripes(m)};
     return with_type(a->type, [&](auto t) {
         typedef decltype(t) T;
-        // (before dx, which may be dy itself)
-        if (sums) {
-            k_norm_columns<T><<<dim3(unsigned(cdiv(d, kColumns)), unsigned(b.parts)), kThreads, 0, stream>>>(b);
-            k_norm_join<T><<<dim3(unsigned(std::min(cdiv(2 * d, 64), kMostBlocks))), 1024, 0, stream>>>(b);
-        }
-        if (a->dx && m > 0) k_norm_back_long<T><<<rows_grid(m), kThreads, 0, stream>>>(b);
-        return launched();
+        const auto join = [&] {
+            if (sums) k_norm_join<T><<<dim3(unsigned(std::min(cdiv(2 * d, 64), kMostBlocks))), 1024, 0, stream>>>(b);
+            return launched();
+        };
+        const auto any_length = [&] {
+            // (before dx, which may be dy itself)
+            if (sums)
+                k_norm_columns<T><<<dim3(unsigned(cdiv(d, kColumns)), unsigned(b.parts)), kThreads, 0, stream>>>(b);
+            const int rc = join();
+            if (a->dx && m > 0) k_norm_back_long<T><<<rows_grid(m), kThreads, 0, stream>>>(b);
+            return rc == DGC_OK ? launched() : rc;
+        };
+        if (m == 0) return any_length();
+        return backward_shape(
+            d,
+            [&](auto lanes, auto k, auto threads) {
+                constexpr int L = decltype(lanes)::value, K = decltype(k)::value, N = decltype(threads)::value;
+                b.parts = std::min(cdiv(m, N / L), back_parts(m, d, N));
+                const bool res = b.residual && b.dx;
+                const auto kernel = sums ? res ? k_norm_back<T, L, K, N, true, true> : k_norm_back<T, L, K, N, true, false>
+                                         : res ? k_norm_back<T, L, K, N, false, true> : k_norm_back<T, L, K, N, false, false>;
+                kernel<<<dim3(unsigned(b.parts)), N, 0, stream>>>(b);
+                return join();
+            },
+            any_length);
     });
 }
 

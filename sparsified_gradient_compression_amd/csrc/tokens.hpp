@@ -124,6 +124,41 @@ __device__ __forceinline__ int valid_of(int64_t end, int64_t at) {
     return end - at >= kRow ? kRow : end > at ? int(end - at) : 0;
 }
 
+// Where a lane reads 8 columns of a row of at least 8: from its first one, or as far
+// before it as the row is too short, so that all lanes read whole eights without
+// a branch (what lies behind a branch would be waited for at its end).  The first
+// `skip` of them are another lane's; of a lane behind the row all 8.
+struct Span {
+    int64_t at;
+    int skip;
+};
+
+__device__ __forceinline__ Span span_of(int64_t d, int64_t c) {
+    const int64_t at = c + kRow <= d ? c : d - kRow;
+    return {at, c - at < kRow ? int(c - at) : kRow};
+}
+
+// 0 in the place of what is not the lane's.
+template <class V>
+__device__ __forceinline__ void hide(const Span& w, V* v) {
+    if (w.skip > 0)
+#pragma unroll
+        for (int i = 0; i < kRow; ++i)
+            if (i < w.skip) v[i] = V(0.0f);
+}
+
+// (p: the row's first element)
+template <bool ONCE = false, class T>
+__device__ __forceinline__ void store_span(T* p, const Span& w, const float* v) {
+    if (w.skip == 0) {
+        store8<ONCE>(p + w.at, kRow, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRow; ++i)
+            if (i >= w.skip) p[w.at + i] = T(v[i]);
+    }
+}
+
 // Over 2^k lanes that lie side by side; every one of them gets the sum.
 template <int LANES, class F>
 __device__ __forceinline__ F sum_lanes(F s) {
