@@ -3,16 +3,21 @@
 //
 // The gradient sorts the tokens by id first, keeping their order among equal
 // ids, so that a row's sum runs over neighbours in the sorted order and no two
-// workgroups add to the same row: no atomics, and the same bits every run.
-//   k_tiles   1024 ids of a workgroup sorted
-//   k_merge   up to kFan sorted runs at a time made one: an id's place is its
-//             own in its run plus, for each other run, how many lie before it
-//   k_sum     units of kUnit sorted tokens: an id's sum over its tokens there.  An
-//             id whose tokens go over a unit's ends leaves partial sums
-//   k_join    adds these up
-//   k_absent  zeros for the rows that no id names
+// workgroups add to the same row: no float atomics, and the same bits every run.
+//   k_sort_one            up to kOne tokens: all passes of a radix sort in LDS
+//   k_count, k_scatter    more: a pass for each digit of the ids.  k_count finds
+//                         the first digit's counts tile by tile, each k_scatter
+//                         those of the next on its way (of whole numbers: their
+//                         order does not matter)
+//   k_scan                for many tiles, the counts of the tiles before each
+//   k_sum                 units of sorted tokens: an id's sum over its tokens there.
+//                         An id whose tokens go over a unit's ends leaves partial
+//                         sums.  In the same launch zeros for the rows that no id names
+//   k_join                adds the partial sums up
 #include <algorithm>
+#include <type_traits>
 
+#include "launch_grid.hpp"
 #include "tokens.hpp"
 
 using namespace dgc::tokens;
@@ -21,11 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kMostBlocks = 1 << 20;  // of a launch: workgroups take what is left in turn
-constexpr int kTile = 1024, kSub = 256;
-constexpr int kFan = 32;
-constexpr int kUnit = 32;
-constexpr int kAhead = 8;                 // tokens whose rows are under way together
-constexpr int64_t kFillBytes = 64 << 10;  // of a workgroup's rows in k_absent
 
 struct Lookup {
     int64_t m, vocab, d;
@@ -64,6 +64,265 @@ __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
 
 // ------------------------------------------------------------------ sorting
 
+constexpr int kSorters = 1024;            // threads of a sorting workgroup
+constexpr int kSortWaves = kSorters / 64;
+constexpr int kEach = 2;                  // tokens of a thread in k_scatter
+constexpr int64_t kTile = kSorters * kEach;
+constexpr int kOneEach = 4;               // ... at most in k_sort_one
+constexpr int64_t kOne = kSorters * kOneEach;
+constexpr int kMostBits = 9, kMostBins = 1 << kMostBits;  // of a digit
+constexpr int64_t kFewTiles = 128;        // whose counts each workgroup of k_scatter adds up by itself
+
+struct Sort {
+    int64_t m, vocab, tiles;
+    int wide_index;
+    const void* ids;                // first pass: the keys; padding is `vocab`, behind all ids
+    const uint32_t *key, *pos;      // later passes
+    uint32_t *key_out, *pos_out;
+    int shift, bits, next_bits;     // of this pass's digit; next_bits 0: the last pass
+    uint32_t *count, *next, *clear;  // [tiles + 1][bins] of this pass, the next and the one after
+    int scanned;                    // count holds the tiles' before each, and all of them last
+};
+
+__device__ __forceinline__ uint32_t key_of(const Sort& a, int64_t i) {
+    if (!a.ids) return a.key[i];
+    const int64_t id = id_at(a.ids, a.wide_index, i);
+    return id >= 0 && id < a.vocab ? uint32_t(id) : uint32_t(a.vocab);
+}
+
+// What a sorting workgroup has in LDS.
+struct Bins {
+    uint32_t wave[kSortWaves][kMostBins];  // each wave's counts, then what lies before it in the workgroup
+    uint32_t base[kMostBins];              // where a bin begins
+    uint32_t sums[kMostBins / 64];
+};
+
+// How many of the tokens before it in its wave have a token's digit.  A wave's
+// tokens are its rounds of 64 in a row; its counts in LDS go along.
+template <int E>
+__device__ __forceinline__ void rank_in_wave(Bins& b, const uint32_t* digit, const bool* on, int rounds, int bits,
+                                             uint32_t* rank) {
+    uint32_t* const count = b.wave[threadIdx.x >> 6];
+    const uint64_t before = (uint64_t(1) << (threadIdx.x & 63)) - 1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e >= rounds) break;
+        uint64_t same = __ballot(on[e]);
+        for (int i = 0; i < bits; ++i) {
+            const uint64_t set = __ballot(digit[e] >> i & 1);
+            same &= digit[e] >> i & 1 ? set : ~set;
+        }
+        const uint32_t old = count[digit[e]];
+        rank[e] = old + __popcll(same & before);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (on[e] && (same & before) == 0) count[digit[e]] = old + __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+__device__ __forceinline__ void clear_counts(Bins& b, int bins) {
+    for (int i = threadIdx.x; i < kSortWaves * bins; i += kSorters) b.wave[i / bins][i % bins] = 0;
+}
+
+// Each wave's counts become the sum of those before it.  Returns, to thread i, bin
+// i's count.
+__device__ __forceinline__ uint32_t scan_waves(Bins& b, int bins) {
+    uint32_t s = 0;
+    if (int(threadIdx.x) < bins)
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) {
+            const uint32_t c = b.wave[w][threadIdx.x];
+            b.wave[w][threadIdx.x] = s;
+            s += c;
+        }
+    return s;
+}
+
+// The sum of the bins' counts before each bin, to thread i that of bin i.
+__device__ __forceinline__ uint32_t scan_bins(Bins& b, uint32_t count, int bins) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t s = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t below = __shfl_up(s, d);
+        if (lane >= d) s += below;
+    }
+    if (lane == 63 && int(threadIdx.x) < kMostBins) b.sums[wave] = s;
+    __syncthreads();
+    if (int(threadIdx.x) < bins)
+        for (int w = 0; w < wave; ++w) s += b.sums[w];
+    return s - count;
+}
+
+__global__ __launch_bounds__(kSorters) void k_sort_one(Sort a, int whole_bits, int digit_bits) {
+    __shared__ Bins b;
+    __shared__ uint32_t keys[kOne];
+    __shared__ uint16_t places[kOne];
+    const int rounds = int((a.m + kSorters - 1) / kSorters), first = (threadIdx.x >> 6) * 64 * rounds + (threadIdx.x & 63);
+    uint32_t key[kOneEach], pos[kOneEach], digit[kOneEach], rank[kOneEach];
+    bool on[kOneEach];
+#pragma unroll
+    for (int e = 0; e < kOneEach; ++e) {
+        const int i = first + e * 64;
+        on[e] = e < rounds && i < a.m;
+        pos[e] = uint32_t(i);
+        key[e] = on[e] ? key_of(a, i) : 0;
+    }
+    for (int shift = 0; shift < whole_bits; shift += digit_bits) {
+        const int bits = whole_bits - shift < digit_bits ? whole_bits - shift : digit_bits, bins = 1 << bits;
+        clear_counts(b, bins);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kOneEach; ++e) digit[e] = key[e] >> shift & (bins - 1);
+        rank_in_wave<kOneEach>(b, digit, on, rounds, bits, rank);
+        __syncthreads();
+        const uint32_t count = scan_waves(b, bins), base = scan_bins(b, count, bins);
+        if (int(threadIdx.x) < bins) b.base[threadIdx.x] = base;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kOneEach; ++e)
+            if (on[e]) {
+                const uint32_t to = b.base[digit[e]] + b.wave[threadIdx.x >> 6][digit[e]] + rank[e];
+                keys[to] = key[e];
+                places[to] = uint16_t(pos[e]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kOneEach; ++e)
+            if (on[e]) {
+                key[e] = keys[first + e * 64];
+                pos[e] = places[first + e * 64];
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < kOneEach; ++e)
+        if (on[e]) {
+            a.key_out[first + e * 64] = key[e];
+            a.pos_out[first + e * 64] = pos[e];
+        }
+}
+
+__device__ __forceinline__ void clear_bins(uint32_t* p, int64_t tile) {
+    if (p)
+        for (int i = threadIdx.x; i < kMostBins; i += kSorters) p[tile * kMostBins + i] = 0;
+}
+
+__global__ __launch_bounds__(kSorters) void k_count(Sort a) {
+    __shared__ uint32_t count[kMostBins];
+    const int64_t tile = blockIdx.x, first = tile * kTile;
+    for (int i = threadIdx.x; i < kMostBins; i += kSorters) count[i] = 0;
+    clear_bins(a.next, tile);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int64_t i = first + e * kSorters + threadIdx.x;
+        if (i < a.m) atomicAdd(&count[key_of(a, i) >> a.shift & ((1 << a.bits) - 1)], 1u);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kMostBins; i += kSorters) a.count[tile * kMostBins + i] = count[i];
+}
+
+// 64 bins over all tiles: a wave adds up a 16th of the tiles, then writes what lies
+// before each of them; all tiles' sums behind the last.
+__global__ __launch_bounds__(kSorters) void k_scan(uint32_t* count, int64_t tiles) {
+    __shared__ uint32_t sums[kSortWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t* const p = count + blockIdx.x * 64 + lane;
+    const int64_t share = (tiles + kSortWaves - 1) / kSortWaves, from = wave * share;
+    const int64_t to = from + share < tiles ? from + share : tiles;
+    uint32_t s = 0;
+#pragma unroll 8
+    for (int64_t t = from; t < to; ++t) s += p[t * kMostBins];
+    sums[wave][lane] = s;
+    __syncthreads();
+    s = 0;
+    for (int w = 0; w < wave; ++w) s += sums[w][lane];
+#pragma unroll 8
+    for (int64_t t = from; t < to; ++t) {
+        const uint32_t c = p[t * kMostBins];
+        p[t * kMostBins] = s;
+        s += c;
+    }
+    if (wave == kSortWaves - 1) p[tiles * kMostBins] = s;
+}
+
+__global__ __launch_bounds__(kSorters) void k_scatter(Sort a) {
+    __shared__ Bins b;
+    const int bins = 1 << a.bits;
+    const int64_t tile = blockIdx.x;
+    const int64_t first = tile * kTile + (threadIdx.x >> 6) * 64 * kEach + (threadIdx.x & 63);
+    uint32_t key[kEach], pos[kEach], digit[kEach], rank[kEach];
+    bool on[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int64_t i = first + e * 64;
+        on[e] = i < a.m;
+        key[e] = on[e] ? key_of(a, i) : 0;
+        pos[e] = on[e] && !a.ids ? a.pos[i] : uint32_t(i);
+        digit[e] = key[e] >> a.shift & (bins - 1);
+    }
+    clear_bins(a.clear, tile);
+    clear_counts(b, bins);
+    // all tiles' counts of a bin, and those of the tiles before this one
+    uint32_t all = 0, before = 0;
+    if (int(threadIdx.x) < bins) {
+        const uint32_t* const p = a.count + threadIdx.x;
+        if (a.scanned) {
+            all = p[a.tiles * kMostBins];
+            before = p[tile * kMostBins];
+        } else {
+#pragma unroll 16
+            for (int64_t t = 0; t < a.tiles; ++t) {
+                const uint32_t c = p[t * kMostBins];
+                all += c;
+                before += t < tile ? c : 0;
+            }
+        }
+    }
+    __syncthreads();
+    rank_in_wave<kEach>(b, digit, on, kEach, a.bits, rank);
+    __syncthreads();
+    scan_waves(b, bins);
+    const uint32_t base = scan_bins(b, all, bins) + before;
+    if (int(threadIdx.x) < bins) b.base[threadIdx.x] = base;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+        if (on[e]) {
+            const uint32_t to = b.base[digit[e]] + b.wave[threadIdx.x >> 6][digit[e]] + rank[e];
+            a.key_out[to] = key[e];
+            a.pos_out[to] = pos[e];
+            if (a.next_bits)
+                atomicAdd(&a.next[int64_t(to / kTile) * kMostBins + (key[e] >> (a.shift + a.bits) & ((1 << a.next_bits) - 1))],
+                          1u);
+        }
+}
+
+// ------------------------------------------------------------------- adding
+
+constexpr int kAhead = 8;                  // tokens whose rows are under way together
+constexpr int kMostUnit = 32;              // sorted tokens of a unit, at most
+constexpr int kLeastAcross = 8;            // lanes side by side on a row, at least
+constexpr int kMostUnits = kThreads / kLeastAcross;  // of a workgroup
+constexpr int64_t kFillBytes = 64 << 10;   // of a workgroup's rows without a name
+
+struct Sums {
+    int64_t m, vocab, d;
+    const uint32_t *key, *pos;
+    const void* dy;
+    int64_t lddy;
+    float scale;
+    int accumulate;
+    void* dtable;
+    int64_t lddt;
+    float* part;  // [units][2][d]: of an id that came from before the unit, and of one that goes on behind it
+    int unit;     // sorted tokens of a unit
+    int64_t units;
+    int across;            // lanes side by side on a row, a power of two
+    int64_t spans, tasks;  // of `across` lanes' columns in a row; of all units together
+    int64_t rows, fills;   // rows of a workgroup that fills, and such workgroups
+};
+
 // How many of n ascending numbers are below k.
 __device__ __forceinline__ int64_t below(const uint32_t* p, int64_t n, uint32_t k) {
     int64_t lo = 0;
@@ -79,211 +338,241 @@ __device__ __forceinline__ int64_t below(const uint32_t* p, int64_t n, uint32_t 
     return lo;
 }
 
-struct Sort {
-    int64_t m, vocab;
-    int wide_index;
-    const void* ids;
-    uint32_t* key;  // ids in order; padding is `vocab`, behind all others
-    uint32_t* pos;  // the tokens that they are of
+// C columns of a lane: 4, where they come to 16 bytes of binary32 (stores that lie
+// side by side), or 8.
+template <class T, int C>
+struct Some {
+    T t[C];
 };
 
-constexpr uint32_t kBehind = 0x80000000u;  // more than any key
-
-__global__ __launch_bounds__(kTile) void k_tiles(Sort a) {
-    __shared__ uint32_t key[2][kTile];
-    __shared__ uint16_t pos[2][kTile];
-    const int i = threadIdx.x, sub = i / kSub * kSub;
-    const int64_t first = int64_t(blockIdx.x) * kTile;
-    uint32_t k = kBehind;
-    if (first + i < a.m) {
-        const int64_t id = id_at(a.ids, a.wide_index, first + i);
-        k = id >= 0 && id < a.vocab ? uint32_t(id) : uint32_t(a.vocab);
-    }
-    key[0][i] = k;
-    __syncthreads();
-    // the place among 256, by counting; equal ones keep their order
-    int rank = sub;
-    for (int j = 0; j < kSub; j += 4) {
-        const u32x4 q = *reinterpret_cast<const u32x4*>(&key[0][sub + j]);
+// TINY: rows of fewer than C columns, which one lane reads one by one.  Else a lane
+// whose columns go over the row's end begins before them: see Span.
+template <bool TINY, class T, int C>
+__device__ __forceinline__ Some<T, C> get(const T* row, const Span& w, int64_t d) {
+    Some<T, C> s;
+    if constexpr (TINY) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rank += q[e] < k + (sub + j + e < i);
-    }
-    key[1][rank] = k;
-    pos[1][rank] = uint16_t(i);
-    __syncthreads();
-    // the place among the four sorted quarters
-    k = key[1][i];
-    rank = i - sub;
-    for (int s = 0; s < kTile; s += kSub)
-        if (s != sub) rank += int(below(&key[1][s], kSub, k + (s < sub)));
-    key[0][rank] = k;
-    pos[0][rank] = pos[1][i];
-    __syncthreads();
-    if (first + i < a.m) {
-        a.key[first + i] = key[0][i];
-        a.pos[first + i] = uint32_t(first + pos[0][i]);
-    }
-}
-
-struct Merge {
-    int64_t m, run;  // runs of so many
-    const uint32_t *key, *pos;
-    uint32_t *key_out, *pos_out;
-};
-
-__global__ __launch_bounds__(kThreads) void k_merge(Merge a) {
-    const int64_t runs = (a.m + a.run - 1) / a.run;
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < a.m; i += int64_t(gridDim.x) * kThreads) {
-        const int64_t r = i / a.run, first = r / kFan * kFan, last = first + kFan < runs ? first + kFan : runs;
-        const uint32_t k = a.key[i];
-        int64_t rank = i - r * a.run;
-        for (int64_t s = first; s < last; ++s) {
-            const int64_t at = s * a.run, n = a.m - at < a.run ? a.m - at : a.run;
-            if (s != r) rank += below(a.key + at, n, k + (s < r));
+        for (int i = 0; i < C; ++i) s.t[i] = i < d ? row[i] : T(0.0f);
+    } else {
+        constexpr int kBytes = C * int(sizeof(T));
+        if constexpr (kBytes == 8) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef u32x2 V __attribute__((aligned(2), may_alias));
+            const u32x2 v = *reinterpret_cast<const V*>(row + w.at);
+            __builtin_memcpy(s.t, &v, 8);
+        } else {
+            typedef typename At<sizeof(T)>::V V;
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const u32x4 v = reinterpret_cast<const V*>(row + w.at)[i];
+                __builtin_memcpy(s.t + i * (16 / sizeof(T)), &v, 16);
+            }
         }
-        a.key_out[first * a.run + rank] = k;
-        a.pos_out[first * a.run + rank] = a.pos[i];
+    }
+    return s;
+}
+
+template <bool TINY, class T, int C>
+__device__ __forceinline__ void put(T* row, const Span& w, int64_t d, const float* v) {
+    if (!TINY && w.skip == 0) {
+        constexpr int kBytes = C * int(sizeof(T));
+        T t[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) t[i] = T(v[i]);
+        if constexpr (kBytes == 8) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef u32x2 V __attribute__((aligned(2), may_alias));
+            u32x2 x;
+            __builtin_memcpy(&x, t, 8);
+            *reinterpret_cast<V*>(row + w.at) = x;
+        } else {
+            typedef typename At<sizeof(T)>::V V;
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                u32x4 x;
+                __builtin_memcpy(&x, t + i * (16 / sizeof(T)), 16);
+                reinterpret_cast<V*>(row + w.at)[i] = x;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (TINY ? i < d : i >= w.skip) row[w.at + i] = T(v[i]);
     }
 }
 
-// ------------------------------------------------------------------- adding
-
-struct Sums {
-    int64_t m, vocab, d;
-    const uint32_t *key, *pos;
-    const void* dy;
-    int64_t lddy;
-    float scale;
-    int accumulate;
-    void* dtable;
-    int64_t lddt;
-    float* part;  // [units][2][d]: of an id that came from before the unit, and of one that goes on behind it
-    int64_t units;
-    int across;
-    int64_t spans, tasks;
-    int64_t rows;  // of a workgroup in k_absent
-};
-
-template <class G>
-__device__ __forceinline__ void finish8(const Sums& a, uint32_t id, int64_t c, int valid, const float* sum) {
-    G* const p = static_cast<G*>(a.dtable) + int64_t(id) * a.lddt + c;
-    float v[kRow], old[kRow];
-    if (a.accumulate) load8(p, valid, old);
-#pragma unroll
-    for (int i = 0; i < kRow; ++i) v[i] = a.accumulate ? old[i] + a.scale * sum[i] : a.scale * sum[i];
-    store8(p, valid, v);
+// The span of C columns from c on.
+template <bool TINY, int C>
+__device__ __forceinline__ Span columns(int64_t d, int64_t c) {
+    if (TINY) return {0, c == 0 ? 0 : C};
+    const int64_t at = c + C <= d ? c : d - C;
+    return {at, c - at < C ? int(c - at) : C};
 }
 
-template <class T, class G>
+template <bool TINY, class G, int C>
+__device__ __forceinline__ void finish(const Sums& a, uint32_t id, const Span& w, const float* sum) {
+    if (w.skip >= C) return;
+    G* const row = static_cast<G*>(a.dtable) + int64_t(id) * a.lddt;
+    float v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = a.scale * sum[i];
+    if (a.accumulate) {
+        const Some<G, C> old = get<TINY, G, C>(row, w, a.d);
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] += float(old.t[i]);
+    }
+    put<TINY, G, C>(row, w, a.d, v);
+}
+
+template <bool TINY, int C>
+__device__ __forceinline__ void leave(const Sums& a, int64_t unit, int which, const Span& w, const float* sum) {
+    if (w.skip < C) put<TINY, float, C>(a.part + (unit * 2 + which) * a.d, w, a.d, sum);
+}
+
+// Zeros for rows that no id names.
+template <class G>
+__device__ __forceinline__ void fill(const Sums& a, int64_t chunk, uint32_t* named) {
+    const int64_t first = chunk * a.rows;
+    const int count = int(a.vocab - first < a.rows ? a.vocab - first : a.rows);
+    if (int(threadIdx.x) < count) {
+        const uint32_t mine = uint32_t(first + threadIdx.x);
+        const int64_t at = below(a.key, a.m, mine);
+        named[threadIdx.x] = at < a.m && a.key[at] == mine;
+    }
+    __syncthreads();
+    constexpr int kWide = 16 / sizeof(G);
+    const float zero[8] = {};
+    for (int r = 0; r < count; ++r) {
+        if (named[r]) continue;
+        G* const row = static_cast<G*>(a.dtable) + (first + r) * a.lddt;
+        for (int64_t c = threadIdx.x * kWide; c < a.d; c += kThreads * kWide) {
+            if (c + kWide <= a.d)
+                put<false, G, kWide>(row, {c, 0}, a.d, zero);
+            else
+                for (int64_t i = c; i < a.d; ++i) row[i] = G(0.0f);
+        }
+    }
+}
+
+template <class T, class G, int C, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_sum(Sums a) {
+    __shared__ uint32_t key[kMostUnits][kMostUnit + 2], pos[kMostUnits][kMostUnit];
+    const int64_t block = dgc::block_number();
+    if (block >= a.tasks) {
+        if (block < a.tasks + a.fills) fill<G>(a, block - a.tasks, &key[0][0]);
+        return;
+    }
     const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, each = kThreads / a.across;
-    for (int64_t task = blockIdx.x; task < a.tasks; task += gridDim.x) {
-        const int64_t u = task / a.spans * each + ty, c = (task % a.spans * a.across + tx) * kRow;
-        const int valid = valid_of(a.d, c);
-        if (u >= a.units || valid == 0) continue;
-        const int64_t begin = u * kUnit, end = begin + kUnit < a.m ? begin + kUnit : a.m;
-        uint32_t id = a.key[begin];
-        bool before = begin > 0 && a.key[begin - 1] == id;
-        float sum[kRow] = {};
-        float* const part = a.part + u * 2 * a.d + c;
-        for (int64_t t = begin; t < end; t += kAhead) {
-            Eight<T> row[kAhead];
-            uint32_t key[kAhead];
+    const int64_t first = block / a.spans * each;
+    const Span w = columns<TINY, C>(a.d, (block % a.spans * a.across + tx) * C);
+    // the units' ids, with one before and one behind, and tokens; what there is not is an
+    // id behind all others, of a token that is there
+    for (int i = threadIdx.x; i < each * (a.unit + 2); i += kThreads) {
+        const int u = i / (a.unit + 2), j = i % (a.unit + 2);
+        const int64_t at = (first + u) * a.unit + j - 1;
+        const bool there = at >= 0 && at < a.m;
+        key[u][j] = there ? a.key[at] : 0xFFFFFFFFu;
+        if (j > 0 && j <= a.unit) pos[u][j - 1] = there ? a.pos[at] : 0;
+    }
+    __syncthreads();
+    const int64_t unit = first + ty;
+    if (unit >= a.units) return;
+    uint32_t id = key[ty][1];
+    bool before = key[ty][0] == id;
+    float sum[C] = {};
+    const T* const dy = static_cast<const T*>(a.dy);
+    Some<T, C> row[kAhead], next[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                key[j] = t + j < end ? a.key[t + j] : uint32_t(a.vocab);
-                const int64_t from = t + j < end ? a.pos[t + j] : a.pos[begin];
-                row[j] = read8(static_cast<const T*>(a.dy) + from * a.lddy + c, valid);
-            }
+    for (int j = 0; j < kAhead; ++j) row[j] = get<TINY, T, C>(dy + int64_t(pos[ty][j]) * a.lddy, w, a.d);
+    for (int t = 0; t < a.unit; t += kAhead) {
+        const int then = t + kAhead < a.unit ? t + kAhead : t;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (key[j] != id) {
-                    if (t + j < end) {
-                        if (id < a.vocab) {
-                            if (before)
-                                store8(part, valid, sum);
-                            else
-                                finish8<G>(a, id, c, valid, sum);
-                        }
-                        before = false;
-                        id = key[j];
+        for (int j = 0; j < kAhead; ++j) next[j] = get<TINY, T, C>(dy + int64_t(pos[ty][then + j]) * a.lddy, w, a.d);
 #pragma unroll
-                        for (int i = 0; i < kRow; ++i) sum[i] = 0.0f;
-                    }
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t now = key[ty][t + j + 1];
+            if (now != id) {
+                if (id < a.vocab) {
+                    if (before)
+                        leave<TINY, C>(a, unit, 0, w, sum);
+                    else
+                        finish<TINY, G, C>(a, id, w, sum);
                 }
-                float v[kRow];
-                widen(row[j], v);
-                if (t + j < end)
+                before = false;
+                id = now;
 #pragma unroll
-                    for (int i = 0; i < kRow; ++i) sum[i] += v[i];
+                for (int i = 0; i < C; ++i) sum[i] = 0.0f;
             }
+#pragma unroll
+            for (int i = 0; i < C; ++i) sum[i] += float(row[j].t[i]);
         }
-        if (id >= a.vocab) continue;
-        if (before)
-            store8(part, valid, sum);
-        else if (end < a.m && a.key[end] == id)
-            store8(part + a.d, valid, sum);
-        else
-            finish8<G>(a, id, c, valid, sum);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) row[j] = next[j];
     }
+    if (id >= a.vocab) return;
+    if (before)
+        leave<TINY, C>(a, unit, 0, w, sum);
+    else if (key[ty][a.unit + 1] == id)
+        leave<TINY, C>(a, unit, 1, w, sum);
+    else
+        finish<TINY, G, C>(a, id, w, sum);
 }
 
-// The id whose tokens begin in unit u and go on behind it, over all units that it
+// The id whose tokens begin in a unit and go on behind it, over all units that it
 // reaches.
-template <class G>
+template <class G, int C, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_join(Sums a) {
+    constexpr int kTogether = 16;  // partial sums under way together
     const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, each = kThreads / a.across;
-    for (int64_t task = blockIdx.x; task < a.tasks; task += gridDim.x) {
-        const int64_t u = task / a.spans * each + ty, c = (task % a.spans * a.across + tx) * kRow;
-        const int valid = valid_of(a.d, c);
-        const int64_t begin = u * kUnit, end = begin + kUnit;
-        if (end >= a.m || valid == 0) continue;
-        const uint32_t id = a.key[end - 1];
-        if (id >= a.vocab || a.key[end] != id) continue;
-        if (a.key[begin] == id && begin > 0 && a.key[begin - 1] == id) continue;  // begins earlier
-        const int64_t last = (end + below(a.key + end, a.m - end, id + 1) - 1) / kUnit;
-        double sum[kRow];
-        float v[kRow];
-        load8(a.part + (u * 2 + 1) * a.d + c, valid, v);
+    const int64_t block = dgc::block_number();
+    if (block >= a.tasks) return;
+    const int64_t u = block / a.spans * each + ty, begin = u * a.unit, end = begin + a.unit;
+    const Span w = columns<TINY, C>(a.d, (block % a.spans * a.across + tx) * C);
+    if (end >= a.m) return;
+    const uint32_t id = a.key[end - 1];
+    if (id >= a.vocab || a.key[end] != id) return;
+    if (a.key[begin] == id && begin > 0 && a.key[begin - 1] == id) return;  // begins earlier
+    const int64_t last = (end + below(a.key + end, a.m - end, id + 1) - 1) / a.unit;
+    const Some<float, C> mine = get<TINY, float, C>(a.part + (u * 2 + 1) * a.d, w, a.d);
+    double sum[C];
 #pragma unroll
-        for (int i = 0; i < kRow; ++i) sum[i] = double(v[i]);
-#pragma unroll 4
-        for (int64_t w = u + 1; w <= last; ++w) {
-            load8(a.part + w * 2 * a.d + c, valid, v);
+    for (int i = 0; i < C; ++i) sum[i] = double(mine.t[i]);
+    for (int64_t v = u + 1; v <= last; v += kTogether) {
+        Some<float, C> p[kTogether];
 #pragma unroll
-            for (int i = 0; i < kRow; ++i) sum[i] += double(v[i]);
-        }
+        for (int k = 0; k < kTogether; ++k)
+            p[k] = get<TINY, float, C>(a.part + (v + k <= last ? v + k : last) * 2 * a.d, w, a.d);
 #pragma unroll
-        for (int i = 0; i < kRow; ++i) v[i] = float(sum[i]);
-        finish8<G>(a, id, c, valid, v);
+        for (int k = 0; k < kTogether; ++k)
+            if (v + k <= last)
+#pragma unroll
+                for (int i = 0; i < C; ++i) sum[i] += double(p[k].t[i]);
     }
-}
-
-template <class G>
-__global__ __launch_bounds__(kThreads) void k_absent(Sums a) {
-    __shared__ uint8_t named[kThreads];
-    const int64_t chunks = (a.vocab + a.rows - 1) / a.rows;
-    for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-        const int64_t first = chunk * a.rows, mine = first + threadIdx.x;
-        const int count = int(a.vocab - first < a.rows ? a.vocab - first : a.rows);
-        __syncthreads();
-        if (int(threadIdx.x) < count) {
-            const int64_t at = below(a.key, a.m, uint32_t(mine));
-            named[threadIdx.x] = at < a.m && a.key[at] == uint32_t(mine);
-        }
-        __syncthreads();
-        const float zero[kRow] = {};
-        for (int r = 0; r < count; ++r)
-            if (!named[r])
-                for (int64_t c = threadIdx.x * kRow; c < a.d; c += kThreads * kRow)
-                    store8(static_cast<G*>(a.dtable) + (first + r) * a.lddt + c, valid_of(a.d, c), zero);
-    }
+    float out[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) out[i] = float(sum[i]);
+    finish<TINY, G, C>(a, id, w, out);
 }
 
 // --------------------------------------------------------------------- host
 
+int bit_length(int64_t v) {
+    int bits = 1;
+    while (v >> bits) ++bits;
+    return bits;
+}
+
+int across_of(int64_t d, int columns, int least) {
+    int across = kThreads;
+    while (across > least && int64_t(across) / 2 * columns >= d) across /= 2;
+    return across;
+}
+
+// Sorted tokens of a unit: fewer, a multiple of kAhead, where there are few tokens.
+int unit_of(int64_t m) { return m < 8192 ? 8 : kMostUnit; }
+
 struct Space {
-    size_t key[2], pos[2], part, total;
+    size_t key[2], pos[2], count[3], part, total;
 };
 
 Space space(int64_t m, int64_t d) {
@@ -294,15 +583,58 @@ Space space(int64_t m, int64_t d) {
         s.pos[i] = s.total + list;
         s.total += 2 * list;
     }
+    if (m > kOne)
+        for (size_t& c : s.count) {
+            c = s.total;
+            s.total += round_up(size_t(cdiv(m, kTile) + 1) * kMostBins * 4);
+        }
     s.part = s.total;
-    if (m > kUnit) s.total += round_up(size_t(cdiv(m, kUnit)) * 2 * size_t(d) * 4);
+    if (m > unit_of(m)) s.total += round_up(size_t(cdiv(m, unit_of(m))) * 2 * size_t(d) * 4);
     return s;
 }
 
-int across_of(int64_t d) {
-    int across = kThreads;
-    while (across > 1 && across / 2 * kRow >= d) across /= 2;
-    return across;
+// Sorts the tokens into one of the two lists; returns which.
+int sort(const dgc_embedding_backward_args& a, char* ws, const Space& sp, hipStream_t stream) {
+    uint32_t *key[2], *pos[2], *count[3];
+    for (int i = 0; i < 2; ++i) {
+        key[i] = reinterpret_cast<uint32_t*>(ws + sp.key[i]);
+        pos[i] = reinterpret_cast<uint32_t*>(ws + sp.pos[i]);
+    }
+    for (int i = 0; i < 3; ++i) count[i] = reinterpret_cast<uint32_t*>(ws + sp.count[i]);
+    const int whole = bit_length(a.vocab), passes = (whole + kMostBits - 1) / kMostBits;
+    const int bits = (whole + passes - 1) / passes;
+    Sort s{};
+    s.m = a.m;
+    s.vocab = a.vocab;
+    s.tiles = cdiv(a.m, kTile);
+    s.wide_index = a.index_type == DGC_INT64;
+    s.ids = a.ids;
+    s.key_out = key[0];
+    s.pos_out = pos[0];
+    if (a.m <= kOne) {
+        k_sort_one<<<1, kSorters, 0, stream>>>(s, whole, bits);
+        return 0;
+    }
+    int out = 0;
+    for (int pass = 0; pass < passes; ++pass, out ^= 1) {
+        s.shift = pass * bits;
+        s.bits = std::min(bits, whole - s.shift);
+        s.next_bits = std::max(0, std::min(bits, whole - s.shift - s.bits));
+        s.count = count[pass % 3];
+        s.next = count[(pass + 1) % 3];
+        s.clear = count[(pass + 2) % 3];
+        s.key_out = key[out];
+        s.pos_out = pos[out];
+        const dim3 grid(unsigned(s.tiles));
+        if (pass == 0) k_count<<<grid, kSorters, 0, stream>>>(s);
+        s.scanned = s.tiles > kFewTiles;
+        if (s.scanned) k_scan<<<kMostBins / 64, kSorters, 0, stream>>>(s.count, s.tiles);
+        k_scatter<<<grid, kSorters, 0, stream>>>(s);
+        s.ids = nullptr;
+        s.key = key[out];
+        s.pos = pos[out];
+    }
+    return out ^ 1;
 }
 
 dim3 grid(int64_t tasks) { return dim3(unsigned(std::min(tasks, kMostBlocks))); }
@@ -328,7 +660,7 @@ int dgc_embedding(const dgc_embedding_args* a, hipStream_t stream) {
         return DGC_EINVAL;
     if (m == 0 || d == 0) return DGC_OK;
     Lookup k{m, a->vocab, d, a->index_type == DGC_INT64, a->ids, a->table, a->ldt, float(a->scale), a->y, a->ldy,
-             across_of(d), 0, 0};
+             across_of(d, kRow, 1), 0, 0};
     k.spans = cdiv(d, int64_t(k.across) * kRow);
     k.tasks = k.spans * cdiv(m, kThreads / k.across);
     return with_type(a->type, [&](auto t) {
@@ -353,34 +685,42 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
     if (rc != DGC_OK) return rc;
     if (vocab == 0 || d == 0 || (m == 0 && a->accumulate)) return DGC_OK;
     char* const ws = static_cast<char*>(workspace);
-    uint32_t *key[2], *pos[2];
-    for (int i = 0; i < 2; ++i) {
-        key[i] = reinterpret_cast<uint32_t*>(ws + sp.key[i]);
-        pos[i] = reinterpret_cast<uint32_t*>(ws + sp.pos[i]);
-    }
-    int in = 0;
-    if (m > 0) {
-        const Sort s{m, vocab, a->index_type == DGC_INT64, a->ids, key[0], pos[0]};
-        k_tiles<<<dim3(unsigned(cdiv(m, kTile))), kTile, 0, stream>>>(s);
-        for (int64_t run = kTile; run < m; run *= kFan, in ^= 1)
-            k_merge<<<grid(cdiv(m, kThreads)), kThreads, 0, stream>>>(
-                Merge{m, run, key[in], pos[in], key[in ^ 1], pos[in ^ 1]});
-    }
-    Sums k{m, vocab, d, key[in], pos[in], a->dy, a->lddy, float(a->scale), int(a->accumulate), a->dtable, a->lddt,
-           reinterpret_cast<float*>(ws + sp.part), cdiv(m, kUnit), across_of(d), 0, 0, 0};
-    k.spans = cdiv(d, int64_t(k.across) * kRow);
-    k.tasks = k.spans * cdiv(k.units, kThreads / k.across);
+    const int in = m > 0 ? sort(*a, ws, sp, stream) : 0;
+    Sums k{};
+    k.m = m;
+    k.vocab = vocab;
+    k.d = d;
+    k.key = reinterpret_cast<const uint32_t*>(ws + sp.key[in]);
+    k.pos = reinterpret_cast<const uint32_t*>(ws + sp.pos[in]);
+    k.dy = a->dy;
+    k.lddy = a->lddy;
+    k.scale = float(a->scale);
+    k.accumulate = int(a->accumulate);
+    k.dtable = a->dtable;
+    k.lddt = a->lddt;
+    k.part = reinterpret_cast<float*>(ws + sp.part);
+    k.unit = unit_of(m);
+    k.units = cdiv(m, k.unit);
     k.rows = std::max<int64_t>(1, std::min<int64_t>(kThreads, kFillBytes / (d * gsize)));
+    k.fills = k.accumulate ? 0 : cdiv(vocab, k.rows);
     return with_type(a->type, [&](auto t) {
         typedef decltype(t) T;
-        const auto with = [&](auto g) {
+        const auto with = [&](auto g, auto tiny) {
             typedef decltype(g) G;
-            if (!k.accumulate) k_absent<G><<<grid(cdiv(vocab, k.rows)), kThreads, 0, stream>>>(k);
-            if (m > 0) k_sum<T, G><<<grid(k.tasks), kThreads, 0, stream>>>(k);
-            if (m > kUnit) k_join<G><<<grid(k.tasks), kThreads, 0, stream>>>(k);
+            constexpr int C = sizeof(G) == 4 ? 4 : 8;
+            constexpr bool TINY = decltype(tiny)::value;
+            k.across = across_of(d, C, kLeastAcross);
+            k.spans = cdiv(d, int64_t(k.across) * C);
+            k.tasks = k.spans * cdiv(k.units, kThreads / k.across);
+            const int64_t blocks = k.tasks + k.fills;
+            k_sum<T, G, C, TINY><<<dgc::grid_of(blocks, kThreads), kThreads, 0, stream>>>(k);
+            if (k.units > 1) k_join<G, C, TINY><<<dgc::grid_of(k.tasks, kThreads), kThreads, 0, stream>>>(k);
             return launched();
         };
-        return a->grad_type == DGC_FP32 ? with(float()) : with(t);
+        const auto sized = [&](auto g) {
+            return d < (sizeof(g) == 4 ? 4 : 8) ? with(g, std::true_type()) : with(g, std::false_type());
+        };
+        return a->grad_type == DGC_FP32 ? sized(float()) : sized(t);
     });
 }
 
