@@ -48,7 +48,21 @@ __device__ __forceinline__ void philox(uint32_t* c, uint32_t k0, uint32_t k1) {
     }
 }
 
-template <class T>
+// v: 8 elements of row r from column 8 * group on, residual: what is added to them.
+template <bool RESIDUAL>
+__device__ __forceinline__ void drop8(const Args& a, uint64_t offset, int64_t r, int64_t group, float* v,
+                                      const float* residual) {
+    uint32_t bits[4] = {uint32_t(group), uint32_t(r), uint32_t(offset), uint32_t(offset >> 32)};
+    philox(bits, uint32_t(a.seed), uint32_t(a.seed >> 32));
+#pragma unroll
+    for (int i = 0; i < kRow; ++i) {
+        const uint32_t u = i % 2 ? bits[i / 2] >> 16 : bits[i / 2] & 0xFFFF;
+        v[i] = u < a.kept ? v[i] * a.scale : 0.0f;
+        if (RESIDUAL) v[i] += residual[i];
+    }
+}
+
+template <class T, bool RESIDUAL>
 __global__ __launch_bounds__(kThreads) void k_dropout(Args a) {
     const uint64_t offset = a.offset + (a.step ? uint64_t(*a.step) : 0);
     const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, rows = kThreads / a.across;
@@ -56,18 +70,26 @@ __global__ __launch_bounds__(kThreads) void k_dropout(Args a) {
         const int64_t r = task / a.spans * rows + ty, group = task % a.spans * a.across + tx, c = group * kRow;
         const int valid = valid_of(a.d, c);
         if (r >= a.m || valid == 0) continue;
-        float v[kRow], res[kRow];
-        load8(static_cast<const T*>(a.x) + r * a.ldx + c, valid, v);
-        if (a.residual) load8(static_cast<const T*>(a.residual) + r * a.ldr + c, valid, res);
-        uint32_t bits[4] = {uint32_t(group), uint32_t(r), uint32_t(offset), uint32_t(offset >> 32)};
-        philox(bits, uint32_t(a.seed), uint32_t(a.seed >> 32));
-#pragma unroll
-        for (int i = 0; i < kRow; ++i) {
-            const uint32_t u = i % 2 ? bits[i / 2] >> 16 : bits[i / 2] & 0xFFFF;
-            v[i] = u < a.kept ? v[i] * a.scale : 0.0f;
-            if (a.residual) v[i] += res[i];
+        const T* const x = static_cast<const T*>(a.x) + r * a.ldx + c;
+        const T* const res = RESIDUAL ? static_cast<const T*>(a.residual) + r * a.ldr + c : nullptr;
+        T* const y = static_cast<T*>(a.y) + r * a.ldy + c;
+        float v[kRow], w[kRow];
+        // (two ways through and through: a load behind a branch of its own would be
+        // waited for there, before the next is on its way)
+        if (valid == kRow) {
+            const Eight<T> ex = read8(x);
+            Eight<T> er;
+            if (RESIDUAL) er = read8(res);
+            widen(ex, v);
+            if (RESIDUAL) widen(er, w);
+            drop8<RESIDUAL>(a, offset, r, group, v, w);
+            store8(y, kRow, v);
+        } else {
+            load8(x, valid, v);
+            if (RESIDUAL) load8(res, valid, w);
+            drop8<RESIDUAL>(a, offset, r, group, v, w);
+            store8(y, valid, v);
         }
-        store8(static_cast<T*>(a.y) + r * a.ldy + c, valid, v);
     }
 }
 
@@ -92,7 +114,8 @@ extern "C" int dgc_dropout(const dgc_dropout_args* a, hipStream_t stream) {
     k.spans = cdiv(d, int64_t(k.across) * kRow);
     k.tasks = k.spans * cdiv(m, kThreads / k.across);
     return with_type(a->type, [&](auto t) {
-        k_dropout<decltype(t)><<<dim3(unsigned(std::min(k.tasks, kMostBlocks))), kThreads, 0, stream>>>(k);
+        const auto kernel = k.residual ? k_dropout<decltype(t), true> : k_dropout<decltype(t), false>;
+        kernel<<<dim3(unsigned(std::min(k.tasks, kMostBlocks))), kThreads, 0, stream>>>(k);
         return launched();
     });
 }

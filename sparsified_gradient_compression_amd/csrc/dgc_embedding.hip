@@ -52,13 +52,22 @@ __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
         const int valid = valid_of(a.d, c);
         if (r >= a.m || valid == 0) continue;
         const int64_t id = id_at(a.ids, a.wide_index, r);
+        const bool known = id >= 0 && id < a.vocab;
+        T* const y = static_cast<T*>(a.y) + r * a.ldy + c;
+        const T* const row = static_cast<const T*>(a.table) + id * a.ldt + c;
         float v[kRow] = {};
-        if (id >= 0 && id < a.vocab) {
-            load8(static_cast<const T*>(a.table) + id * a.ldt + c, valid, v);
+        if (known && valid == kRow) {
+            const Eight<T> e = read8(row);
+            widen(e, v);
 #pragma unroll
             for (int i = 0; i < kRow; ++i) v[i] *= a.scale;
+            store8(y, kRow, v);
+        } else {
+            if (known) load8(row, valid, v);
+#pragma unroll
+            for (int i = 0; i < kRow; ++i) v[i] *= a.scale;
+            store8(y, valid, v);
         }
-        store8(static_cast<T*>(a.y) + r * a.ldy + c, valid, v);
     }
 }
 
@@ -66,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
 
 constexpr int kSorters = 1024;            // threads of a sorting workgroup
 constexpr int kSortWaves = kSorters / 64;
-constexpr int kEach = 2;                  // tokens of a thread in k_scatter
+constexpr int kEach = 1;                  // tokens of a thread in k_scatter
 constexpr int64_t kTile = kSorters * kEach;
 constexpr int kOneEach = 4;               // ... at most in k_sort_one
 constexpr int64_t kOne = kSorters * kOneEach;
@@ -81,6 +90,8 @@ struct Sort {
     uint32_t *key_out, *pos_out;
     int shift, bits, next_bits;     // of this pass's digit; next_bits 0: the last pass
     uint32_t *count, *next, *clear;  // [tiles + 1][bins] of this pass, the next and the one after
+    int tile_bits;                  // of a tile's number
+    uint32_t* joins;                // see Sums; 0 at first
     int scanned;                    // count holds the tiles' before each, and all of them last
 };
 
@@ -97,6 +108,15 @@ struct Bins {
     uint32_t sums[kMostBins / 64];
 };
 
+// The lanes, of those in `all`, whose v is the same in its lower bits.
+__device__ __forceinline__ uint64_t lanes_like(uint32_t v, int bits, uint64_t all) {
+    for (int i = 0; i < bits; ++i) {
+        const uint64_t set = __ballot(v >> i & 1);
+        all &= v >> i & 1 ? set : ~set;
+    }
+    return all;
+}
+
 // How many of the tokens before it in its wave have a token's digit.  A wave's
 // tokens are its rounds of 64 in a row; its counts in LDS go along.
 template <int E>
@@ -107,11 +127,7 @@ __device__ __forceinline__ void rank_in_wave(Bins& b, const uint32_t* digit, con
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (e >= rounds) break;
-        uint64_t same = __ballot(on[e]);
-        for (int i = 0; i < bits; ++i) {
-            const uint64_t set = __ballot(digit[e] >> i & 1);
-            same &= digit[e] >> i & 1 ? set : ~set;
-        }
+        const uint64_t same = lanes_like(digit[e], bits, __ballot(on[e]));
         const uint32_t old = count[digit[e]];
         rank[e] = old + __popcll(same & before);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -158,6 +174,7 @@ __global__ __launch_bounds__(kSorters) void k_sort_one(Sort a, int whole_bits, i
     __shared__ Bins b;
     __shared__ uint32_t keys[kOne];
     __shared__ uint16_t places[kOne];
+    if (threadIdx.x == 0) *a.joins = 0;
     const int rounds = int((a.m + kSorters - 1) / kSorters), first = (threadIdx.x >> 6) * 64 * rounds + (threadIdx.x & 63);
     uint32_t key[kOneEach], pos[kOneEach], digit[kOneEach], rank[kOneEach];
     bool on[kOneEach];
@@ -212,6 +229,7 @@ __global__ __launch_bounds__(kSorters) void k_count(Sort a) {
     const int64_t tile = blockIdx.x, first = tile * kTile;
     for (int i = threadIdx.x; i < kMostBins; i += kSorters) count[i] = 0;
     clear_bins(a.next, tile);
+    if (tile == 0 && threadIdx.x == 0) *a.joins = 0;
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
@@ -287,15 +305,22 @@ __global__ __launch_bounds__(kSorters) void k_scatter(Sort a) {
     if (int(threadIdx.x) < bins) b.base[threadIdx.x] = base;
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kEach; ++e)
+    for (int e = 0; e < kEach; ++e) {
+        uint32_t to = 0;
         if (on[e]) {
-            const uint32_t to = b.base[digit[e]] + b.wave[threadIdx.x >> 6][digit[e]] + rank[e];
+            to = b.base[digit[e]] + b.wave[threadIdx.x >> 6][digit[e]] + rank[e];
             a.key_out[to] = key[e];
             a.pos_out[to] = pos[e];
-            if (a.next_bits)
-                atomicAdd(&a.next[int64_t(to / kTile) * kMostBins + (key[e] >> (a.shift + a.bits) & ((1 << a.next_bits) - 1))],
-                          1u);
         }
+        if (a.next_bits == 0) continue;
+        // One addition for all of a wave's tokens that count at the same place: common
+        // ids share their upper digit, and 32768 of them one by one took 28 us.
+        const uint32_t upper = key[e] >> (a.shift + a.bits) & ((1 << a.next_bits) - 1), tile_to = to / uint32_t(kTile);
+        const uint64_t like = lanes_like(upper, a.next_bits, __ballot(on[e]));
+        const uint64_t same = lanes_like(tile_to, a.tile_bits, like);
+        if (on[e] && (same & ((uint64_t(1) << (threadIdx.x & 63)) - 1)) == 0)
+            atomicAdd(&a.next[int64_t(tile_to) * kMostBins + upper], uint32_t(__popcll(same)));
+    }
 }
 
 // ------------------------------------------------------------------- adding
@@ -304,6 +329,7 @@ constexpr int kAhead = 8;                  // tokens whose rows are under way to
 constexpr int kMostUnit = 32;              // sorted tokens of a unit, at most
 constexpr int kLeastAcross = 8;            // lanes side by side on a row, at least
 constexpr int kMostUnits = kThreads / kLeastAcross;  // of a workgroup
+constexpr int kJoiners = 256;              // threads of a joining workgroup
 constexpr int64_t kFillBytes = 64 << 10;   // of a workgroup's rows without a name
 
 struct Sums {
@@ -316,6 +342,7 @@ struct Sums {
     void* dtable;
     int64_t lddt;
     float* part;  // [units][2][d]: of an id that came from before the unit, and of one that goes on behind it
+    uint32_t* joins;  // the number of units whose last id goes on behind them, and these units and ids, in any order
     int unit;     // sorted tokens of a unit
     int64_t units;
     int across;            // lanes side by side on a row, a power of two
@@ -512,46 +539,66 @@ __global__ __launch_bounds__(kThreads) void k_sum(Sums a) {
     if (id >= a.vocab) return;
     if (before)
         leave<TINY, C>(a, unit, 0, w, sum);
-    else if (key[ty][a.unit + 1] == id)
+    else if (key[ty][a.unit + 1] == id) {
         leave<TINY, C>(a, unit, 1, w, sum);
-    else
+        if (w.at == 0 && tx == 0) {
+            uint32_t* const entry = a.joins + 2 + 2 * int64_t(atomicAdd(a.joins, 1u));
+            entry[0] = uint32_t(unit);
+            entry[1] = id;
+        }
+    } else
         finish<TINY, G, C>(a, id, w, sum);
 }
 
-// The id whose tokens begin in a unit and go on behind it, over all units that it
-// reaches.
+// Ids whose tokens begin in a unit and go on behind it, over all units that they
+// reach: groups of `across` lanes take their partial sums in turn, and
+// the groups' sums are added in their order.
 template <class G, int C, bool TINY>
-__global__ __launch_bounds__(kThreads) void k_join(Sums a) {
-    constexpr int kTogether = 16;  // partial sums under way together
-    const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, each = kThreads / a.across;
-    const int64_t block = dgc::block_number();
-    if (block >= a.tasks) return;
-    const int64_t u = block / a.spans * each + ty, begin = u * a.unit, end = begin + a.unit;
-    const Span w = columns<TINY, C>(a.d, (block % a.spans * a.across + tx) * C);
-    if (end >= a.m) return;
-    const uint32_t id = a.key[end - 1];
-    if (id >= a.vocab || a.key[end] != id) return;
-    if (a.key[begin] == id && begin > 0 && a.key[begin - 1] == id) return;  // begins earlier
-    const int64_t last = (end + below(a.key + end, a.m - end, id + 1) - 1) / a.unit;
-    const Some<float, C> mine = get<TINY, float, C>(a.part + (u * 2 + 1) * a.d, w, a.d);
-    double sum[C];
+__global__ __launch_bounds__(kJoiners) void k_join(Sums a) {
+    constexpr int kTogether = 8;  // partial sums under way together
+    __shared__ double sums[kJoiners * C];
+    const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, groups = kJoiners / a.across;
+    const int64_t tasks = int64_t(*a.joins) * a.spans;
+    for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+        const uint32_t* const entry = a.joins + 2 + 2 * (task / a.spans);
+        const int64_t u = entry[0];
+        const uint32_t id = entry[1];
+        // the last unit that begins with it, a lane looking at one unit each
+        int64_t last = u;
+        for (int n = 64; n == 64; last += n) {
+            const int64_t v = last + 1 + (threadIdx.x & 63);
+            const uint64_t reached = __ballot(v * a.unit < a.m && a.key[v * a.unit] == id);
+            n = ~reached == 0 ? 64 : __builtin_ctzll(~reached);
+        }
+        const Span w = columns<TINY, C>(a.d, (task % a.spans * a.across + tx) * C);
+        double sum[C] = {};
+        for (int64_t v = u + ty; v <= last; v += int64_t(groups) * kTogether) {
+            Some<float, C> p[kTogether];
 #pragma unroll
-    for (int i = 0; i < C; ++i) sum[i] = double(mine.t[i]);
-    for (int64_t v = u + 1; v <= last; v += kTogether) {
-        Some<float, C> p[kTogether];
+            for (int k = 0; k < kTogether; ++k) {
+                const int64_t at = v + int64_t(k) * groups <= last ? v + int64_t(k) * groups : last;
+                p[k] = get<TINY, float, C>(a.part + (at * 2 + (at == u)) * a.d, w, a.d);
+            }
 #pragma unroll
-        for (int k = 0; k < kTogether; ++k)
-            p[k] = get<TINY, float, C>(a.part + (v + k <= last ? v + k : last) * 2 * a.d, w, a.d);
+            for (int k = 0; k < kTogether; ++k)
+                if (v + int64_t(k) * groups <= last)
 #pragma unroll
-        for (int k = 0; k < kTogether; ++k)
-            if (v + k <= last)
+                    for (int i = 0; i < C; ++i) sum[i] += double(p[k].t[i]);
+        }
+        __syncthreads();  // the task before has been read
 #pragma unroll
-                for (int i = 0; i < C; ++i) sum[i] += double(p[k].t[i]);
+        for (int i = 0; i < C; ++i) sums[i * kJoiners + threadIdx.x] = sum[i];
+        __syncthreads();
+        if (ty > 0) continue;
+        const int used = last - u < groups ? int(last - u) + 1 : groups;
+        for (int g = 1; g < used; ++g)
+#pragma unroll
+            for (int i = 0; i < C; ++i) sum[i] += sums[i * kJoiners + g * a.across + tx];
+        float out[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) out[i] = float(sum[i]);
+        finish<TINY, G, C>(a, id, w, out);
     }
-    float out[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) out[i] = float(sum[i]);
-    finish<TINY, G, C>(a, id, w, out);
 }
 
 // --------------------------------------------------------------------- host
@@ -572,7 +619,7 @@ int across_of(int64_t d, int columns, int least) {
 int unit_of(int64_t m) { return m < 8192 ? 8 : kMostUnit; }
 
 struct Space {
-    size_t key[2], pos[2], count[3], part, total;
+    size_t key[2], pos[2], count[3], joins, part, total;
 };
 
 Space space(int64_t m, int64_t d) {
@@ -588,6 +635,8 @@ Space space(int64_t m, int64_t d) {
             c = s.total;
             s.total += round_up(size_t(cdiv(m, kTile) + 1) * kMostBins * 4);
         }
+    s.joins = s.total;
+    s.total += round_up(size_t(cdiv(m, unit_of(m)) + 1) * 8);
     s.part = s.total;
     if (m > unit_of(m)) s.total += round_up(size_t(cdiv(m, unit_of(m))) * 2 * size_t(d) * 4);
     return s;
@@ -607,10 +656,12 @@ int sort(const dgc_embedding_backward_args& a, char* ws, const Space& sp, hipStr
     s.m = a.m;
     s.vocab = a.vocab;
     s.tiles = cdiv(a.m, kTile);
+    s.tile_bits = bit_length(s.tiles - 1);
     s.wide_index = a.index_type == DGC_INT64;
     s.ids = a.ids;
     s.key_out = key[0];
     s.pos_out = pos[0];
+    s.joins = reinterpret_cast<uint32_t*>(ws + sp.joins);
     if (a.m <= kOne) {
         k_sort_one<<<1, kSorters, 0, stream>>>(s, whole, bits);
         return 0;
@@ -698,6 +749,7 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
     k.accumulate = int(a->accumulate);
     k.dtable = a->dtable;
     k.lddt = a->lddt;
+    k.joins = reinterpret_cast<uint32_t*>(ws + sp.joins);
     k.part = reinterpret_cast<float*>(ws + sp.part);
     k.unit = unit_of(m);
     k.units = cdiv(m, k.unit);
@@ -714,7 +766,11 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
             k.tasks = k.spans * cdiv(k.units, kThreads / k.across);
             const int64_t blocks = k.tasks + k.fills;
             k_sum<T, G, C, TINY><<<dgc::grid_of(blocks, kThreads), kThreads, 0, stream>>>(k);
-            if (k.units > 1) k_join<G, C, TINY><<<dgc::grid_of(k.tasks, kThreads), kThreads, 0, stream>>>(k);
+            if (k.units > 1) {
+                k.across = std::min(k.across, 64);
+                k.spans = cdiv(d, int64_t(k.across) * C);
+                k_join<G, C, TINY><<<grid(std::min<int64_t>(k.units * k.spans, 2048)), kJoiners, 0, stream>>>(k);
+            }
             return launched();
         };
         const auto sized = [&](auto g) {
