@@ -400,10 +400,15 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     if (lane == 0) a.p.last[part * a.p.strips + strip] = last;
 }
 
+// Keeps the compiler from moving memory accesses over it; a wave's accesses to LDS
+// are done in the order of its instructions.
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
+
 template <class T, int C, bool BACK, bool EVEN>
 __global__ __launch_bounds__(kThreads) void k_along(Args a) {
-    __shared__ float sum[2][kWaves][2][kLanes * C];
-    __shared__ int fresh[2][kWaves];
+    // What each wave handed on last, and how often it has.
+    __shared__ float handed[kWaves][kLanes * C];
+    __shared__ uint32_t times[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Place spot = place(a);
     const int64_t part = spot.part, strip = spot.strip;
@@ -413,11 +418,12 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const Row end = m - begin > Row(a.p.rows) ? begin + Row(a.p.rows) : m;
     Raw<T, C, BACK, true> q, next;
     fetch<T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
-    float carry[C] = {}, kept[C] = {};
+    float kept[C] = {};
     int64_t kept_row = -1;
-    if (a.p.split) {
+    if (wave == 0) {
+        float carry[C] = {};
         constexpr int kBatch = 8;  // parts whose sums are under way together
-        for (int64_t p = 0; p < part; p += kBatch) {
+        for (int64_t p = 0; a.p.split && p < part; p += kBatch) {
             float A[kBatch][C], B[kBatch][C];
             int64_t began[kBatch];
 #pragma unroll
@@ -433,14 +439,19 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
 #pragma unroll
                     for (int j = 0; j < C; ++j) carry[j] = began[i] >= 0 ? B[i][j] : fmaf(A[i][j], carry[j], B[i][j]);
         }
-        // (of the last part no sequence goes on)
-        if (part < a.p.count - 1) {
-            kept_row = a.p.last[part * a.p.strips + strip];
-            get_wide<C>(a.p.kept, part * a.s.d, c, kept);
-        }
+        // as if the last wave had handed it on
+#pragma unroll
+        for (int j = 0; j < C; ++j) handed[kWaves - 1][lane * C + j] = carry[j];
+        if (lane < kWaves) times[lane] = 0;
     }
+    // (of the last part no sequence goes on)
+    if (a.p.split && part < a.p.count - 1) {
+        kept_row = a.p.last[part * a.p.strips + strip];
+        get_wide<C>(a.p.kept, part * a.s.d, c, kept);
+    }
+    __syncthreads();
     // A chunk; the next one's rows are on their way into `next` meanwhile.
-    int turn = 0;
+    uint32_t turn = 0;
     const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         constexpr bool PLAIN = decltype(plain)::value;
         fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
@@ -448,26 +459,33 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
         clear(s);
         float f[kRows][C], r[kRows][C];
         add_rows<PLAIN>(a, q, k, v0, c, kept_row, kept, s, f, r);
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            sum[turn][wave][0][lane * C + j] = s.A[j];
-            sum[turn][wave][1][lane * C + j] = s.B[j];
-        }
-        if (lane == 0) fresh[turn][wave] = s.fresh;
-        __syncthreads();
         const Row r0 = row<BACK>(a, v0);
         Walk out = walk<T, BACK>(a.out, a.ldo, r0, c), out2 = walk<T, BACK>(a.out2, a.ldo2, r0, c);
-        float now[C];
-#pragma unroll 4
-        for (int w = 0; w < kWaves; ++w) {
-            const bool began = fresh[turn][w];
+        // (A and B are worked out here, not behind the wait)
 #pragma unroll
-            for (int j = 0; j < C; ++j) {
-                if (w == wave) now[j] = carry[j];
-                const float A = sum[turn][w][0][lane * C + j], B = sum[turn][w][1][lane * C + j];
-                carry[j] = began ? B : fmaf(A, carry[j], B);
-            }
+        for (int j = 0; j < C; ++j) asm volatile("" : "+v"(s.A[j]), "+v"(s.B[j]));
+        // What the wave before has handed on for this chunk (the first: the last one for
+        // the chunk before), and at once what comes of it behind this wave's rows.  The
+        // workgroup's waves are all resident, and each hands on in each chunk, whatever its
+        // rows are.
+        const int from = wave == 0 ? kWaves - 1 : wave - 1;
+        const uint32_t want = wave == 0 ? turn : turn + 1;
+        // (relaxed: what orders LDS alone; an acquire would wait for global memory too)
+        const auto seen = [&] {
+            return uint32_t(__builtin_amdgcn_readfirstlane(
+                int(__hip_atomic_load(&times[from], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP))));
+        };
+        while (seen() != want) __builtin_amdgcn_s_sleep(1);
+        in_order();
+        float now[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            now[j] = handed[from][lane * C + j];
+            handed[wave][lane * C + j] = s.fresh ? s.B[j] : fmaf(s.A[j], now[j], s.B[j]);
         }
+        in_order();
+        if (lane == 0) __hip_atomic_store(&times[wave], turn + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        in_order();
 #pragma unroll
         for (int i = 0; i < kRows; ++i, out.p += out.step, out2.p += out2.step) {
             if (!PLAIN && !(k.inside >> i & 1)) continue;
@@ -501,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
             if (BACK && a.out2) put<T, C>(out2, c, z);
             if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
         }
-        turn ^= 1;
+        ++turn;
     };
     // Loads and stores are counted together and in order.  Where every way into a
     // chunk but that from a plain one has waited for all of them, a wait for the
