@@ -141,10 +141,11 @@ __device__ __forceinline__ Place place(const Args& a) {
 
 // A workgroup's columns: `base` is the first lane's first one, the same for a
 // whole wave, as rows are, so that an address is a scalar and a lane's small part.
+// Lanes behind the last column do the last one's work once more, and store the same
+// in the same place.
 struct Columns {
     int64_t base;
     uint32_t lane;  // a lane's first column behind that
-    bool mine;      // not a copy of another lane's, behind the last column
 };
 
 template <int C>
@@ -152,8 +153,7 @@ __device__ __forceinline__ Columns columns_of(int64_t d, int64_t strip) {
     Columns c;
     c.base = strip * kLanes * C;
     const uint32_t lane = (threadIdx.x & 63) * C;
-    c.mine = c.base + lane < d;
-    c.lane = c.mine ? lane : uint32_t(d - C - c.base);
+    c.lane = c.base + lane < d ? lane : uint32_t(d - C - c.base);
     return c;
 }
 
@@ -186,9 +186,18 @@ __device__ __forceinline__ Walk walk(const void* p, int64_t ld, Row r, const Col
     return {reinterpret_cast<const char*>(static_cast<const T*>(p) + c.base) + int64_t(r) * bytes, BACK ? -bytes : bytes};
 }
 
+// A lane's bytes behind a row's scalar address, widened where they are used: kept as
+// 64 bits over a loop they would be added by a vector instruction for each row.
+template <class T>
+__device__ __forceinline__ uint64_t lane_bytes(const Columns& c) {
+    uint32_t bytes = c.lane * uint32_t(sizeof(T));
+    asm("" : "+v"(bytes));
+    return bytes;
+}
+
 template <class T, int C>
-__device__ __forceinline__ Some<T, C> get(const Walk& w, const Columns& c) {
-    const char* const q = w.p + uint64_t(uint32_t(c.lane * sizeof(T)));
+__device__ __forceinline__ Some<T, C> get(const Walk& w, uint64_t lane) {
+    const char* const q = w.p + lane;
     if constexpr (sizeof(T) * C == 2)
         return {*reinterpret_cast<const Half*>(q)};
     else
@@ -196,8 +205,8 @@ __device__ __forceinline__ Some<T, C> get(const Walk& w, const Columns& c) {
 }
 
 template <class T, int C>
-__device__ __forceinline__ void put(const Walk& w, const Columns& c, const float* v) {
-    char* const q = const_cast<char*>(w.p) + uint64_t(uint32_t(c.lane * sizeof(T)));
+__device__ __forceinline__ void put(const Walk& w, uint64_t lane, const float* v) {
+    char* const q = const_cast<char*>(w.p) + lane;
     T t[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = T(v[i]);
@@ -255,30 +264,42 @@ struct Raw {
     int32_t own;                        // see marks()
 };
 
-// Behind `end` the last row again and again: every lane loads at all times.
-template <class T, int C, bool BACK, bool EVEN, bool ALL>
-__device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
-    const int lane = threadIdx.x & 63;
-    q.own = v0 < end && lane < kRows + 2 ? owner<BACK, EVEN>(a, int64_t(v0) - 1 + lane) : -1;
-    const Row r = row<BACK>(a, v0 < end ? v0 : end - 1);
+// SHORT: there are fewer rows; behind `end` the last one again and again.
+template <bool SHORT, class T, int C, bool BACK, bool ALL>
+__device__ __forceinline__ void fetch_rows(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
+    const Row r = row<BACK>(a, !SHORT || v0 < end ? v0 : end - 1);
     Walk gate = walk<T, BACK>(a.gate, a.ldg, r, c), x = walk<T, BACK>(a.x, a.ldx, r, c);
-    Walk dh = walk<T, BACK>(a.dh, a.lddh, r, c), h = walk<T, BACK>(a.h, a.ldh, r > 0 ? r - 1 : 0, c);
+    Walk dh = walk<T, BACK>(a.dh, a.lddh, r, c), h = walk<T, BACK>(a.h, a.ldh, !SHORT || r > 0 ? r - 1 : 0, c);
+    const uint64_t lane = lane_bytes<T>(c);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         if (i > 0) {
-            const bool more = v0 + i < end;
+            const bool more = !SHORT || v0 + i < end;
             gate.p += more ? gate.step : 0;
             x.p += more ? x.step : 0;
             dh.p += more ? dh.step : 0;
-            h.p += more && v0 + i < Row(a.s.m) - 1 ? h.step : 0;
+            h.p += more && (!SHORT || v0 + i < Row(a.s.m) - 1) ? h.step : 0;
         }
-        q.gate[i] = get<T, C>(gate, c);
-        q.in[i] = get<T, C>(BACK ? dh : x, c);
+        q.gate[i] = get<T, C>(gate, lane);
+        q.in[i] = get<T, C>(BACK ? dh : x, lane);
         if constexpr (BACK && ALL) {
-            q.x[i] = get<T, C>(x, c);
-            q.h[i] = get<T, C>(h, c);
+            q.x[i] = get<T, C>(x, lane);
+            q.h[i] = get<T, C>(h, lane);
         }
     }
+}
+
+template <bool BACK, bool EVEN>
+__device__ __forceinline__ int32_t owners(const Args& a, Row v0, Row end) {
+    const int lane = threadIdx.x & 63;
+    return v0 < end && lane < kRows + 2 ? owner<BACK, EVEN>(a, int64_t(v0) - 1 + lane) : -1;
+}
+
+// Every lane loads at all times, as many times.
+template <class T, int C, bool BACK, bool EVEN, bool ALL>
+__device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
+    q.own = owners<BACK, EVEN>(a, v0, end);
+    fetch_rows<true>(a, v0, end, c, q);
 }
 
 template <int C>
@@ -392,11 +413,9 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
             if (first >= 0) s.kept[j] = sum[w][2][lane * C + j];
         }
     }
-    if (c.mine) {
-        put_wide<C>(a.p.sums, part * 2 * a.s.d, c, s.A);
-        put_wide<C>(a.p.sums, (part * 2 + 1) * a.s.d, c, s.B);
-        put_wide<C>(a.p.kept, part * a.s.d, c, s.kept);
-    }
+    put_wide<C>(a.p.sums, part * 2 * a.s.d, c, s.A);
+    put_wide<C>(a.p.sums, (part * 2 + 1) * a.s.d, c, s.B);
+    put_wide<C>(a.p.kept, part * a.s.d, c, s.kept);
     if (lane == 0) a.p.last[part * a.p.strips + strip] = last;
 }
 
@@ -454,13 +473,21 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     uint32_t turn = 0;
     const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         constexpr bool PLAIN = decltype(plain)::value;
-        fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
+        if constexpr (PLAIN) {
+            // there is a whole next chunk, or none: then these rows once more
+            const Row then = v0 + Row(kChunk);
+            next.own = owners<BACK, EVEN>(a, then, end);
+            fetch_rows<false>(a, then < end ? then : v0, end, c, next);
+        } else {
+            fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
+        }
         Sum<C> s;
         clear(s);
         float f[kRows][C], r[kRows][C];
         add_rows<PLAIN>(a, q, k, v0, c, kept_row, kept, s, f, r);
         const Row r0 = row<BACK>(a, v0);
         Walk out = walk<T, BACK>(a.out, a.ldo, r0, c), out2 = walk<T, BACK>(a.out2, a.ldo2, r0, c);
+        const uint64_t bytes = lane_bytes<T>(c);
         // (A and B are worked out here, not behind the wait)
 #pragma unroll
         for (int j = 0; j < C; ++j) asm volatile("" : "+v"(s.A[j]), "+v"(s.B[j]));
@@ -514,9 +541,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
                     y[j] = now[j];
                 }
             }
-            if (!c.mine) continue;
-            if (!BACK || a.out) put<T, C>(out, c, y);
-            if (BACK && a.out2) put<T, C>(out2, c, z);
+            if (!BACK || a.out) put<T, C>(out, bytes, y);
+            if (BACK && a.out2) put<T, C>(out2, bytes, z);
             if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
         }
         ++turn;
@@ -528,7 +554,9 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const auto take = [&](Row base, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         const Row v0 = base + wave * kRows;
         const Marks k = marks(q.own, v0, end);
-        if (k.plain()) {
+        // (plain rows have one behind them: the matrix does not end there)
+        const Row then = v0 + Row(kChunk);
+        if (k.plain() && (then >= end || (then + kRows <= end && then + kRows < m))) {
             chunk(std::true_type(), k, v0, q, next);
         } else {
             chunk(std::false_type(), k, v0, q, next);
