@@ -33,6 +33,7 @@ constexpr int kRows = 8;                       // of a wave at a time
 constexpr int64_t kChunk = kWaves * kRows;     // rows of a workgroup at a time
 constexpr int64_t kShort = 8;                  // rows of a sequence, see run()
 constexpr int64_t kFill = 256;                 // workgroups that fill the card
+constexpr int64_t kLarge = 256ll << 20;        // bytes: what the last cache holds
 constexpr int64_t kMostBlocks = 1 << 20;       // of a launch: workgroups take what is left in turn
 
 struct Rows {
@@ -195,13 +196,19 @@ __device__ __forceinline__ uint64_t lane_bytes(const Columns& c) {
     return bytes;
 }
 
-template <class T, int C>
+// Outputs go past the caches: 8 x 8192 rows x 1024 backward 220 us, 250 through
+// them.  ONCE: inputs too, where the last cache does not hold them: 4 x 8192 x 4096
+// backward 327 us, 340 through them, but 4 x 1024 x 4096 47 us, 37 through them.
+template <class T, int C, bool ONCE>
 __device__ __forceinline__ Some<T, C> get(const Walk& w, uint64_t lane) {
     const char* const q = w.p + lane;
-    if constexpr (sizeof(T) * C == 2)
-        return {*reinterpret_cast<const Half*>(q)};
-    else
-        return {*reinterpret_cast<const Word2*>(q)};
+    if constexpr (sizeof(T) * C == 2) {
+        const Half* const h = reinterpret_cast<const Half*>(q);
+        return {ONCE ? __builtin_nontemporal_load(h) : *h};
+    } else {
+        const Word2* const h = reinterpret_cast<const Word2*>(q);
+        return {ONCE ? __builtin_nontemporal_load(h) : *h};
+    }
 }
 
 template <class T, int C>
@@ -211,11 +218,11 @@ __device__ __forceinline__ void put(const Walk& w, uint64_t lane, const float* v
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = T(v[i]);
     if constexpr (sizeof(T) * C == 2) {
-        *reinterpret_cast<Half*>(q) = __builtin_bit_cast(uint16_t, t[0]);
+        __builtin_nontemporal_store(__builtin_bit_cast(uint16_t, t[0]), reinterpret_cast<Half*>(q));
     } else {
         uint32_t w32;
         __builtin_memcpy(&w32, t, 4);
-        *reinterpret_cast<Word2*>(q) = w32;
+        __builtin_nontemporal_store(w32, reinterpret_cast<Word2*>(q));
     }
 }
 
@@ -265,7 +272,7 @@ struct Raw {
 };
 
 // SHORT: there are fewer rows; behind `end` the last one again and again.
-template <bool SHORT, class T, int C, bool BACK, bool ALL>
+template <bool SHORT, bool ONCE, class T, int C, bool BACK, bool ALL>
 __device__ __forceinline__ void fetch_rows(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
     const Row r = row<BACK>(a, !SHORT || v0 < end ? v0 : end - 1);
     Walk gate = walk<T, BACK>(a.gate, a.ldg, r, c), x = walk<T, BACK>(a.x, a.ldx, r, c);
@@ -280,11 +287,11 @@ __device__ __forceinline__ void fetch_rows(const Args& a, Row v0, Row end, const
             dh.p += more ? dh.step : 0;
             h.p += more && (!SHORT || v0 + i < Row(a.s.m) - 1) ? h.step : 0;
         }
-        q.gate[i] = get<T, C>(gate, lane);
-        q.in[i] = get<T, C>(BACK ? dh : x, lane);
+        q.gate[i] = get<T, C, ONCE>(gate, lane);
+        q.in[i] = get<T, C, ONCE>(BACK ? dh : x, lane);
         if constexpr (BACK && ALL) {
-            q.x[i] = get<T, C>(x, lane);
-            q.h[i] = get<T, C>(h, lane);
+            q.x[i] = get<T, C, ONCE>(x, lane);
+            q.h[i] = get<T, C, ONCE>(h, lane);
         }
     }
 }
@@ -296,10 +303,10 @@ __device__ __forceinline__ int32_t owners(const Args& a, Row v0, Row end) {
 }
 
 // Every lane loads at all times, as many times.
-template <class T, int C, bool BACK, bool EVEN, bool ALL>
+template <bool ONCE, class T, int C, bool BACK, bool EVEN, bool ALL>
 __device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
     q.own = owners<BACK, EVEN>(a, v0, end);
-    fetch_rows<true>(a, v0, end, c, q);
+    fetch_rows<true, ONCE>(a, v0, end, c, q);
 }
 
 template <int C>
@@ -379,9 +386,9 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     clear(s);
     int64_t last = -1;
     Raw<T, C, BACK, false> q, next;
-    fetch<T, C, BACK, EVEN>(a, begin, end, c, q);
+    fetch<false, T, C, BACK, EVEN>(a, begin, end, c, q);
     for (Row v = begin; v < end; v += kRows) {
-        fetch<T, C, BACK, EVEN>(a, v + kRows, end, c, next);
+        fetch<false, T, C, BACK, EVEN>(a, v + kRows, end, c, next);
         const Marks k = marks(q.own, v, end);
         float f[kRows][C], r[kRows][C];
         if (k.plain())
@@ -423,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
 // are done in the order of its instructions.
 __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
-template <class T, int C, bool BACK, bool EVEN>
+template <class T, int C, bool BACK, bool EVEN, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     // What each wave handed on last, and how often it has.
     __shared__ float handed[kWaves][kLanes * C];
@@ -436,7 +443,7 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const Row m = Row(a.s.m), begin = spot.part * Row(a.p.rows);
     const Row end = m - begin > Row(a.p.rows) ? begin + Row(a.p.rows) : m;
     Raw<T, C, BACK, true> q, next;
-    fetch<T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
+    fetch<ONCE, T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
     float kept[C] = {};
     int64_t kept_row = -1;
     if (wave == 0) {
@@ -477,9 +484,9 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
             // there is a whole next chunk, or none: then these rows once more
             const Row then = v0 + Row(kChunk);
             next.own = owners<BACK, EVEN>(a, then, end);
-            fetch_rows<false>(a, then < end ? then : v0, end, c, next);
+            fetch_rows<false, ONCE>(a, then < end ? then : v0, end, c, next);
         } else {
-            fetch<T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
+            fetch<ONCE, T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
         }
         Sum<C> s;
         clear(s);
@@ -676,9 +683,12 @@ bool rows_ok(int64_t type, int64_t index_type, int64_t m, int64_t d, int64_t bat
 
 int64_t strips_of(int64_t d, int columns) { return cdiv(d, kLanes * columns); }
 
-// Parts of whole chunks that fill the card.
-int64_t part_rows(int64_t m, int64_t strips) {
-    return std::max<int64_t>(cdiv(cdiv(m * strips, kFill), kChunk), 1) * kChunk;
+constexpr int kMostRounds = 3;
+
+// Rows of parts of whole chunks that fill the card so many times, not quite.
+int64_t part_rows(int64_t m, int64_t strips, int rounds) {
+    const int64_t parts = std::max<int64_t>(rounds * kFill / strips, 1);
+    return std::max<int64_t>(cdiv(cdiv(m, parts), kChunk), 1) * kChunk;
 }
 
 struct Plan {
@@ -686,28 +696,55 @@ struct Plan {
     Parts p{};
 };
 
+// What a plan takes, as a multiple of the time that the memory needs: whole rounds
+// of workgroups at the memory's rate, and a last one at that or at the rate of a
+// compute unit by itself, `alone` of the time that it has in a whole round.
+// Measured on bf16 rows of 4096 columns, 2^27 elements, microseconds by workgroups:
+//   forward, two columns to a lane   128 191   160 163   256 154   288 217
+//   forward, one                     128 337   192 226   256 172   264 331   576 228
+//   backward                          64 831   128 459   256 331   320 430   512 326
+//   with a first pass                forward 229, backward 398
+struct Rate {
+    double alone, most;  // most: against the best kernel of its direction
+};
+constexpr Rate kForwardTwo = {0.62, 1.0}, kForwardOne = {0.98, 1.12}, kBackwardOne = {0.65, 1.0};
+constexpr double kTwiceForward = 1.5, kTwiceBackward = 1.2;  // with a first pass
+
+double expected(const Rate& r, int64_t blocks, int64_t rows) {
+    const double whole = double(blocks / kFill * kFill), rest = double(blocks % kFill), n = double(blocks);
+    // (a workgroup's start costs it two chunks' time)
+    const double start = 1.0 + 2.0 * double(kChunk) / double(rows);
+    return r.most * start * (whole / n + (rest > 0 ? std::max(rest / n, r.alone * double(kFill) / n) : 0.0));
+}
+
 // most: columns that a lane may have.
-Plan plan(int64_t m, int64_t d, int64_t batch, bool even, int most) {
-    Plan k;
+Plan plan(int64_t m, int64_t d, int64_t batch, bool even, bool back, int most) {
+    Plan best;
+    double least = 1e30;
     if (d % 2 != 0) most = 1;
-    // sequences of equal length, as many in a part as fill the card
-    if (even)
-        for (int columns = most; columns > 0; --columns) {
-            const int64_t strips = strips_of(d, columns), length = m / batch;
-            const int64_t rows = std::max<int64_t>(part_rows(m, strips) / length, 1) * length;
+    for (int columns = most; columns > 0; --columns) {
+        const Rate& rate = back ? kBackwardOne : columns == 2 ? kForwardTwo : kForwardOne;
+        const auto offer = [&](int64_t rows, double passes) {
+            Plan k;
             k.columns = columns;
+            k.p.strips = strips_of(d, columns);
             k.p.rows = rows;
-            k.p.strips = strips;
             k.p.count = cdiv(m, rows);
-            if (k.p.count * strips >= kFill || m <= kChunk) return k;
-        }
-    if (even && k.p.count * k.p.strips >= kFill * 3 / 4) return k;
-    k.columns = most;
-    k.p.strips = strips_of(d, k.columns);
-    k.p.rows = part_rows(m, k.p.strips);
-    k.p.count = cdiv(m, k.p.rows);
-    k.p.split = k.p.count > 1;
-    return k;
+            const bool one = k.p.count == 1;
+            k.p.split = passes > 1.0 && !one;
+            const double cost = expected(rate, k.p.count * k.p.strips, rows) * (one ? 1.0 : passes);
+            if (cost >= least) return;
+            least = cost;
+            best = k;
+        };
+        const int64_t strips = strips_of(d, columns);
+        // parts of whole sequences of equal length, which need no first pass
+        const int64_t length = even ? m / batch : 0;
+        if (even) offer(std::max<int64_t>(part_rows(m, strips, 1) / length, 1) * length, 1.0);
+        for (int rounds = 1; rounds <= kMostRounds; ++rounds)
+            offer(part_rows(m, strips, rounds), back ? kTwiceBackward : kTwiceForward);
+    }
+    return best;
 }
 
 struct Space {
@@ -718,7 +755,8 @@ Space space(int64_t m, int64_t d) {
     Space s{};
     int64_t parts = 0, strips = strips_of(d, 1);
     for (int columns = 1; columns <= 2; ++columns)
-        parts = std::max(parts, cdiv(m, part_rows(m, strips_of(d, columns))));
+        for (int rounds = 1; rounds <= kMostRounds; ++rounds)
+            parts = std::max(parts, cdiv(m, part_rows(m, strips_of(d, columns), rounds)));
     s.owner = 0;
     s.sums = round_up(size_t(m) * 4);
     s.kept = s.sums + round_up(size_t(parts) * 2 * size_t(d) * 4);
@@ -748,7 +786,7 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
         });
     }
     // (two columns of the backward pass or of binary32 do not fit a lane's registers)
-    const Plan k = plan(a.s.m, a.s.d, a.s.batch, !a.s.offsets, !BACK && type != DGC_FP32 ? 2 : 1);
+    const Plan k = plan(a.s.m, a.s.d, a.s.batch, !a.s.offsets, BACK, !BACK && type != DGC_FP32 ? 2 : 1);
     a.p = k.p;
     a.p.sums = reinterpret_cast<float*>(ws + sp.sums);
     a.p.kept = reinterpret_cast<float*>(ws + sp.kept);
@@ -761,7 +799,9 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
         if (a.p.split)
             k_parts<T, C, BACK, EVEN>
                 <<<dgc::grid_of((a.p.count - 1) * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
-        k_along<T, C, BACK, EVEN><<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        const int64_t bytes = a.s.m * a.s.d * int64_t(sizeof(T)) * (BACK ? 4 : 2);
+        const auto kernel = bytes > kLarge ? k_along<T, C, BACK, EVEN, true> : k_along<T, C, BACK, EVEN, false>;
+        kernel<<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
         return launched();
     };
     const auto wide = [&](auto t, auto columns) {
