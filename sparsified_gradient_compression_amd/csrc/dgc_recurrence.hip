@@ -651,24 +651,32 @@ __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans
 // reaches it.  And the initial values of empty sequences are their final ones.
 __global__ __launch_bounds__(256) void k_owner(Rows s, int32_t* owner, const float* init, int64_t ldi, float* final,
                                                int64_t ldf) {
+    constexpr int kHeld = 2048;  // offsets that fit into LDS: a search there waits for no memory
+    __shared__ uint32_t held[kHeld];
     const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+    const bool hold = s.offsets && s.batch < kHeld;
+    if (hold) {
+        for (int64_t b = threadIdx.x; b <= s.batch; b += 256) held[b] = uint32_t(row_of(s, b));
+        __syncthreads();
+    }
+    const auto row_at = [&](int64_t b) { return hold ? int64_t(held[b]) : row_of(s, b); };
     if (s.offsets)
         for (int64_t r = first; r < s.m; r += step) {
             int64_t lo = 0, n = s.batch + 1;
             while (n > 0) {
                 const int64_t half = n / 2;
-                if (row_of(s, lo + half) <= r) {
+                if (row_at(lo + half) <= r) {
                     lo += half + 1;
                     n -= half + 1;
                 } else {
                     n = half;
                 }
             }
-            owner[r] = lo > 0 && lo <= s.batch && r < row_of(s, lo) ? int32_t(lo - 1) : -1;
+            owner[r] = lo > 0 && lo <= s.batch && r < row_at(lo) ? int32_t(lo - 1) : -1;
         }
     if (!final) return;
     for (int64_t b = blockIdx.x; b < s.batch; b += gridDim.x)
-        if (!s.offsets || row_of(s, b) >= row_of(s, b + 1))
+        if (!s.offsets || row_at(b) >= row_at(b + 1))
             for (int64_t c = threadIdx.x; c < s.d; c += 256)
                 final[b * ldf + c] = init ? init[b * ldi + c] : 0.0f;
 }
@@ -712,8 +720,8 @@ constexpr double kTwiceForward = 1.5, kTwiceBackward = 1.2;  // with a first pas
 
 double expected(const Rate& r, int64_t blocks, int64_t rows) {
     const double whole = double(blocks / kFill * kFill), rest = double(blocks % kFill), n = double(blocks);
-    // (a workgroup's start costs it two chunks' time)
-    const double start = 1.0 + 2.0 * double(kChunk) / double(rows);
+    // (a workgroup's start costs it half a chunk's time)
+    const double start = 1.0 + 0.5 * double(kChunk) / double(rows);
     return r.most * start * (whole / n + (rest > 0 ? std::max(rest / n, r.alone * double(kFill) / n) : 0.0));
 }
 
