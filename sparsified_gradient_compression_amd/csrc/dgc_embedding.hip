@@ -411,14 +411,14 @@ __device__ __forceinline__ void put(T* row, const Span& w, int64_t d, const floa
             typedef u32x2 V __attribute__((aligned(2), may_alias));
             u32x2 x;
             __builtin_memcpy(&x, t, 8);
-            *reinterpret_cast<V*>(row + w.at) = x;
+            __builtin_nontemporal_store(x, reinterpret_cast<V*>(row + w.at));
         } else {
             typedef typename At<sizeof(T)>::V V;
 #pragma unroll
             for (int i = 0; i < kBytes / 16; ++i) {
                 u32x4 x;
                 __builtin_memcpy(&x, t + i * (16 / sizeof(T)), 16);
-                reinterpret_cast<V*>(row + w.at)[i] = x;
+                __builtin_nontemporal_store(x, reinterpret_cast<V*>(row + w.at) + i);
             }
         }
     } else {
