@@ -4,6 +4,7 @@
 // The gradient sorts the tokens by id first, keeping their order among equal
 // ids, so that a row's sum runs over neighbours in the sorted order and no two
 // workgroups add to the same row: no float atomics, and the same bits every run.
+// Rows that no id names are filled with zeros in the sorting launches.
 //   k_sort_one            up to kOne tokens: all passes of a radix sort in LDS
 //   k_count, k_scatter    more: a pass for each digit of the ids.  k_count finds
 //                         the first digit's counts tile by tile, each k_scatter
@@ -11,8 +12,7 @@
 //                         order does not matter)
 //   k_scan                for many tiles, the counts of the tiles before each
 //   k_sum                 units of sorted tokens: an id's sum over its tokens there.
-//                         An id whose tokens go over a unit's ends leaves partial
-//                         sums.  In the same launch zeros for the rows that no id names
+//                         An id whose tokens go over a unit's ends leaves partial sums
 //   k_join                adds the partial sums up
 #include <algorithm>
 #include <type_traits>
@@ -92,6 +92,7 @@ struct Sort {
     uint32_t *count, *next, *clear;  // [tiles + 1][bins] of this pass, the next and the one after
     int tile_bits;                  // of a tile's number
     uint32_t* joins;                // see Sums; 0 at first
+    uint32_t* token;                // see Fill; or NULL
     int scanned;                    // count holds the tiles' before each, and all of them last
 };
 
@@ -99,6 +100,62 @@ __device__ __forceinline__ uint32_t key_of(const Sort& a, int64_t i) {
     if (!a.ids) return a.key[i];
     const int64_t id = id_at(a.ids, a.wide_index, i);
     return id >= 0 && id < a.vocab ? uint32_t(id) : uint32_t(a.vocab);
+}
+
+// ------------------------------------------------- rows that no id names
+
+constexpr int64_t kFillBytes = 128 << 10;  // of a workgroup's rows
+
+// Zeros for those rows, in workgroups of the sorting launches: their few workgroups
+// take their time waiting for each other's counts and leave the card to these.
+// 32768 tokens, 50000 x 2048 float: 128 us, beside the sums instead 136; 32768 tokens,
+// 200000 x 512 bf16: 57 and 73; 8192 tokens, 50000 x 256 float: 34 and 37.
+struct Fill {
+    int64_t m, vocab;
+    int wide_index;
+    const void* ids;
+    char* dtable;
+    int64_t ld, bytes;  // of a row and from row to row, in bytes
+    int64_t rows;       // of a workgroup
+    int across;         // lanes side by side, a power of two: a row's bytes in 16s, or the workgroup
+    int64_t first;      // chunk of this launch
+    // Of each id that is named a token that has it, else anything: it is looked up
+    // there whether it does.  NULL: the ids themselves are looked through.
+    const uint32_t* token;
+};
+
+__device__ __forceinline__ void fill(const Fill& a, int64_t block, uint8_t* named) {
+    const int64_t first = (a.first + block) * a.rows;
+    const int count = int(a.vocab - first < a.rows ? a.vocab - first : a.rows);
+    if (int(threadIdx.x) < count) {
+        bool there = false;
+        if (a.token) {
+            const uint32_t t = a.token[first + threadIdx.x];
+            there = t < a.m && id_at(a.ids, a.wide_index, t) == first + threadIdx.x;
+        }
+        named[threadIdx.x] = there;
+    }
+    __syncthreads();
+    if (!a.token) {
+        for (int64_t i = threadIdx.x; i < a.m; i += kSorters) {
+            const int64_t id = id_at(a.ids, a.wide_index, i) - first;
+            if (id >= 0 && id < count) named[id] = 1;
+        }
+        __syncthreads();
+    }
+    typedef typename At<2>::V V;
+    const u32x4 zero = {0, 0, 0, 0};
+    const int lane = threadIdx.x & (a.across - 1), step = kSorters / a.across;
+    for (int r = threadIdx.x / a.across; r < count; r += step) {
+        if (named[r]) continue;
+        char* const row = a.dtable + (first + r) * a.ld;
+        for (int64_t c = lane * 16; c < a.bytes; c += a.across * 16) {
+            if (c + 16 <= a.bytes)
+                __builtin_nontemporal_store(zero, reinterpret_cast<V*>(row + c));
+            else
+                for (int64_t i = c; i < a.bytes; i += 2) *reinterpret_cast<uint16_t*>(row + i) = 0;
+        }
+    }
 }
 
 // What a sorting workgroup has in LDS.
@@ -170,10 +227,16 @@ __device__ __forceinline__ uint32_t scan_bins(Bins& b, uint32_t count, int bins)
     return s - count;
 }
 
-__global__ __launch_bounds__(kSorters) void k_sort_one(Sort a, int whole_bits, int digit_bits) {
+// (sorters: 1, or 0 where there are no tokens; the other workgroups fill)
+__global__ __launch_bounds__(kSorters) void k_sort_one(Sort a, Fill f, int sorters, int whole_bits, int digit_bits) {
     __shared__ Bins b;
     __shared__ uint32_t keys[kOne];
     __shared__ uint16_t places[kOne];
+    const int64_t block = dgc::block_number();
+    if (block >= sorters) {
+        if ((f.first + block - sorters) * f.rows < f.vocab) fill(f, block - sorters, reinterpret_cast<uint8_t*>(keys));
+        return;
+    }
     if (threadIdx.x == 0) *a.joins = 0;
     const int rounds = int((a.m + kSorters - 1) / kSorters), first = (threadIdx.x >> 6) * 64 * rounds + (threadIdx.x & 63);
     uint32_t key[kOneEach], pos[kOneEach], digit[kOneEach], rank[kOneEach];
@@ -234,7 +297,10 @@ __global__ __launch_bounds__(kSorters) void k_count(Sort a) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
         const int64_t i = first + e * kSorters + threadIdx.x;
-        if (i < a.m) atomicAdd(&count[key_of(a, i) >> a.shift & ((1 << a.bits) - 1)], 1u);
+        if (i >= a.m) continue;
+        const uint32_t key = key_of(a, i);
+        atomicAdd(&count[key >> a.shift & ((1 << a.bits) - 1)], 1u);
+        if (a.token && key < a.vocab) a.token[key] = uint32_t(i);  // (one of them; see Fill)
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kMostBins; i += kSorters) a.count[tile * kMostBins + i] = count[i];
@@ -264,10 +330,15 @@ __global__ __launch_bounds__(kSorters) void k_scan(uint32_t* count, int64_t tile
     if (wave == kSortWaves - 1) p[tiles * kMostBins] = s;
 }
 
-__global__ __launch_bounds__(kSorters) void k_scatter(Sort a) {
+__global__ __launch_bounds__(kSorters) void k_scatter(Sort a, Fill f) {
     __shared__ Bins b;
     const int bins = 1 << a.bits;
-    const int64_t tile = blockIdx.x;
+    const int64_t tile = dgc::block_number();
+    if (tile >= a.tiles) {
+        const int64_t block = tile - a.tiles;
+        if (f.rows > 0 && (f.first + block) * f.rows < f.vocab) fill(f, block, reinterpret_cast<uint8_t*>(b.base));
+        return;
+    }
     const int64_t first = tile * kTile + (threadIdx.x >> 6) * 64 * kEach + (threadIdx.x & 63);
     uint32_t key[kEach], pos[kEach], digit[kEach], rank[kEach];
     bool on[kEach];
@@ -330,7 +401,6 @@ constexpr int kMostUnit = 32;              // sorted tokens of a unit, at most
 constexpr int kLeastAcross = 8;            // lanes side by side on a row, at least
 constexpr int kMostUnits = kThreads / kLeastAcross;  // of a workgroup
 constexpr int kJoiners = 256;              // threads of a joining workgroup
-constexpr int64_t kFillBytes = 64 << 10;   // of a workgroup's rows without a name
 
 struct Sums {
     int64_t m, vocab, d;
@@ -347,23 +417,7 @@ struct Sums {
     int64_t units;
     int across;            // lanes side by side on a row, a power of two
     int64_t spans, tasks;  // of `across` lanes' columns in a row; of all units together
-    int64_t rows, fills;   // rows of a workgroup that fills, and such workgroups
 };
-
-// How many of n ascending numbers are below k.
-__device__ __forceinline__ int64_t below(const uint32_t* p, int64_t n, uint32_t k) {
-    int64_t lo = 0;
-    while (n > 0) {
-        const int64_t half = n / 2;
-        if (p[lo + half] < k) {
-            lo += half + 1;
-            n -= half + 1;
-        } else {
-            n = half;
-        }
-    }
-    return lo;
-}
 
 // C columns of a lane: 4, where they come to 16 bytes of binary32 (stores that lie
 // side by side), or 8.
@@ -456,39 +510,11 @@ __device__ __forceinline__ void leave(const Sums& a, int64_t unit, int which, co
     if (w.skip < C) put<TINY, float, C>(a.part + (unit * 2 + which) * a.d, w, a.d, sum);
 }
 
-// Zeros for rows that no id names.
-template <class G>
-__device__ __forceinline__ void fill(const Sums& a, int64_t chunk, uint32_t* named) {
-    const int64_t first = chunk * a.rows;
-    const int count = int(a.vocab - first < a.rows ? a.vocab - first : a.rows);
-    if (int(threadIdx.x) < count) {
-        const uint32_t mine = uint32_t(first + threadIdx.x);
-        const int64_t at = below(a.key, a.m, mine);
-        named[threadIdx.x] = at < a.m && a.key[at] == mine;
-    }
-    __syncthreads();
-    constexpr int kWide = 16 / sizeof(G);
-    const float zero[8] = {};
-    for (int r = 0; r < count; ++r) {
-        if (named[r]) continue;
-        G* const row = static_cast<G*>(a.dtable) + (first + r) * a.lddt;
-        for (int64_t c = threadIdx.x * kWide; c < a.d; c += kThreads * kWide) {
-            if (c + kWide <= a.d)
-                put<false, G, kWide>(row, {c, 0}, a.d, zero);
-            else
-                for (int64_t i = c; i < a.d; ++i) row[i] = G(0.0f);
-        }
-    }
-}
-
 template <class T, class G, int C, bool TINY>
 __global__ __launch_bounds__(kThreads) void k_sum(Sums a) {
     __shared__ uint32_t key[kMostUnits][kMostUnit + 2], pos[kMostUnits][kMostUnit];
     const int64_t block = dgc::block_number();
-    if (block >= a.tasks) {
-        if (block < a.tasks + a.fills) fill<G>(a, block - a.tasks, &key[0][0]);
-        return;
-    }
+    if (block >= a.tasks) return;
     const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, each = kThreads / a.across;
     const int64_t first = block / a.spans * each;
     const Span w = columns<TINY, C>(a.d, (block % a.spans * a.across + tx) * C);
@@ -619,10 +645,10 @@ int across_of(int64_t d, int columns, int least) {
 int unit_of(int64_t m) { return m < 8192 ? 8 : kMostUnit; }
 
 struct Space {
-    size_t key[2], pos[2], count[3], joins, part, total;
+    size_t key[2], pos[2], count[3], token, joins, part, total;
 };
 
-Space space(int64_t m, int64_t d) {
+Space space(int64_t m, int64_t vocab, int64_t d) {
     Space s{};
     const size_t list = round_up(size_t(m) * 4);
     for (int i = 0; i < 2; ++i) {
@@ -635,6 +661,8 @@ Space space(int64_t m, int64_t d) {
             c = s.total;
             s.total += round_up(size_t(cdiv(m, kTile) + 1) * kMostBins * 4);
         }
+    s.token = s.total;
+    if (m > kOne) s.total += round_up(size_t(vocab) * 4);
     s.joins = s.total;
     s.total += round_up(size_t(cdiv(m, unit_of(m)) + 1) * 8);
     s.part = s.total;
@@ -642,30 +670,49 @@ Space space(int64_t m, int64_t d) {
     return s;
 }
 
-// Sorts the tokens into one of the two lists; returns which.
+// Sorts the tokens into one of the two lists and fills the rows that none names;
+// returns which list.
 int sort(const dgc_embedding_backward_args& a, char* ws, const Space& sp, hipStream_t stream) {
+    const int64_t size = size_of(a.grad_type), bytes = a.d * size;
+    Fill f{};
+    f.m = a.m;
+    f.vocab = a.vocab;
+    f.wide_index = a.index_type == DGC_INT64;
+    f.ids = a.ids;
+    f.dtable = static_cast<char*>(a.dtable);
+    f.ld = a.lddt * size;
+    f.bytes = bytes;
+    f.rows = a.accumulate ? 0 : std::max<int64_t>(1, std::min<int64_t>(kSorters, kFillBytes / bytes));
+    for (f.across = 1; f.across < kSorters && f.across * 16 < bytes;) f.across *= 2;
+    const int64_t chunks = a.accumulate ? 0 : cdiv(a.vocab, f.rows);
+    Sort s{};
+    const int whole = bit_length(a.vocab), passes = (whole + kMostBits - 1) / kMostBits;
+    const int bits = (whole + passes - 1) / passes;
+    if (a.m == 0) {
+        k_sort_one<<<dgc::grid_of(chunks, kSorters), kSorters, 0, stream>>>(s, f, 0, whole, bits);
+        return 0;
+    }
     uint32_t *key[2], *pos[2], *count[3];
     for (int i = 0; i < 2; ++i) {
         key[i] = reinterpret_cast<uint32_t*>(ws + sp.key[i]);
         pos[i] = reinterpret_cast<uint32_t*>(ws + sp.pos[i]);
     }
     for (int i = 0; i < 3; ++i) count[i] = reinterpret_cast<uint32_t*>(ws + sp.count[i]);
-    const int whole = bit_length(a.vocab), passes = (whole + kMostBits - 1) / kMostBits;
-    const int bits = (whole + passes - 1) / passes;
-    Sort s{};
     s.m = a.m;
     s.vocab = a.vocab;
     s.tiles = cdiv(a.m, kTile);
     s.tile_bits = bit_length(s.tiles - 1);
-    s.wide_index = a.index_type == DGC_INT64;
+    s.wide_index = f.wide_index;
     s.ids = a.ids;
     s.key_out = key[0];
     s.pos_out = pos[0];
     s.joins = reinterpret_cast<uint32_t*>(ws + sp.joins);
     if (a.m <= kOne) {
-        k_sort_one<<<1, kSorters, 0, stream>>>(s, whole, bits);
+        k_sort_one<<<dgc::grid_of(1 + chunks, kSorters), kSorters, 0, stream>>>(s, f, 1, whole, bits);
         return 0;
     }
+    s.token = a.accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + sp.token);
+    f.token = s.token;
     int out = 0;
     for (int pass = 0; pass < passes; ++pass, out ^= 1) {
         s.shift = pass * bits;
@@ -676,11 +723,13 @@ int sort(const dgc_embedding_backward_args& a, char* ws, const Space& sp, hipStr
         s.clear = count[(pass + 2) % 3];
         s.key_out = key[out];
         s.pos_out = pos[out];
-        const dim3 grid(unsigned(s.tiles));
-        if (pass == 0) k_count<<<grid, kSorters, 0, stream>>>(s);
+        if (pass == 0) k_count<<<dim3(unsigned(s.tiles)), kSorters, 0, stream>>>(s);
         s.scanned = s.tiles > kFewTiles;
         if (s.scanned) k_scan<<<kMostBins / 64, kSorters, 0, stream>>>(s.count, s.tiles);
-        k_scatter<<<grid, kSorters, 0, stream>>>(s);
+        // this pass's share of the rows to fill
+        f.first = chunks * pass / passes;
+        const int64_t blocks = s.tiles + chunks * (pass + 1) / passes - f.first;
+        k_scatter<<<dgc::grid_of(blocks, kSorters), kSorters, 0, stream>>>(s, f);
         s.ids = nullptr;
         s.key = key[out];
         s.pos = pos[out];
@@ -696,7 +745,7 @@ extern "C" {
 
 int dgc_embedding_workspace_bytes(int64_t m, int64_t vocab, int64_t d, int32_t backward, size_t* bytes) {
     if (!bytes || !side_ok(m) || !side_ok(vocab) || !side_ok(d) || (d > 0 && m > kMostArea / d)) return DGC_EINVAL;
-    *bytes = backward && m > 0 && d > 0 ? space(m, d).total : 0;
+    *bytes = backward && m > 0 && d > 0 ? space(m, vocab, d).total : 0;
     return DGC_OK;
 }
 
@@ -731,12 +780,13 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
     if (!mat_ok(a->dy, a->lddy, m, d, size_of(a->type)) || !vec_ok(a->ids, m, size_of(a->index_type)) ||
         !mat_ok(a->dtable, a->lddt, vocab, d, gsize) || (d > 0 && m > kMostArea / d))
         return DGC_EINVAL;
-    const Space sp = space(m, d);
+    const Space sp = space(m, vocab, d);
     int rc = space_ok(workspace, workspace_bytes, m > 0 && d > 0 ? sp.total : 0);
     if (rc != DGC_OK) return rc;
     if (vocab == 0 || d == 0 || (m == 0 && a->accumulate)) return DGC_OK;
     char* const ws = static_cast<char*>(workspace);
-    const int in = m > 0 ? sort(*a, ws, sp, stream) : 0;
+    const int in = sort(*a, ws, sp, stream);
+    if (m == 0) return launched();
     Sums k{};
     k.m = m;
     k.vocab = vocab;
@@ -753,8 +803,6 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
     k.part = reinterpret_cast<float*>(ws + sp.part);
     k.unit = unit_of(m);
     k.units = cdiv(m, k.unit);
-    k.rows = std::max<int64_t>(1, std::min<int64_t>(kThreads, kFillBytes / (d * gsize)));
-    k.fills = k.accumulate ? 0 : cdiv(vocab, k.rows);
     return with_type(a->type, [&](auto t) {
         typedef decltype(t) T;
         const auto with = [&](auto g, auto tiny) {
@@ -764,8 +812,7 @@ int dgc_embedding_backward(const dgc_embedding_backward_args* a, void* workspace
             k.across = across_of(d, C, kLeastAcross);
             k.spans = cdiv(d, int64_t(k.across) * C);
             k.tasks = k.spans * cdiv(k.units, kThreads / k.across);
-            const int64_t blocks = k.tasks + k.fills;
-            k_sum<T, G, C, TINY><<<dgc::grid_of(blocks, kThreads), kThreads, 0, stream>>>(k);
+            k_sum<T, G, C, TINY><<<dgc::grid_of(k.tasks, kThreads), kThreads, 0, stream>>>(k);
             if (k.units > 1) {
                 k.across = std::min(k.across, 64);
                 k.spans = cdiv(d, int64_t(k.across) * C);
