@@ -642,7 +642,7 @@ int across_of(int64_t d, int columns, int least) {
 }
 
 // Sorted tokens of a unit: fewer, a multiple of kAhead, where there are few tokens.
-int unit_of(int64_t m) { return m < 8192 ? 8 : kMostUnit; }
+int unit_of(int64_t m) { return m <= kOne ? kAhead : kMostUnit; }
 
 struct Space {
     size_t key[2], pos[2], count[3], token, joins, part, total;

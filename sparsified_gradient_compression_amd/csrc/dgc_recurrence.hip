@@ -6,16 +6,24 @@
 // row hands to the one before it, f g, and u = f dh.  Rows [a, b) together are
 // c <- A c + B with A the product of their f, so they can be worked on side by
 // side: the waves of a workgroup take kRows rows each, work out their A and B,
-// and after one exchange through LDS go over their rows (still in registers)
-// again with the c that comes in.  A row where a sequence begins takes its
-// initial value instead of what comes in, and says so beside A and B (a product
-// with 0 would not stop an infinity).
+// take c from the wave before through LDS, hand on A c + B at once, and go over
+// their rows (still in registers) again with the c that came in.  A row where a
+// sequence begins takes its initial value instead of what comes in, and says so
+// beside A and B (a product with 0 would not stop an infinity).
 //
 // A workgroup goes along a part of the rows in chunks of kWaves * kRows, the next
 // chunk's loads under way while it works on this one.  Where sequences of
 // equal length give enough parts, parts begin where sequences do and every
 // input is read once.  Else a first pass leaves A and B of each part, and
-// the second folds those before its part.
+// the second folds those before its part: see plan().
+//
+// What bounds it is memory, where there are enough rows and columns to fill the
+// card: forward moves 3 numbers for each element, backward 6.  bf16, microseconds:
+//   forward   8 x 4096 x 4096 154 (5.2 TB/s)   64 x 8192 x 512 298 (5.4)
+//   backward  4 x 8192 x 4096 329 (4.9)        8 x 4096 x 4096 332
+//   with a first pass  1 x 32768 x 4096 forward 228, backward 398
+//   9734 x 1152 in sequences of many lengths   forward 33 (2.0 of 67 MB)
+// A barrier for each chunk, every wave folding all waves' sums: 181 for 154.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,10 +39,15 @@ constexpr int kWaves = 16;
 constexpr int kThreads = kLanes * kWaves;
 constexpr int kRows = 8;                       // of a wave at a time
 constexpr int64_t kChunk = kWaves * kRows;     // rows of a workgroup at a time
-constexpr int64_t kShort = 8;                  // rows of a sequence, see run()
+// Rows of a sequence that k_short goes along.  bf16, us forward and backward, by
+// k_short and by k_along: 64 x 4 x 1280 4.2 6.2 and 6.9 9.0, 64 x 8 x 1280 6.5 10.1
+// and 7.1 9.0, 4096 x 8 x 1280 40 103 and 51 145, 64 x 16 x 1280 11.0 18.2 and 7.2 9.2.
+constexpr int64_t kShort = 8;
 constexpr int64_t kFill = 256;                 // workgroups that fill the card
 constexpr int64_t kLarge = 256ll << 20;        // bytes: what the last cache holds
 constexpr int64_t kMostBlocks = 1 << 20;       // of a launch: workgroups take what is left in turn
+constexpr int64_t kLine = 128;                 // bytes of a cache's line
+constexpr uint32_t kDies = 8;                  // each with a cache of its own; workgroups go to them in turn
 
 struct Rows {
     int64_t m, d, batch;
@@ -48,9 +61,10 @@ struct Rows {
 struct Parts {
     int64_t rows, count, strips;  // rows of a part, parts, strips of columns
     int split;                    // whether sequences go from part to part
+    int close;                    // whether workgroups side by side share a die, see run()
     float* sums;                  // then [count][2][d]: A and B of each part
     float* kept;                  // [count][d]: the initial value of the last sequence that begins in a part
-    int64_t* last;                // [count]: and that sequence's first row, or -1
+    int64_t* last;                // [count][strips]: and that sequence's first row, or -1
 };
 
 struct Args {
@@ -133,7 +147,9 @@ struct Place {
 };
 
 __device__ __forceinline__ Place place(const Args& a) {
-    const uint32_t block = uint32_t(dgc::block_number()), part = block / uint32_t(a.p.strips);
+    uint32_t block = uint32_t(dgc::block_number());
+    if (a.p.close) block = block % kDies * (gridDim.x * gridDim.y / kDies) + block / kDies;
+    const uint32_t part = block / uint32_t(a.p.strips);
     Place w;
     w.part = __builtin_amdgcn_readfirstlane(part);
     w.strip = __builtin_amdgcn_readfirstlane(block - part * uint32_t(a.p.strips));
@@ -196,33 +212,47 @@ __device__ __forceinline__ uint64_t lane_bytes(const Columns& c) {
     return bytes;
 }
 
-// Outputs go past the caches: 8 x 8192 rows x 1024 backward 220 us, 250 through
-// them.  ONCE: inputs too, where the last cache does not hold them: 4 x 8192 x 4096
-// backward 327 us, 340 through them, but 4 x 1024 x 4096 47 us, 37 through them.
-template <class T, int C, bool ONCE>
+// What goes past the caches: outputs (8 x 8192 x 1024 backward 206 us, 228 through
+// them), and inputs that the last cache does not hold: 4 x 8192 x 4096 backward
+// 327 us, 340 through them, but 4 x 1024 x 4096 47 us, 37 through them.  Yet where rows
+// do not begin at a line, two strips share lines, and of what the last cache does not
+// hold nothing does: 64 x 1024 x 1001 backward 182 us, 237 with the outputs past them,
+// 275 with both.
+enum Past { kOut, kBoth, kNone };
+
+template <class T, int C, Past PAST>
 __device__ __forceinline__ Some<T, C> get(const Walk& w, uint64_t lane) {
     const char* const q = w.p + lane;
     if constexpr (sizeof(T) * C == 2) {
         const Half* const h = reinterpret_cast<const Half*>(q);
-        return {ONCE ? __builtin_nontemporal_load(h) : *h};
+        return {PAST == kBoth ? __builtin_nontemporal_load(h) : *h};
     } else {
         const Word2* const h = reinterpret_cast<const Word2*>(q);
-        return {ONCE ? __builtin_nontemporal_load(h) : *h};
+        return {PAST == kBoth ? __builtin_nontemporal_load(h) : *h};
     }
 }
 
-template <class T, int C>
+template <class T, int C, Past PAST>
 __device__ __forceinline__ void put(const Walk& w, uint64_t lane, const float* v) {
     char* const q = const_cast<char*>(w.p) + lane;
     T t[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = T(v[i]);
     if constexpr (sizeof(T) * C == 2) {
-        __builtin_nontemporal_store(__builtin_bit_cast(uint16_t, t[0]), reinterpret_cast<Half*>(q));
+        Half* const h = reinterpret_cast<Half*>(q);
+        const uint16_t bits = __builtin_bit_cast(uint16_t, t[0]);
+        if constexpr (PAST == kNone)
+            *h = bits;
+        else
+            __builtin_nontemporal_store(bits, h);
     } else {
-        uint32_t w32;
-        __builtin_memcpy(&w32, t, 4);
-        __builtin_nontemporal_store(w32, reinterpret_cast<Word2*>(q));
+        Word2* const h = reinterpret_cast<Word2*>(q);
+        uint32_t bits;
+        __builtin_memcpy(&bits, t, 4);
+        if constexpr (PAST == kNone)
+            *h = bits;
+        else
+            __builtin_nontemporal_store(bits, h);
     }
 }
 
@@ -244,8 +274,9 @@ struct Marks {
     uint32_t inside, first, last;  // of any sequence; in the order of the recurrence its first, its last
     int32_t own;                   // lane i + 1: row i's sequence
     __device__ int32_t sequence(int i) const { return __builtin_amdgcn_readlane(own, i + 1); }
-    // rows of a sequence that began before them and goes on behind them
-    __device__ bool plain() const { return inside == (1u << kRows) - 1 && (first | last) == 0; }
+    // rows of sequences all; of one that began before them and goes on behind them
+    __device__ bool whole() const { return inside == (1u << kRows) - 1; }
+    __device__ bool plain() const { return whole() && (first | last) == 0; }
 };
 
 // own: lane i + 1 holds row i's sequence, for i from -1 to kRows.
@@ -272,7 +303,7 @@ struct Raw {
 };
 
 // SHORT: there are fewer rows; behind `end` the last one again and again.
-template <bool SHORT, bool ONCE, class T, int C, bool BACK, bool ALL>
+template <bool SHORT, Past PAST, class T, int C, bool BACK, bool ALL>
 __device__ __forceinline__ void fetch_rows(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
     const Row r = row<BACK>(a, !SHORT || v0 < end ? v0 : end - 1);
     Walk gate = walk<T, BACK>(a.gate, a.ldg, r, c), x = walk<T, BACK>(a.x, a.ldx, r, c);
@@ -287,11 +318,11 @@ __device__ __forceinline__ void fetch_rows(const Args& a, Row v0, Row end, const
             dh.p += more ? dh.step : 0;
             h.p += more && (!SHORT || v0 + i < Row(a.s.m) - 1) ? h.step : 0;
         }
-        q.gate[i] = get<T, C, ONCE>(gate, lane);
-        q.in[i] = get<T, C, ONCE>(BACK ? dh : x, lane);
+        q.gate[i] = get<T, C, PAST>(gate, lane);
+        q.in[i] = get<T, C, PAST>(BACK ? dh : x, lane);
         if constexpr (BACK && ALL) {
-            q.x[i] = get<T, C, ONCE>(x, lane);
-            q.h[i] = get<T, C, ONCE>(h, lane);
+            q.x[i] = get<T, C, PAST>(x, lane);
+            q.h[i] = get<T, C, PAST>(h, lane);
         }
     }
 }
@@ -303,10 +334,10 @@ __device__ __forceinline__ int32_t owners(const Args& a, Row v0, Row end) {
 }
 
 // Every lane loads at all times, as many times.
-template <bool ONCE, class T, int C, bool BACK, bool EVEN, bool ALL>
+template <Past PAST, class T, int C, bool BACK, bool EVEN, bool ALL>
 __device__ __forceinline__ void fetch(const Args& a, Row v0, Row end, const Columns& c, Raw<T, C, BACK, ALL>& q) {
     q.own = owners<BACK, EVEN>(a, v0, end);
-    fetch_rows<true, ONCE>(a, v0, end, c, q);
+    fetch_rows<true, PAST>(a, v0, end, c, q);
 }
 
 template <int C>
@@ -329,13 +360,16 @@ struct Sum {
     bool fresh;
 };
 
-template <bool PLAIN, class T, int C, bool BACK, bool ALL>
+// What is known of a wave's rows when it is compiled: see Marks.
+enum Kind { kPlain, kWhole, kAny };
+
+template <Kind KIND, class T, int C, bool BACK, bool ALL>
 __device__ __forceinline__ void add_rows(const Args& a, const Raw<T, C, BACK, ALL>& q, const Marks& k, Row v0, const Columns& c,
                                          int64_t kept_row, const float* kept, Sum<C>& s, float (*f)[C], float (*r)[C]) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        if (!PLAIN) {
-            if (!(k.inside >> i & 1)) continue;
+        if (KIND == kAny && !(k.inside >> i & 1)) continue;
+        if (KIND != kPlain) {
             if (k.first >> i & 1) {
                 if (int64_t(v0) + i == kept_row) {
 #pragma unroll
@@ -386,15 +420,15 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
     clear(s);
     int64_t last = -1;
     Raw<T, C, BACK, false> q, next;
-    fetch<false, T, C, BACK, EVEN>(a, begin, end, c, q);
+    fetch<kOut, T, C, BACK, EVEN>(a, begin, end, c, q);
     for (Row v = begin; v < end; v += kRows) {
-        fetch<false, T, C, BACK, EVEN>(a, v + kRows, end, c, next);
+        fetch<kOut, T, C, BACK, EVEN>(a, v + kRows, end, c, next);
         const Marks k = marks(q.own, v, end);
         float f[kRows][C], r[kRows][C];
         if (k.plain())
-            add_rows<true>(a, q, k, v, c, -1, nullptr, s, f, r);
+            add_rows<kPlain>(a, q, k, v, c, -1, nullptr, s, f, r);
         else
-            add_rows<false>(a, q, k, v, c, -1, nullptr, s, f, r);
+            add_rows<kAny>(a, q, k, v, c, -1, nullptr, s, f, r);
         if (k.first) last = int64_t(v) + 31 - __builtin_clz(k.first);
         q = next;
     }
@@ -430,7 +464,7 @@ __global__ __launch_bounds__(kThreads) void k_parts(Args a) {
 // are done in the order of its instructions.
 __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
-template <class T, int C, bool BACK, bool EVEN, bool ONCE>
+template <class T, int C, bool BACK, bool EVEN, Past PAST>
 __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     // What each wave handed on last, and how often it has.
     __shared__ float handed[kWaves][kLanes * C];
@@ -443,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const Row m = Row(a.s.m), begin = spot.part * Row(a.p.rows);
     const Row end = m - begin > Row(a.p.rows) ? begin + Row(a.p.rows) : m;
     Raw<T, C, BACK, true> q, next;
-    fetch<ONCE, T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
+    fetch<PAST, T, C, BACK, EVEN>(a, begin + wave * kRows, end, c, q);
     float kept[C] = {};
     int64_t kept_row = -1;
     if (wave == 0) {
@@ -478,20 +512,20 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     __syncthreads();
     // A chunk; the next one's rows are on their way into `next` meanwhile.
     uint32_t turn = 0;
-    const auto chunk = [&](auto plain, const Marks& k, Row v0, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
-        constexpr bool PLAIN = decltype(plain)::value;
-        if constexpr (PLAIN) {
+    const auto chunk = [&](auto kind, const Marks& k, Row v0, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
+        constexpr Kind KIND = decltype(kind)::value;
+        if constexpr (KIND != kAny) {
             // there is a whole next chunk, or none: then these rows once more
             const Row then = v0 + Row(kChunk);
             next.own = owners<BACK, EVEN>(a, then, end);
-            fetch_rows<false, ONCE>(a, then < end ? then : v0, end, c, next);
+            fetch_rows<false, PAST>(a, then < end ? then : v0, end, c, next);
         } else {
-            fetch<ONCE, T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
+            fetch<PAST, T, C, BACK, EVEN>(a, v0 + Row(kChunk), end, c, next);
         }
         Sum<C> s;
         clear(s);
         float f[kRows][C], r[kRows][C];
-        add_rows<PLAIN>(a, q, k, v0, c, kept_row, kept, s, f, r);
+        add_rows<KIND>(a, q, k, v0, c, kept_row, kept, s, f, r);
         const Row r0 = row<BACK>(a, v0);
         Walk out = walk<T, BACK>(a.out, a.ldo, r0, c), out2 = walk<T, BACK>(a.out2, a.ldo2, r0, c);
         const uint64_t bytes = lane_bytes<T>(c);
@@ -522,8 +556,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
         in_order();
 #pragma unroll
         for (int i = 0; i < kRows; ++i, out.p += out.step, out2.p += out2.step) {
-            if (!PLAIN && !(k.inside >> i & 1)) continue;
-            const bool first = !PLAIN && (k.first >> i & 1), last = !PLAIN && (k.last >> i & 1);
+            if (KIND == kAny && !(k.inside >> i & 1)) continue;
+            const bool first = KIND != kPlain && (k.first >> i & 1), last = KIND != kPlain && (k.last >> i & 1);
             float y[C], z[C], start[C];
             if (first) {
                 // the last one's initial value is at hand: it may have been overwritten by the rows behind
@@ -548,8 +582,8 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
                     y[j] = now[j];
                 }
             }
-            if (!BACK || a.out) put<T, C>(out, bytes, y);
-            if (BACK && a.out2) put<T, C>(out2, bytes, z);
+            if (!BACK || a.out) put<T, C, PAST>(out, bytes, y);
+            if (BACK && a.out2) put<T, C, PAST>(out2, bytes, z);
             if (last && a.final) put_wide<C>(a.final, int64_t(sequence) * a.ldf, c, now);
         }
         ++turn;
@@ -561,12 +595,15 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
     const auto take = [&](Row base, const Raw<T, C, BACK, true>& q, Raw<T, C, BACK, true>& next) {
         const Row v0 = base + wave * kRows;
         const Marks k = marks(q.own, v0, end);
-        // (plain rows have one behind them: the matrix does not end there)
+        // (row by row without a look, the rows need one behind them)
         const Row then = v0 + Row(kChunk);
-        if (k.plain() && (then >= end || (then + kRows <= end && then + kRows < m))) {
-            chunk(std::true_type(), k, v0, q, next);
+        const bool sure = then < end ? then + kRows <= end && then + kRows < m : v0 + kRows < m;
+        if (sure && k.plain()) {
+            chunk(std::integral_constant<Kind, kPlain>(), k, v0, q, next);
+        } else if (sure && k.whole()) {
+            chunk(std::integral_constant<Kind, kWhole>(), k, v0, q, next);
         } else {
-            chunk(std::false_type(), k, v0, q, next);
+            chunk(std::integral_constant<Kind, kAny>(), k, v0, q, next);
             wait();
         }
     };
@@ -579,9 +616,9 @@ __global__ __launch_bounds__(kThreads) void k_along(Args a) {
 }
 
 // Short sequences of equal length: a lane goes along 8 columns of one, row by
-// row.
-// kAtOnce: rows whose loads are under way together.
-template <class T, bool BACK, int kAtOnce>
+// row.  (Four rows' loads together: 4096 x 8 x 1280 backward 216 us, one by one 103.)
+// Those of one row are a step of generation: 64 x 1 x 1280 takes 2.5 us, a launch's.
+template <class T, bool BACK>
 __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans, int64_t tasks) {
     const int tx = threadIdx.x & (across - 1), ty = threadIdx.x / across, each = 256 / across;
     for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
@@ -592,56 +629,44 @@ __global__ __launch_bounds__(256) void k_short(Args a, int across, int64_t spans
         float now[kRow] = {};
         if (a.init) load8(a.init + b * a.ldi + c, valid, now);
         const int64_t end = begin + a.s.length;
-        for (int64_t i = 0; i < a.s.length; i += kAtOnce) {
-            Eight<T> gate[kAtOnce], in[kAtOnce], xs[BACK ? kAtOnce : 1], hs[BACK ? kAtOnce : 1];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const int64_t t = BACK ? (end - 1 - i - k > begin ? end - 1 - i - k : begin)
-                                       : (begin + i + k < end ? begin + i + k : end - 1);
-                gate[k] = read8(static_cast<const T*>(a.gate) + t * a.ldg + c, valid);
-                in[k] = read8(BACK ? static_cast<const T*>(a.dh) + t * a.lddh + c
-                                   : static_cast<const T*>(a.x) + t * a.ldx + c, valid);
-                if constexpr (BACK) {
-                    xs[k] = read8(static_cast<const T*>(a.x) + t * a.ldx + c, valid);
-                    hs[k] = read8(static_cast<const T*>(a.h) + (t > begin ? t - 1 : t) * a.ldh + c, valid);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                if (i + k >= a.s.length) break;
-                const int64_t t = BACK ? end - 1 - i - k : begin + i + k;
-                float z[kRow], u[kRow], x[kRow], h[kRow];
-                widen(gate[k], z);
-                widen(in[k], u);
-                if constexpr (BACK) {
-                    widen(xs[k], x);
-                    widen(hs[k], h);
-                    if (t == begin) {
-                        if (a.h0) {
-                            load8(a.h0 + b * a.ldh0 + c, valid, h);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < kRow; ++j) h[j] = 0.0f;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kRow; ++j) {
-                    float f, r;
-                    gate_pair<sizeof(T) == 4>(z[j], f, r);
-                    if (BACK) {
-                        const float g = u[j] + now[j];
-                        z[j] = g * (h[j] - x[j]) * (f * r);
-                        x[j] = r * g;
-                        now[j] = f * g;
+        for (int64_t i = 0; i < a.s.length; ++i) {
+            const int64_t t = BACK ? end - 1 - i : begin + i;
+            float z[kRow], u[kRow], x[kRow], h[kRow];
+            const Eight<T> gate = read8(static_cast<const T*>(a.gate) + t * a.ldg + c, valid);
+            const Eight<T> in = read8(BACK ? static_cast<const T*>(a.dh) + t * a.lddh + c
+                                           : static_cast<const T*>(a.x) + t * a.ldx + c, valid);
+            if constexpr (BACK) {
+                const Eight<T> xs = read8(static_cast<const T*>(a.x) + t * a.ldx + c, valid);
+                const Eight<T> hs = read8(static_cast<const T*>(a.h) + (t > begin ? t - 1 : t) * a.ldh + c, valid);
+                widen(xs, x);
+                widen(hs, h);
+                if (t == begin) {
+                    if (a.h0) {
+                        load8(a.h0 + b * a.ldh0 + c, valid, h);
                     } else {
-                        now[j] = fmaf(f, now[j], r * u[j]);
-                        x[j] = now[j];
+#pragma unroll
+                        for (int j = 0; j < kRow; ++j) h[j] = 0.0f;
                     }
                 }
-                if (!BACK || a.out) store8(static_cast<T*>(a.out) + t * a.ldo + c, valid, x);
-                if (BACK && a.out2) store8(static_cast<T*>(a.out2) + t * a.ldo2 + c, valid, z);
             }
+            widen(gate, z);
+            widen(in, u);
+#pragma unroll
+            for (int j = 0; j < kRow; ++j) {
+                float f, r;
+                gate_pair<sizeof(T) == 4>(z[j], f, r);
+                if (BACK) {
+                    const float g = u[j] + now[j];
+                    z[j] = g * (h[j] - x[j]) * (f * r);
+                    x[j] = r * g;
+                    now[j] = f * g;
+                } else {
+                    now[j] = fmaf(f, now[j], r * u[j]);
+                    x[j] = now[j];
+                }
+            }
+            if (!BACK || a.out) store8(static_cast<T*>(a.out) + t * a.ldo + c, valid, x);
+            if (BACK && a.out2) store8(static_cast<T*>(a.out2) + t * a.ldo2 + c, valid, z);
         }
         if (a.final) store8(a.final + b * a.ldf + c, valid, now);
     }
@@ -788,8 +813,8 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
         while (across > 1 && across / 2 * kRow >= a.s.d) across /= 2;
         const int64_t spans = cdiv(a.s.d, int64_t(across) * kRow), tasks = spans * cdiv(a.s.batch, 256 / across);
         return with_type(type, [&](auto t) {
-            const auto kernel = a.s.length <= 4 ? k_short<decltype(t), BACK, 1> : k_short<decltype(t), BACK, 4>;
-            kernel<<<dim3(unsigned(std::min(tasks, kMostBlocks))), 256, 0, stream>>>(a, across, spans, tasks);
+            k_short<decltype(t), BACK>
+                <<<dim3(unsigned(std::min(tasks, kMostBlocks))), 256, 0, stream>>>(a, across, spans, tasks);
             return launched();
         });
     }
@@ -804,12 +829,22 @@ int run(int64_t type, Args a, char* ws, const Space& sp, hipStream_t stream) {
         typedef decltype(t) T;
         constexpr int C = decltype(columns)::value;
         constexpr bool EVEN = decltype(even)::value;
-        if (a.p.split)
-            k_parts<T, C, BACK, EVEN>
-                <<<dgc::grid_of((a.p.count - 1) * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        // Strips that share lines go to the same die: 8 x 4096 x 1001 backward 101 us, to one
+        // after the other 161.  (Else in turn: 64 x 8192 x 512 forward 298 us, so 333.)
+        const auto lined = [](const void* p, int64_t ld) {
+            return !p || (reinterpret_cast<uintptr_t>(p) | uint64_t(ld) * sizeof(T)) % kLine == 0;
+        };
+        a.p.close = !(lined(a.gate, a.ldg) && lined(a.x, a.ldx) && lined(a.dh, a.lddh) && lined(a.h, a.ldh) &&
+                      lined(a.out, a.ldo) && lined(a.out2, a.ldo2));
+        const auto blocks = [&](int64_t parts) {
+            return dgc::grid_of(cdiv(parts * a.p.strips, kDies) * kDies, kThreads);
+        };
+        if (a.p.split) k_parts<T, C, BACK, EVEN><<<blocks(a.p.count - 1), kThreads, 0, stream>>>(a);
         const int64_t bytes = a.s.m * a.s.d * int64_t(sizeof(T)) * (BACK ? 4 : 2);
-        const auto kernel = bytes > kLarge ? k_along<T, C, BACK, EVEN, true> : k_along<T, C, BACK, EVEN, false>;
-        kernel<<<dgc::grid_of(a.p.count * a.p.strips, kThreads), kThreads, 0, stream>>>(a);
+        const auto kernel = bytes <= kLarge ? k_along<T, C, BACK, EVEN, kOut>
+                            : a.p.close     ? k_along<T, C, BACK, EVEN, kNone>
+                                            : k_along<T, C, BACK, EVEN, kBoth>;
+        kernel<<<blocks(a.p.count), kThreads, 0, stream>>>(a);
         return launched();
     };
     const auto wide = [&](auto t, auto columns) {
