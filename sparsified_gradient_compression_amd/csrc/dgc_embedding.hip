@@ -14,6 +14,12 @@
 //   k_sum                 units of sorted tokens: an id's sum over its tokens there.
 //                         An id whose tokens go over a unit's ends leaves partial sums
 //   k_join                adds the partial sums up
+// Memory bounds it where there are many tokens: 32768 of 50000 ids, 2048 columns,
+// bf16 into binary32, 544 MB (91 us at an addition's rate) in 128 us: count 5,
+// scatter and fill 28 and 36, sum 35, join 10.  Few are bound by launches and by
+// the sort's steps, each of which waits for the one before: 1531 of 10000 ids,
+// 1152 columns, fp16, in 18.7 us: sort 7.4, sum 6, join 5.  Merging sorted runs by
+// searches instead took 51 us for 32768.
 #include <algorithm>
 #include <type_traits>
 
@@ -44,6 +50,8 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int wide, int64_t i) {
     return wide ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
 }
 
+// Rows copied, scaled: 16384 x 4096 in bf16 40 to 51 us (5.3 TB/s and more: common ids
+// come from the caches), 3 x 2048 2.0 us, a launch's time.
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
     const int tx = threadIdx.x & (a.across - 1), ty = threadIdx.x / a.across, rows = kThreads / a.across;
@@ -78,9 +86,13 @@ constexpr int kSortWaves = kSorters / 64;
 constexpr int kEach = 1;                  // tokens of a thread in k_scatter
 constexpr int64_t kTile = kSorters * kEach;
 constexpr int kOneEach = 4;               // ... at most in k_sort_one
+// Tokens that one workgroup sorts, in a launch: 4096 of 50000 ids, 1024 columns 30 us, 4097 34.
 constexpr int64_t kOne = kSorters * kOneEach;
 constexpr int kMostBits = 9, kMostBins = 1 << kMostBits;  // of a digit
-constexpr int64_t kFewTiles = 128;        // whose counts each workgroup of k_scatter adds up by itself
+// Tiles whose counts each workgroup of k_scatter adds up by itself: a launch of k_scan
+// for 64 makes 52 us 59 (256 columns), for 128 74 us 77; none for 512 makes 121 us
+// (64 columns) 133.
+constexpr int64_t kFewTiles = 128;
 
 struct Sort {
     int64_t m, vocab, tiles;
@@ -642,6 +654,8 @@ int across_of(int64_t d, int columns, int least) {
 }
 
 // Sorted tokens of a unit: fewer, a multiple of kAhead, where there are few tokens.
+// 1152 columns of 10000 ids, by 8 and by 32: 1024 tokens 19 us and 24, 4096 25 and
+// 27, 8192 35 and 33, 16384 47 and 38.
 int unit_of(int64_t m) { return m <= kOne ? kAhead : kMostUnit; }
 
 struct Space {

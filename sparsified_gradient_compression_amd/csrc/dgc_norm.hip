@@ -1,5 +1,15 @@
 // dgc_norm.hip -- layer norm and its gradients.  See include/dgc.h for the
 // contract of every function.
+//
+// Memory bounds both directions: a row is read once, held in registers for its
+// mean, for the squares about that mean (the mean of the squares less the
+// mean's square would cancel) and for its output.  bf16, gain and bias in
+// binary32, us and rate of rows alone:
+//   16384 x 4096   forward 52 (5.1 TB/s; a copy of as many bytes 55)   backward with
+//                  the residual and both sums 104 (5.2)
+//   1 x 4096       forward 3.3, a launch's time
+//   777 x 1152     backward 6.8, and 3.7 for the join: launches and 3 rows of a wave
+// Loads or stores past the caches: 16384 x 4096 forward 64 to 66.
 #include <algorithm>
 #include <type_traits>
 
@@ -381,8 +391,8 @@ __global__ __launch_bounds__(THREADS) void k_norm_back(Backward a) {
     }
 }
 
-// Column sums of dy n and dy over a stripe of rows: 64 lanes of 8 columns by 4
-// rows at a time.
+// Column sums of dy n and dy over a stripe of rows, for rows that do not fit into
+// registers: 64 lanes of 8 columns by 4 rows at a time.
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_norm_columns(Backward a) {
     __shared__ float lds[3][64][2 * kRow + 1];
@@ -424,8 +434,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_columns(Backward a) {
     }
 }
 
-// The stripes' sums joined: a workgroup per 64 columns, a wave per 16th of the
-// stripes.
+// The stripes' sums joined, in binary64: a workgroup per 64 columns, a wave per 16th
+// of the stripes.  512 parts of 2 x 4096 columns 5.8 us (2.9 TB/s, from the caches).
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_join(Backward a) {
     __shared__ double lds[16][64];
@@ -493,7 +503,7 @@ int forward_shape(int64_t d, F f, G g) {
     return g();
 }
 
-// Backward, with the residual:
+// Backward, with the residual, bf16, microseconds by lanes x eights:
 //   16384 x 1152   64 x 3  40.9   128 x 2 49.9   256 x 1  61
 //   16384 x 4096   256 x 2 104    512 x 1 111    512 x 2  145
 //   8192 x 8192    512 x 2 104    256 x 4 109
