@@ -344,6 +344,9 @@ template <int C>
 __device__ __forceinline__ void state_of(const float* p, int64_t ld, int32_t sequence, const Columns& c, float* v) {
     if (p) {
         get_wide<C>(p, int64_t(sequence) * ld, c, v);
+        // (waited for here, where there is a state, not where the two ways meet)
+#pragma unroll
+        for (int i = 0; i < C; ++i) asm volatile("" : "+v"(v[i]));
     } else {
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = 0.0f;
