@@ -19,9 +19,9 @@
 //
 // What bounds it is memory, where there are enough rows and columns to fill the
 // card: forward moves 3 numbers for each element, backward 6.  bf16, microseconds:
-//   forward   8 x 4096 x 4096 154 (5.2 TB/s)   64 x 8192 x 512 298 (5.4)
-//   backward  4 x 8192 x 4096 329 (4.9)        8 x 4096 x 4096 332
-//   with a first pass  1 x 32768 x 4096 forward 228, backward 398
+//   forward   8 x 4096 x 4096 150 (5.4 TB/s)   64 x 8192 x 512 298 (5.4)
+//   backward  4 x 8192 x 4096 327 (4.9)        4096 x 64 x 1280 809 (5.0)
+//   with a first pass  1 x 32768 x 4096 forward 223, backward 398
 //   9734 x 1152 in sequences of many lengths   forward 33 (2.0 of 67 MB)
 // A barrier for each chunk, every wave folding all waves' sums: 181 for 154.
 #include <algorithm>
@@ -40,9 +40,10 @@ constexpr int kThreads = kLanes * kWaves;
 constexpr int kRows = 8;                       // of a wave at a time
 constexpr int64_t kChunk = kWaves * kRows;     // rows of a workgroup at a time
 // Rows of a sequence that k_short goes along.  bf16, us forward and backward, by
-// k_short and by k_along: 64 x 4 x 1280 4.2 6.2 and 6.9 9.0, 64 x 8 x 1280 6.5 10.1
-// and 7.1 9.0, 4096 x 8 x 1280 40 103 and 51 145, 64 x 16 x 1280 11.0 18.2 and 7.2 9.2.
-constexpr int64_t kShort = 8;
+// k_short and by k_along: 64 x 4 x 1280 4.2 6.1 and 6.5 8.4, 64 x 6 5.3 8.1 and 6.5
+// 8.3, 64 x 8 6.4 10.1 and 6.6 8.5, 512 x 6 7.3 13.7 and 7.4 22.2, 512 x 8 10.7 17.8
+// and 10.1 15.7, 4096 x 6 31 77 and 32 95, 4096 x 8 40 102 and 41 106.
+constexpr int64_t kShort = 6;
 constexpr int64_t kFill = 256;                 // workgroups that fill the card
 constexpr int64_t kLarge = 256ll << 20;        // bytes: what the last cache holds
 constexpr int64_t kMostBlocks = 1 << 20;       // of a launch: workgroups take what is left in turn
@@ -344,7 +345,8 @@ template <int C>
 __device__ __forceinline__ void state_of(const float* p, int64_t ld, int32_t sequence, const Columns& c, float* v) {
     if (p) {
         get_wide<C>(p, int64_t(sequence) * ld, c, v);
-        // (waited for here, where there is a state, not where the two ways meet)
+        // (waited for here, where there is a state, not where the two ways meet: without
+        // states 4096 x 64 x 1280 backward takes 1006 us then, so 809)
 #pragma unroll
         for (int i = 0; i < C; ++i) asm volatile("" : "+v"(v[i]));
     } else {

@@ -36,7 +36,8 @@ def test_recurrences_beyond_the_caches(lengths, ragged, d):
 
 
 @pytest.mark.parametrize("batch,length,d", [(200, 24, 136), (64, 128, 520), (500, 9, 129), (40, 136, 1001), (1000, 16, 72),
-                                            (3, 8, 1001), (70, 8, 65)])
+                                            (3, 8, 1001), (70, 8, 65),
+                                            (30, 6, 200), (30, 7, 200)])
 def test_many_sequences_of_equal_length(batch, length, d):
     for i, dtype in enumerate((BF16, FP16, FP32)):
         say(f"even {batch} x {length} x {d} {dtype}")
