@@ -487,6 +487,8 @@ using Int = std::integral_constant<int, V>;
 //   16384 x 1152   64 x 3  14.6   64 x 4  21.3   256 x 1  26.4
 //   16384 x 2048   64 x 4  27.9   256 x 1 27.6
 //   16384 x 4096   256 x 2 51.0   512 x 1 52.6   64 x 8   96
+//   16384 x 4104   256 x 3 48     512 x 2 58     256 x 4  73   (5120: 64, 67, 73)
+//   8192 x 8200    512 x 3 48     512 x 4 74
 template <class F, class G>
 int forward_shape(int64_t d, F f, G g) {
     if (d < kRow) return g();
@@ -498,7 +500,9 @@ int forward_shape(int64_t d, F f, G g) {
     if (d <= 1536) return f(Int<64>(), Int<3>(), Int<256>());
     if (d <= 2048) return f(Int<256>(), Int<1>(), Int<256>());
     if (d <= 4096) return f(Int<256>(), Int<2>(), Int<256>());
+    if (d <= 6144) return f(Int<256>(), Int<3>(), Int<256>());
     if (d <= 8192) return f(Int<256>(), Int<4>(), Int<256>());
+    if (d <= 12288) return f(Int<512>(), Int<3>(), Int<512>());
     if (d <= 16384) return f(Int<512>(), Int<4>(), Int<512>());
     return g();
 }
@@ -507,7 +511,14 @@ int forward_shape(int64_t d, F f, G g) {
 //   16384 x 1152   64 x 3  40.9   128 x 2 49.9   256 x 1  61
 //   16384 x 4096   256 x 2 104    512 x 1 111    512 x 2  145
 //   8192 x 8192    512 x 2 104    256 x 4 109
-//   4096 x 16384   512 x 4 196    256 x 8 302 (its sums leave the registers)
+// and without it:
+//   16384 x 4104   256 x 3 85     512 x 2 101
+//   16384 x 5120   256 x 3 100    512 x 2 106
+//   16384 x 6144   256 x 3 124    512 x 2 114
+//   8192 x 8200    512 x 3 86     512 x 4 219    1024 x 2 209
+//   8192 x 12288   512 x 3 123    512 x 4 245    1024 x 2 227
+// The longest, with it (their sums leave the registers of all of these):
+//   4096 x 16384   512 x 4 196    256 x 8 302
 template <class F, class G>
 int backward_shape(int64_t d, F f, G g) {
     if (d < kRow) return g();
@@ -519,7 +530,9 @@ int backward_shape(int64_t d, F f, G g) {
     if (d <= 1536) return f(Int<64>(), Int<3>(), Int<256>());
     if (d <= 2048) return f(Int<256>(), Int<1>(), Int<256>());
     if (d <= 4096) return f(Int<256>(), Int<2>(), Int<256>());
+    if (d <= 5120) return f(Int<256>(), Int<3>(), Int<256>());
     if (d <= 8192) return f(Int<512>(), Int<2>(), Int<512>());
+    if (d <= 12288) return f(Int<512>(), Int<3>(), Int<512>());
     if (d <= 16384) return f(Int<512>(), Int<4>(), Int<512>());
     return g();
 }

@@ -42,24 +42,22 @@ struct Eight {
     T t[kRow];
 };
 
-// ONCE: past the caches, for what is not read again soon.
-template <bool ONCE = false, class T>
+template <class T>
 __device__ __forceinline__ Eight<T> read8(const T* p) {
     typedef typename At<sizeof(T)>::V V;
     Eight<T> e;
 #pragma unroll
     for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
-        const V* q = reinterpret_cast<const V*>(p) + i;
-        const u32x4 w = ONCE ? __builtin_nontemporal_load(q) : *q;
+        const u32x4 w = reinterpret_cast<const V*>(p)[i];
         __builtin_memcpy(e.t + i * (16 / sizeof(T)), &w, 16);
     }
     return e;
 }
 
 // The first `valid` of 8; the others are 0.
-template <bool ONCE = false, class T>
+template <class T>
 __device__ __forceinline__ Eight<T> read8(const T* p, int valid) {
-    if (valid >= kRow) return read8<ONCE>(p);
+    if (valid >= kRow) return read8(p);
     Eight<T> e;
 #pragma unroll
     for (int i = 0; i < kRow; ++i) e.t[i] = i < valid ? p[i] : T(0.0f);
@@ -72,13 +70,13 @@ __device__ __forceinline__ void widen(const Eight<T>& e, float* v) {
     for (int i = 0; i < kRow; ++i) v[i] = float(e.t[i]);
 }
 
-template <bool ONCE = false, class T>
+template <class T>
 __device__ __forceinline__ void load8(const T* p, int valid, float* v) {
-    widen(read8<ONCE>(p, valid), v);
+    widen(read8(p, valid), v);
 }
 
 // Rounds to nearest, ties to even: the one rounding of an output.
-template <bool ONCE = false, class T>
+template <class T>
 __device__ __forceinline__ void store8(T* p, int valid, const float* v) {
     typedef typename At<sizeof(T)>::V V;
     if (valid >= kRow) {
@@ -89,11 +87,7 @@ __device__ __forceinline__ void store8(T* p, int valid, const float* v) {
         for (int i = 0; i < int(sizeof(T)) / 2; ++i) {
             u32x4 w;
             __builtin_memcpy(&w, e.t + i * (16 / sizeof(T)), 16);
-            V* q = reinterpret_cast<V*>(p) + i;
-            if constexpr (ONCE)
-                __builtin_nontemporal_store(w, q);
-            else
-                *q = w;
+            reinterpret_cast<V*>(p)[i] = w;
         }
     } else {
 #pragma unroll
@@ -110,14 +104,6 @@ __device__ __forceinline__ void load8_either(const void* p, int64_t at, int wide
         load8(static_cast<const float*>(p) + at, valid, v);
     else
         load8(static_cast<const T*>(p) + at, valid, v);
-}
-
-template <class T>
-__device__ __forceinline__ void store8_either(void* p, int64_t at, int wide, int valid, const float* v) {
-    if (wide)
-        store8(static_cast<float*>(p) + at, valid, v);
-    else
-        store8(static_cast<T*>(p) + at, valid, v);
 }
 
 __device__ __forceinline__ int valid_of(int64_t end, int64_t at) {
@@ -148,10 +134,10 @@ __device__ __forceinline__ void hide(const Span& w, V* v) {
 }
 
 // (p: the row's first element)
-template <bool ONCE = false, class T>
+template <class T>
 __device__ __forceinline__ void store_span(T* p, const Span& w, const float* v) {
     if (w.skip == 0) {
-        store8<ONCE>(p + w.at, kRow, v);
+        store8(p + w.at, kRow, v);
     } else {
 #pragma unroll
         for (int i = 0; i < kRow; ++i)
