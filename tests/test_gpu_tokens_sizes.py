@@ -1,11 +1,13 @@
 """Token operators where their kernels go another way: recurrences that the last
 cache does not hold, with rows that begin at cache lines and rows that do not;
 many sequences to a workgroup's chunk; more sequences than offsets are kept
-nearby; tables of more rows than tokens name, by few and by many tokens."""
+nearby; tables of more rows than tokens name, by few and by many tokens; norms of
+several long rows to a workgroup."""
 
 import pytest
 import torch
 
+import test_gpu_norm
 from gpu_harness import say
 from sparsified_gradient_compression_amd import dgc
 from test_gpu_embedding import run_backward
@@ -83,3 +85,12 @@ def test_rows_that_no_token_names(m, vocab, d):
                                                  (FP32, "one", I32, True, 1, 1)):
         say(f"embedding_backward {m} {vocab} {d} {dtype} {kind}")
         run_backward(m, vocab, d, dtype, kind, itype, 2.0, wide, False, pad, shift)
+
+
+@pytest.mark.parametrize("m,d", [(2100, 4099), (2100, 5120), (1100, 5121), (2100, 6144), (1100, 6145), (1100, 8193), (1100, 9001),
+                                 (1100, 12288), (1100, 12289), (1100, 16384)])
+def test_norms_of_many_long_rows(m, d):
+    for dtype, kind, wide, residual in ((BF16, "own", True, True), (FP16, "wide", False, False), (FP32, "own", True, True)):
+        say(f"layer_norm {m} {d} {dtype} {kind}")
+        test_gpu_norm.run_forward(m, d, dtype, kind)
+        test_gpu_norm.run_backward(m, d, dtype, kind, wide, residual)
